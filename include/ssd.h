@@ -270,6 +270,134 @@ int ssd_backward(const ssd_problem_t* p,
                  float* dD, float* dinit, float* ddt_bias,
                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------
+ * The operators around the scan in a Mamba layer.  The conventions at the top of
+ * this file hold for them too, with three differences: a tensor argument needs only
+ * the alignment of its element type; the inputs named with an `ld` field may be
+ * slices of wider rows (an `ld` is the distance in elements from one token to the
+ * next, over the whole batch, channels being contiguous); and every parameter,
+ * state and gradient is fp32 whatever the type of the activations.
+ * ------------------------------------------------------------------------------ */
+
+/* conv flags */
+enum {
+    SSD_CONV_SILU = 1u << 0    /* y = silu(pre) instead of pre */
+};
+
+typedef struct {
+    int64_t batch;      /* rows                                                     */
+    int64_t seqlen;     /* tokens per row (may be 0)                                */
+    int64_t channels;   /* D                                                        */
+    int64_t nseqs;      /* number of sequences: == batch without seq_idx            */
+    int64_t ldx;        /* elements from one token of x to the next (>= channels)   */
+    int32_t width;      /* K: taps, 2 to 4                                          */
+    int32_t dtype;      /* ssd_dtype_t of x and y                                   */
+    uint32_t flags;     /* SSD_CONV_*                                               */
+    int32_t reserved;   /* must be 0                                                */
+} ssd_conv_problem_t;
+
+/* The short causal convolution over each channel (the conv layer before the scan in
+ * the Mamba block; simplified block pseudocode of the "Mamba" paper story):
+ *     pre[t][d] = bias[d] + sum_{j=0}^{K-1} weight[d][K-1-j] in[t-j][d],
+ *     y = pre, or silu(pre) = pre / (1 + exp(-pre)).
+ * in[t-j] is the token j back in the same sequence; before the sequence's first token
+ * it is the matching row of its initial state (K-1 rows, oldest first), or zero.
+ *   x           (batch, seqlen, channels)      dtype, tokens ldx apart
+ *   weight      (channels, width)              fp32
+ *   bias        (channels)                     fp32, or NULL
+ *   init_state  (nseqs, width-1, channels)     fp32, or NULL for zeros
+ *   seq_idx     (batch, seqlen)                int32 or NULL, as in ssd_forward
+ *   y           (batch, seqlen, channels)      dtype, output
+ *   final_state (nseqs, width-1, channels)     fp32 output or NULL: each sequence's last
+ *               K-1 inputs, of a shorter sequence those of its initial state before them.
+ *               Rows of ids that do not occur are not written.
+ * Outputs must not overlap inputs or each other (SSD_ERR_ALIAS): the tokens of a row are
+ * spread over workgroups, so the state is not carried in place.  One kernel launch. */
+int ssd_conv_forward(const ssd_conv_problem_t* p, const void* x, const float* weight, const float* bias,
+                     const float* init_state, const int32_t* seq_idx, void* y, float* final_state, void* stream);
+
+/* Bytes of device workspace ssd_conv_backward needs (0 for an invalid problem): partial
+ * sums of the weight and bias gradients. */
+size_t ssd_conv_backward_workspace_size(const ssd_conv_problem_t* p);
+
+/* Gradients of L for dL/dy = dy (fp32) and dL/dfinal_state = dfinal (fp32, or NULL), all
+ * fp32 and dense: dx (batch, seqlen, channels), dweight (channels, width), dbias
+ * (channels) or NULL, dinit (nseqs, width-1, channels) or NULL (at a zero state when
+ * init_state is NULL; zero for ids that do not occur).  workspace: 256-byte aligned.
+ * The sums over tokens have a fixed order: results are deterministic. */
+int ssd_conv_backward(const ssd_conv_problem_t* p, const void* x, const float* weight, const float* bias,
+                      const float* init_state, const int32_t* seq_idx, const float* dy, const float* dfinal,
+                      float* dx, float* dweight, float* dbias, float* dinit, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* One token (decoding): ssd_conv_forward with seqlen 1 and nseqs == batch, from `state` to
+ * `state_out`, which may be the same buffer (in place) or one that does not overlap it. */
+int ssd_conv_step(const ssd_conv_problem_t* p, const void* x, const float* weight, const float* bias,
+                  const float* state, float* state_out, void* y, void* stream);
+
+/* norm flags */
+enum {
+    SSD_NORM_GATE_FIRST = 1u << 0    /* gate before the norm (else after it) */
+};
+
+typedef struct {
+    int64_t rows;
+    int64_t channels;     /* D                                                              */
+    int64_t group_size;   /* consecutive channels normed together; divides channels; <= 32768 */
+    int64_t ldx;          /* elements from one row of x to the next (>= channels)           */
+    int64_t ldz;          /* the same of z, or of residual                                  */
+    float eps;            /* >= 0                                                           */
+    int32_t x_dtype;      /* ssd_dtype_t of x                                               */
+    int32_t dtype;        /* ssd_dtype_t of z and out                                       */
+    uint32_t flags;       /* SSD_NORM_*                                                     */
+    int32_t reserved;     /* must be 0                                                      */
+} ssd_norm_problem_t;
+
+/* The root-mean-square norm after the scan with its gate, per row and group of channels
+ * (the gate beside the scan in the Mamba block's simplified pseudocode, "Mamba" paper
+ * story; the norm after it, which the pages do not detail, read as
+ * v / sqrt(mean(v^2) + eps)):
+ *     gate first: u = x silu(z), out = u / sqrt(mean(u^2) + eps) weight
+ *     gate after: out = x / sqrt(mean(x^2) + eps) weight silu(z)
+ *   x      (rows, channels)   x_dtype: fp32 (the scan's y) or dtype; rows ldx apart
+ *   z      (rows, channels)   dtype; rows ldz apart
+ *   weight (channels)         fp32
+ *   out    (rows, channels)   dtype, output; overlaps no input (SSD_ERR_ALIAS) */
+int ssd_gated_norm_forward(const ssd_norm_problem_t* p, const void* x, const void* z, const float* weight, void* out,
+                           void* stream);
+
+/* Gradients for dL/dout = dout (fp32): dx, dz (rows, channels) and dweight (channels), fp32
+ * and dense.  workspace: 256-byte aligned, of the size given (0 for an invalid problem). */
+size_t ssd_gated_norm_backward_workspace_size(const ssd_norm_problem_t* p);
+int ssd_gated_norm_backward(const ssd_norm_problem_t* p, const void* x, const void* z, const float* weight,
+                            const float* dout, float* dx, float* dz, float* dweight, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* The norm before a block with its residual addition:
+ *     residual_out = residual + scale x,  out = residual_out / sqrt(mean(residual_out^2) + eps) weight
+ * over whole rows (group_size == channels, x_dtype == dtype, flags 0).
+ *   x            (rows, channels)   dtype, rows ldx apart: the previous block's output
+ *   residual     (rows, channels)   fp32, rows ldz apart, or NULL (the stream starts here)
+ *   weight       (channels)         fp32
+ *   scale        (channels)         fp32, or NULL for 1
+ *   out          (rows, channels)   dtype, output
+ *   residual_out (rows, channels)   fp32, output; may be `residual` itself when that is
+ *                dense (in place).  Any other overlap is SSD_ERR_ALIAS. */
+int ssd_residual_norm_forward(const ssd_norm_problem_t* p, const void* x, const float* residual, const float* weight,
+                              const float* scale, void* out, float* residual_out, void* stream);
+
+/* Gradients for dL/dout = dout and dL/dresidual_out = dresidual_out (NULL: nothing else
+ * uses the stream), from the residual_out that the forward wrote.  dresidual (rows,
+ * channels) is also the gradient of x when scale is NULL; with a scale, dx = scale
+ * dresidual and dscale (channels) are written and x is read (without one, x, dx and
+ * dscale may be NULL).  dweight (channels).  All fp32 and dense.  `scaled`: whether a
+ * scale will be given. */
+size_t ssd_residual_norm_backward_workspace_size(const ssd_norm_problem_t* p, int scaled);
+int ssd_residual_norm_backward(const ssd_norm_problem_t* p, const void* x, const float* residual_out,
+                               const float* weight, const float* scale, const float* dout, const float* dresidual_out,
+                               float* dx, float* dresidual, float* dweight, float* dscale, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* Static description of an error code. */
 const char* ssd_strerror(int status);
 

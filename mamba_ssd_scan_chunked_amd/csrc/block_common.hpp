@@ -1,0 +1,87 @@
+// Device and host helpers shared by the operators around the scan: the causal
+// convolution, the selective scan and the norms.  Internal to the library.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ssd {
+
+// V consecutive elements.  Loads and stores go through memcpy at the element's own
+// alignment: gfx950 reads and writes 16 bytes at any address that is a multiple of
+// the element size in one instruction, so rows of odd length and slices of wider
+// rows take the same path as aligned ones.
+template <typename T, int V> struct Pack {
+    T v[V];
+};
+template <int V, typename T> __device__ inline Pack<T, V> load_pack(const T* p) {
+    Pack<T, V> r;
+    __builtin_memcpy(&r, p, sizeof(r));
+    return r;
+}
+template <int V, typename T> __device__ inline void store_pack(T* p, const Pack<T, V>& r) {
+    __builtin_memcpy(p, &r, sizeof(r));
+}
+template <int V, typename T> __device__ inline void load_f32(const T* p, float* out) {
+    const Pack<T, V> r = load_pack<V>(p);
+#pragma unroll
+    for (int i = 0; i < V; ++i) out[i] = (float)r.v[i];
+}
+// One rounding to nearest even when T is bf16 (the operator's only one).
+template <int V, typename T> __device__ inline void store_f32(T* p, const float* in) {
+    Pack<T, V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.v[i] = (T)in[i];
+    store_pack<V>(p, r);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// e^v from the hardware exp2.  The product v log2(e) is split into its rounded value
+// and its remainder, so the error does not grow with |v| (about 1e-7 relative).
+__device__ inline float exp_accurate(float v) {
+    const float hi = v * kLog2e;
+    // an infinite or huge product has no remainder (inf - inf)
+    const float lo = fabsf(hi) < 1e30f ? fmaf(v, 1.925963033500012e-08f, fmaf(v, kLog2e, -hi)) : 0.f;
+    return __builtin_amdgcn_exp2f(hi) * fmaf(lo, kLn2, 1.f);
+}
+
+// 1 / (1 + e^-v).  e^-v overflows to inf below v = -88, which gives 0 as it should.
+__device__ inline float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + exp_accurate(-v)); }
+__device__ inline float silu(float v) { return v * sigmoid(v); }
+// The gate of a result that is rounded to T: bf16 takes the plain exp2, whose argument's
+// rounding (2^-24 |v| log2 e) is far below bf16's half step and saves six instructions.
+template <typename T> __device__ inline float silu_for(float v) { return silu(v); }
+template <> __device__ inline float silu_for<__bf16>(float v) {
+    return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -kLog2e));
+}
+// d silu / dv = s (1 + v (1 - s)), s = sigmoid(v)
+__device__ inline float silu_slope(float v, float s) { return s * (1.f + v * (1.f - s)); }
+
+// log(1 + e^v) = max(v, 0) + log1p(t), t = e^-|v|, with Goldberg's correction for the
+// rounding of 1 + t ("What every computer scientist should know about floating-point
+// arithmetic", 1991, theorem 4).
+__device__ inline float softplus(float v) {
+    const float t = exp_accurate(-fabsf(v));
+    const float u = 1.f + t;
+    const float l = u == 1.f ? t : __builtin_amdgcn_logf(u) * kLn2 * (t * __builtin_amdgcn_rcpf(u - 1.f));
+    return fmaxf(v, 0.f) + l;
+}
+
+// Sequence id of a token, clamped so that a bad id cannot leave the per-sequence arrays.
+__device__ inline int64_t clamp_id(int32_t id, int64_t nseqs) {
+    return id < 0 ? 0 : (id >= nseqs ? nseqs - 1 : id);
+}
+
+// Column sums of part (rows x cols), rows in a fixed order: columns below `split` go
+// to out, the rest to out2 (either may be null: not wanted).
+struct ColumnSums {
+    const float* part;
+    float *out, *out2;
+    int64_t rows, cols, split;
+};
+hipError_t launch_column_sums(const ColumnSums& c, hipStream_t s);
+hipError_t launch_fill(float* p, int64_t n, hipStream_t s);                          // zeros
+hipError_t launch_copy(float* dst, const float* src, int64_t n, hipStream_t s);      // src null: zeros
+
+}  // namespace ssd

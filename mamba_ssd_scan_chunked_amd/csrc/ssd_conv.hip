@@ -1,0 +1,599 @@
+// The short causal convolution of a Mamba layer (depthwise, K = 2..4 taps): whole
+// sequences, their gradients, and the single-token step.  C entries of include/ssd.h.
+//
+//   pre[t][d] = bias[d] + sum_j w[d][K-1-j] in[t-j][d],   y = pre or silu(pre),
+//
+// in[t-j] being the token j back in the same sequence, or, before the sequence's first
+// token, the row of its initial state (K-1 rows, oldest first), or zero.
+//
+// Memory-bound: each thread owns V neighbouring channels and walks a run of tokens with
+// the last K-1 inputs in registers, so x is read once (plus K-1 rows per run, which the
+// neighbouring run has just brought into L2) and y written once.
+#include "ssd.h"
+
+#include <algorithm>
+#include <cstdio>
+
+#include "block_common.hpp"
+#include "ssd_host.hpp"
+
+namespace ssd {
+
+struct ConvParams {
+    const void* x;
+    const float *w, *bias, *init;
+    const int32_t* seq_idx;
+    void* y;
+    float* fin;
+    const float *dy, *dfin;
+    float *dx, *dinit, *part;
+    int64_t T, D, nseqs, ldx;
+    unsigned total, nvec, nrun, L;
+    int silu;
+};
+
+// Channels of the thread: V from c0.  The last vector of a row is moved back to end
+// with the row (D >= V), so it repeats channels of its neighbour with equal results
+// and no access needs a bound per element.
+struct Place {
+    int64_t c0, b, t0, t1;
+    unsigned run;
+};
+template <int V> __device__ inline Place place_of(const ConvParams& p, unsigned idx) {
+    Place q;
+    const unsigned cv = idx % p.nvec, rest = idx / p.nvec;
+    q.run = rest;
+    q.b = rest / p.nrun;
+    q.t0 = (int64_t)(rest % p.nrun) * p.L;
+    q.t1 = q.t0 + p.L < p.T ? q.t0 + p.L : p.T;
+    const int64_t c = (int64_t)cv * V;
+    q.c0 = c + V <= p.D ? c : p.D - V;
+    return q;
+}
+
+// Weights as w[k][v]; in memory the K taps of a channel lie together.
+template <int V, int K> __device__ inline void load_weights(const ConvParams& p, int64_t c0, float (&w)[K][V]) {
+    float flat[V * K];
+    load_f32<V * K>(p.w + c0 * K, flat);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int k = 0; k < K; ++k) w[k][v] = flat[v * K + k];
+}
+
+// win[i] = row i of the sequence's initial state (zero without one).
+template <int V, int K> __device__ inline void load_init(const ConvParams& p, int64_t seq, int64_t c0, float (&win)[K - 1][V]) {
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) {
+        if (p.init) {
+            load_f32<V>(p.init + (seq * (K - 1) + i) * p.D + c0, win[i]);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) win[i][v] = 0.f;
+        }
+    }
+}
+
+// The window before token t0: win[i] = input K-1-i tokens back.  Returns how many of
+// those K-1 tokens lie in t0's own sequence (its place in it, up to K-1).
+template <typename T, int V, int K, bool SEQ>
+__device__ inline int open_window(const ConvParams& p, const Place& q, const int32_t* ids, float (&win)[K - 1][V]) {
+    const T* x = (const T*)p.x + q.b * p.T * p.ldx + q.c0;
+    int m = 0;
+#pragma unroll
+    for (int lag = 1; lag < K; ++lag)
+        if (q.t0 - lag >= 0 && (!SEQ || ids[q.t0 - lag] == ids[q.t0])) m = lag;
+    const int64_t seq = SEQ ? clamp_id(ids[q.t0], p.nseqs) : q.b;
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) {
+        const int lag = K - 1 - i;
+        if (lag <= m) {
+            load_f32<V>(x + (q.t0 - lag) * p.ldx, win[i]);
+        } else if (p.init) {
+            load_f32<V>(p.init + (seq * (K - 1) + K - 1 + m - lag) * p.D + q.c0, win[i]);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) win[i][v] = 0.f;
+        }
+    }
+    return m;
+}
+
+template <int V, int K> __device__ inline void push(float (&win)[K - 1][V], const float (&in)[V]) {
+#pragma unroll
+    for (int i = 0; i + 1 < K - 1; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) win[i][v] = win[i + 1][v];
+#pragma unroll
+    for (int v = 0; v < V; ++v) win[K - 2][v] = in[v];
+}
+
+constexpr int kAhead = 4;      // tokens whose loads are issued together
+
+template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(256) void conv_forward_kernel(ConvParams p) {
+    const unsigned idx = blockIdx.x * 256u + threadIdx.x;
+    if (idx >= p.total) return;
+    const Place q = place_of<V>(p, idx);
+    const int32_t* ids = SEQ ? p.seq_idx + q.b * p.T : nullptr;
+    float w[K][V], bias[V], win[K - 1][V];
+    load_weights<V, K>(p, q.c0, w);
+    if (p.bias) {
+        load_f32<V>(p.bias + q.c0, bias);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) bias[v] = 0.f;
+    }
+    open_window<T, V, K, SEQ>(p, q, ids, win);
+    const T* x = (const T*)p.x + q.b * p.T * p.ldx + q.c0;
+    T* y = (T*)p.y + q.b * p.T * p.D + q.c0;
+    for (int64_t t = q.t0; t < q.t1; t += kAhead) {
+        Pack<T, V> raw[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (t + u < q.t1) raw[u] = load_pack<V>(x + (t + u) * p.ldx);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (t + u >= q.t1) break;
+            const int64_t tt = t + u;
+            if (SEQ && tt > q.t0 && ids[tt] != ids[tt - 1]) load_init<V, K>(p, clamp_id(ids[tt], p.nseqs), q.c0, win);
+            float in[V], out[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                in[v] = (float)raw[u].v[v];
+                float acc = fmaf(w[K - 1][v], in[v], bias[v]);
+#pragma unroll
+                for (int i = 0; i < K - 1; ++i) acc = fmaf(w[i][v], win[i][v], acc);
+                out[v] = acc;
+            }
+            if (p.silu) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) out[v] = silu_for<T>(out[v]);
+            }
+            store_f32<V>(y + tt * p.D, out);
+            push<V, K>(win, in);
+            if (p.fin && (tt == p.T - 1 || (SEQ && ids[tt + 1] != ids[tt]))) {
+                const int64_t seq = SEQ ? clamp_id(ids[tt], p.nseqs) : q.b;
+#pragma unroll
+                for (int i = 0; i < K - 1; ++i) store_f32<V>(p.fin + (seq * (K - 1) + i) * p.D + q.c0, win[i]);
+            }
+        }
+    }
+}
+
+// Gradients.  With g[t] = dy[t] silu'(pre[t]), input row r receives
+// sum_j w[K-1-j] g[r+j] over the tokens r+j of its own sequence, and, being one of the
+// sequence's last K-1 inputs, its row of dfinal.  A thread walks its run once, keeping
+// the K partial sums of the rows t-K+1 .. t (acc[j]: row t-j); after token t row t-K+1
+// is complete.  It reads K-1 tokens past its run to complete its last rows, and leaves
+// the rows before its run to the run before.  Rows before a sequence's first token are
+// those of its initial state and go to dinit.  dw and dbias are summed per run into
+// `part` (K+1 arrays of runs x D), then over runs in a fixed order.
+template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(256) void conv_backward_kernel(ConvParams p) {
+    const unsigned idx = blockIdx.x * 256u + threadIdx.x;
+    if (idx >= p.total) return;
+    const Place q = place_of<V>(p, idx);
+    const int32_t* ids = SEQ ? p.seq_idx + q.b * p.T : nullptr;
+    float w[K][V], bias[V], win[K - 1][V], acc[K][V], dw[K][V], db[V];
+    load_weights<V, K>(p, q.c0, w);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        db[v] = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) acc[k][v] = dw[k][v] = 0.f;
+    }
+    if (p.bias) {
+        load_f32<V>(p.bias + q.c0, bias);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) bias[v] = 0.f;
+    }
+    int place = open_window<T, V, K, SEQ>(p, q, ids, win);       // of the token at hand in its sequence, up to K-1
+    int64_t seq = SEQ ? clamp_id(ids[q.t0], p.nseqs) : q.b;
+    const T* x = (const T*)p.x + q.b * p.T * p.ldx + q.c0;
+    const float* dy = p.dy + q.b * p.T * p.D + q.c0;
+    float* dx = p.dx + q.b * p.T * p.D + q.c0;
+    const int64_t end = q.t1 + K - 1 < p.T ? q.t1 + K - 1 : p.T;
+
+    // the finished sum of the row j back from token tt
+    auto emit = [&](int64_t tt, int j, const float (&val)[V]) {
+        const int64_t row = tt - j;
+        if (place >= j) {
+            if (row >= q.t0 && row < q.t1) store_f32<V>(dx + row * p.D, val);
+        } else if (p.dinit && tt - place >= q.t0 && tt - place < q.t1) {
+            store_f32<V>(p.dinit + (seq * (K - 1) + K - 1 + place - j) * p.D + q.c0, val);
+        }
+    };
+
+    bool open = true;                     // the run's last sequence goes on past the run
+    for (int64_t t = q.t0; t < end && open; t += kAhead) {
+        Pack<T, V> raw[kAhead];
+        Pack<float, V> dyr[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (t + u < end) {
+                raw[u] = load_pack<V>(x + (t + u) * p.ldx);
+                dyr[u] = load_pack<V>(dy + (t + u) * p.D);
+            }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t tt = t + u;
+            if (tt >= end || !open) break;
+            if (SEQ && tt > q.t0 && ids[tt] != ids[tt - 1]) {
+                seq = clamp_id(ids[tt], p.nseqs);
+                place = 0;
+                load_init<V, K>(p, seq, q.c0, win);
+            }
+            const bool mine = tt < q.t1;
+            float in[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                in[v] = (float)raw[u].v[v];
+                float g = dyr[u].v[v];
+                if (p.silu) {
+                    float pre = fmaf(w[K - 1][v], in[v], bias[v]);
+#pragma unroll
+                    for (int i = 0; i < K - 1; ++i) pre = fmaf(w[i][v], win[i][v], pre);
+                    g *= silu_slope(pre, sigmoid(pre));
+                }
+                acc[0][v] = w[K - 1][v] * g;
+#pragma unroll
+                for (int j = 1; j < K; ++j) acc[j][v] = fmaf(w[K - 1 - j][v], g, acc[j][v]);
+                if (mine) {
+                    db[v] += g;
+                    dw[K - 1][v] = fmaf(g, in[v], dw[K - 1][v]);
+#pragma unroll
+                    for (int i = 0; i < K - 1; ++i) dw[i][v] = fmaf(g, win[i][v], dw[i][v]);
+                }
+            }
+            emit(tt, K - 1, acc[K - 1]);
+            const bool last = tt == p.T - 1 || (SEQ && ids[tt + 1] != ids[tt]);
+            if (last) {
+#pragma unroll
+                for (int j = K - 2; j >= 0; --j) {
+                    if (p.dfin) {
+                        float df[V];
+                        load_f32<V>(p.dfin + (seq * (K - 1) + K - 2 - j) * p.D + q.c0, df);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) acc[j][v] += df[v];
+                    }
+                    emit(tt, j, acc[j]);
+                }
+                // the next sequence's rows start from zero; past the run nothing is left to complete
+                open = tt + 1 < q.t1;
+#pragma unroll
+                for (int j = 0; j < K; ++j)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) acc[j][v] = 0.f;
+            } else {
+#pragma unroll
+                for (int j = K - 1; j > 0; --j)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) acc[j][v] = acc[j - 1][v];
+            }
+            push<V, K>(win, in);
+            if (place < K - 1) ++place;
+        }
+    }
+    float* part = p.part + (int64_t)q.run * p.D * (K + 1);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int k = 0; k < K; ++k) part[(q.c0 + v) * K + k] = dw[k][v];
+    store_f32<V>(part + p.D * K + q.c0, db);
+}
+
+// One token: a thread per (row, channel); state_out may be state (each element is read
+// and then written by one thread).  A few microseconds of launch and latency at any
+// batch that decoding meets.
+template <typename T, int K> __global__ __launch_bounds__(256) void conv_step_kernel(ConvParams p, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const int64_t b = i / p.D, d = i % p.D;
+    const float* st = p.init + b * (K - 1) * p.D + d;
+    float* out = p.fin + b * (K - 1) * p.D + d;
+    const float in = (float)((const T*)p.x)[b * p.ldx + d];
+    float win[K - 1];
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) win[k] = st[k * p.D];
+    float acc = fmaf(p.w[d * K + K - 1], in, p.bias ? p.bias[d] : 0.f);
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) acc = fmaf(p.w[d * K + k], win[k], acc);
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) out[k * p.D] = k + 1 < K - 1 ? win[k + 1] : in;
+    ((T*)p.y)[i] = (T)(p.silu ? silu_for<T>(acc) : acc);
+}
+
+template <typename T, int V, int K, bool BACK> static void launch_conv(const ConvParams& p, hipStream_t s) {
+    const dim3 grid((p.total + 255) / 256), block(256);
+    if constexpr (BACK) {
+        if (p.seq_idx) hipLaunchKernelGGL((conv_backward_kernel<T, V, K, true>), grid, block, 0, s, p);
+        else hipLaunchKernelGGL((conv_backward_kernel<T, V, K, false>), grid, block, 0, s, p);
+    } else {
+        if (p.seq_idx) hipLaunchKernelGGL((conv_forward_kernel<T, V, K, true>), grid, block, 0, s, p);
+        else hipLaunchKernelGGL((conv_forward_kernel<T, V, K, false>), grid, block, 0, s, p);
+    }
+}
+template <typename T, int V, bool BACK> static hipError_t launch_conv_k(int K, const ConvParams& p, hipStream_t s) {
+    if (K == 2) launch_conv<T, V, 2, BACK>(p, s);
+    else if (K == 3) launch_conv<T, V, 3, BACK>(p, s);
+    else launch_conv<T, V, 4, BACK>(p, s);
+    return hipGetLastError();
+}
+template <typename T> static hipError_t launch_step(int K, const ConvParams& p, int64_t n, hipStream_t s) {
+    const dim3 grid((unsigned)((n + 255) / 256)), block(256);
+    if (K == 2) hipLaunchKernelGGL((conv_step_kernel<T, 2>), grid, block, 0, s, p, n);
+    else if (K == 3) hipLaunchKernelGGL((conv_step_kernel<T, 3>), grid, block, 0, s, p, n);
+    else hipLaunchKernelGGL((conv_step_kernel<T, 4>), grid, block, 0, s, p, n);
+    return hipGetLastError();
+}
+
+}  // namespace ssd
+
+namespace {
+
+using namespace ssd_host;
+
+constexpr int64_t kMaxDim = int64_t(1) << 31;
+
+// Channels per thread and tokens per run.
+struct Shape {
+    int V;
+    int64_t nvec, L, nrun, total;
+};
+Shape shape_of(const ssd_conv_problem_t* p, bool backward) {
+    Shape s;
+    // 16 bytes of x per thread forward; four channels backward, which keeps K sums, K
+    // weights, K weight gradients and the window of each in registers
+    s.V = backward ? 4 : (p->dtype == SSD_DTYPE_BF16 ? 8 : 4);
+    if (p->channels < s.V) s.V = 1;
+    s.nvec = (p->channels + s.V - 1) / s.V;
+    // Runs as long as the chip stays full (about 1 << 18 threads): a run re-reads K-1
+    // rows, so longer runs read less.
+    const int64_t want = int64_t(1) << 18;
+    const int64_t longest = backward ? 64 : 32;
+    const int64_t rows = std::max<int64_t>(1, p->batch * s.nvec);
+    const int64_t runs = std::max<int64_t>(1, want / rows);
+    s.L = std::min(longest, std::max<int64_t>(4, (p->seqlen + runs - 1) / runs));
+    s.nrun = std::max<int64_t>(1, (p->seqlen + s.L - 1) / s.L);
+    s.total = s.nvec * s.nrun * p->batch;
+    return s;
+}
+
+int validate(const ssd_conv_problem_t* p) {
+    if (!p) return SSD_ERR_NULL_POINTER;
+    if (p->batch < 0 || p->seqlen < 0 || p->channels <= 0 || p->nseqs < 0 || p->ldx < p->channels)
+        return SSD_ERR_BAD_SHAPE;
+    if (p->batch >= kMaxDim || p->seqlen >= kMaxDim || p->channels >= kMaxDim || p->nseqs >= kMaxDim ||
+        p->ldx >= kMaxDim)
+        return SSD_ERR_BAD_SHAPE;
+    if (p->dtype != SSD_DTYPE_BF16 && p->dtype != SSD_DTYPE_F32) return SSD_ERR_UNSUPPORTED;
+    if (p->width < 2 || p->width > 4 || (p->flags & ~uint32_t(SSD_CONV_SILU)) || p->reserved != 0)
+        return SSD_ERR_UNSUPPORTED;
+    const double elems = double(p->batch) * double(p->seqlen) * double(p->ldx);
+    if (elems > 4e17 || double(p->nseqs) * p->channels * 3 > 4e17) return SSD_ERR_BAD_SHAPE;
+    // threads are numbered in 32 bits
+    if (double(shape_of(p, false).nvec) * shape_of(p, false).nrun * p->batch >= 4e9 ||
+        double(shape_of(p, true).nvec) * shape_of(p, true).nrun * p->batch >= 4e9)
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+struct ConvSizes {
+    int64_t x, y, f, w, state, seq, bias;
+};
+ConvSizes conv_sizes(const ssd_conv_problem_t* p) {
+    ConvSizes s;
+    const int64_t bt = p->batch * p->seqlen, e = elem_size(p->dtype);
+    s.x = bt > 0 ? ((bt - 1) * p->ldx + p->channels) * e : 0;
+    s.y = bt * p->channels * e;
+    s.f = bt * p->channels * 4;
+    s.w = p->channels * p->width * 4;
+    s.bias = p->channels * 4;
+    s.state = p->nseqs * (p->width - 1) * p->channels * 4;
+    s.seq = bt * 4;
+    return s;
+}
+
+struct Buf {
+    const void* ptr;
+    int64_t bytes;
+};
+// every output against every input and the outputs after it
+int check_alias(const Buf* in, int nin, const Buf* out, int nout) {
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j)
+            if (overlap(out[i].ptr, out[i].bytes, in[j].ptr, in[j].bytes)) return SSD_ERR_ALIAS;
+        for (int j = i + 1; j < nout; ++j)
+            if (overlap(out[i].ptr, out[i].bytes, out[j].ptr, out[j].bytes)) return SSD_ERR_ALIAS;
+    }
+    return SSD_OK;
+}
+
+int check_sequences(const ssd_conv_problem_t* p, const int32_t* seq_idx) {
+    if (!seq_idx && p->nseqs != p->batch) return SSD_ERR_BAD_SHAPE;
+    if (seq_idx && p->batch * p->seqlen > 0 && p->nseqs < 1) return SSD_ERR_BAD_SHAPE;
+    return SSD_OK;
+}
+
+ssd::ConvParams params_of(const ssd_conv_problem_t* p, const Shape& s) {
+    ssd::ConvParams c{};
+    c.T = p->seqlen;
+    c.D = p->channels;
+    c.nseqs = p->nseqs;
+    c.ldx = p->ldx;
+    c.total = (unsigned)s.total;
+    c.nvec = (unsigned)s.nvec;
+    c.nrun = (unsigned)s.nrun;
+    c.L = (unsigned)s.L;
+    c.silu = (p->flags & SSD_CONV_SILU) ? 1 : 0;
+    return c;
+}
+
+int64_t backward_bytes(const ssd_conv_problem_t* p) {
+    const Shape s = shape_of(p, true);
+    return p->seqlen == 0 || p->batch == 0 ? 0 : align256(p->batch * s.nrun * p->channels * (p->width + 1) * 4);
+}
+
+int done(const char* what, const ssd_conv_problem_t* p, hipError_t e) {
+    if (log_enabled())
+        std::fprintf(stderr, "[ssd] conv %s dtype=%d batch=%lld T=%lld D=%lld K=%d -> %s\n", what, p->dtype,
+                     (long long)p->batch, (long long)p->seqlen, (long long)p->channels, p->width, hipGetErrorString(e));
+    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssd_conv_backward_workspace_size(const ssd_conv_problem_t* p) {
+    return validate(p) == SSD_OK ? (size_t)backward_bytes(p) : 0;
+}
+
+int ssd_conv_forward(const ssd_conv_problem_t* p, const void* x, const float* weight, const float* bias,
+                     const float* init_state, const int32_t* seq_idx, void* y, float* final_state, void* stream) {
+    const int v = validate(p);
+    if (v != SSD_OK) return v;
+    const bool empty = p->batch == 0 || p->seqlen == 0;
+    if (!weight || (!empty && (!x || !y))) return SSD_ERR_NULL_POINTER;
+    const int q = check_sequences(p, seq_idx);
+    if (q != SSD_OK) return q;
+    const uintptr_t e = (uintptr_t)elem_size(p->dtype);
+    if (misaligned(x, e) || misaligned(y, e) || misaligned(weight, 4) || misaligned(bias, 4) ||
+        misaligned(init_state, 4) || misaligned(seq_idx, 4) || misaligned(final_state, 4))
+        return SSD_ERR_ALIGNMENT;
+    const ConvSizes z = conv_sizes(p);
+    const Buf in[] = {{x, z.x}, {weight, z.w}, {bias, z.bias}, {init_state, z.state}, {seq_idx, z.seq}};
+    const Buf out[] = {{y, z.y}, {final_state, z.state}};
+    const int a = check_alias(in, 5, out, 2);
+    if (a != SSD_OK) return a;
+    const int d = check_device();
+    if (d != SSD_OK) return d;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (empty) {
+        // no token: each row's final state is its initial state
+        if (seq_idx || !final_state) return SSD_OK;
+        return done("forward", p, ssd::launch_copy(final_state, init_state, z.state / 4, st));
+    }
+    const Shape s = shape_of(p, false);
+    ssd::ConvParams c = params_of(p, s);
+    c.x = x;
+    c.w = weight;
+    c.bias = bias;
+    c.init = init_state;
+    c.seq_idx = seq_idx;
+    c.y = y;
+    c.fin = final_state;
+    hipError_t r;
+    if (p->dtype == SSD_DTYPE_BF16)
+        r = s.V == 8 ? ssd::launch_conv_k<__bf16, 8, false>(p->width, c, st)
+                     : ssd::launch_conv_k<__bf16, 1, false>(p->width, c, st);
+    else
+        r = s.V == 4 ? ssd::launch_conv_k<float, 4, false>(p->width, c, st)
+                     : ssd::launch_conv_k<float, 1, false>(p->width, c, st);
+    return done("forward", p, r);
+}
+
+int ssd_conv_backward(const ssd_conv_problem_t* p, const void* x, const float* weight, const float* bias,
+                      const float* init_state, const int32_t* seq_idx, const float* dy, const float* dfinal, float* dx,
+                      float* dweight, float* dbias, float* dinit, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+    const int v = validate(p);
+    if (v != SSD_OK) return v;
+    const bool empty = p->batch == 0 || p->seqlen == 0;
+    if (!weight || !dweight || (!empty && (!x || !dy || !dx))) return SSD_ERR_NULL_POINTER;
+    const int q = check_sequences(p, seq_idx);
+    if (q != SSD_OK) return q;
+    const int64_t wsb = backward_bytes(p);
+    if (wsb > 0 && !workspace) return SSD_ERR_WORKSPACE;
+    if (misaligned(x, (uintptr_t)elem_size(p->dtype)) || misaligned(weight, 4) || misaligned(bias, 4) ||
+        misaligned(init_state, 4) || misaligned(seq_idx, 4) || misaligned(dy, 4) || misaligned(dfinal, 4) ||
+        misaligned(dx, 4) || misaligned(dweight, 4) || misaligned(dbias, 4) || misaligned(dinit, 4) ||
+        misaligned(workspace, 256))
+        return SSD_ERR_ALIGNMENT;
+    if ((int64_t)workspace_bytes < wsb) return SSD_ERR_WORKSPACE;
+    const ConvSizes z = conv_sizes(p);
+    const Buf in[] = {{x, z.x}, {weight, z.w}, {bias, z.bias}, {init_state, z.state}, {seq_idx, z.seq}, {dy, z.f}, {dfinal, z.state}};
+    const Buf out[] = {{dx, z.f}, {dweight, z.w}, {dbias, z.bias}, {dinit, z.state}, {workspace, wsb}};
+    const int a = check_alias(in, 7, out, 5);
+    if (a != SSD_OK) return a;
+    const int d = check_device();
+    if (d != SSD_OK) return d;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t r = hipSuccess;
+    if (empty) {
+        // no token: nothing reaches the weights, and each row's final state is its initial state
+        r = ssd::launch_fill(dweight, z.w / 4, st);
+        if (r == hipSuccess) r = ssd::launch_fill(dbias, z.bias / 4, st);
+        if (r == hipSuccess && dinit) r = ssd::launch_copy(dinit, seq_idx ? nullptr : dfinal, z.state / 4, st);
+        return done("backward", p, r);
+    }
+    const Shape s = shape_of(p, true);
+    ssd::ConvParams c = params_of(p, s);
+    c.x = x;
+    c.w = weight;
+    c.bias = bias;
+    c.init = init_state;
+    c.seq_idx = seq_idx;
+    c.dy = dy;
+    c.dfin = dfinal;
+    c.dx = dx;
+    c.dinit = dinit;
+    c.part = static_cast<float*>(workspace);
+    // ids that do not occur keep a zero gradient
+    if (seq_idx && dinit) r = ssd::launch_fill(dinit, z.state / 4, st);
+    if (r == hipSuccess) {
+        if (p->dtype == SSD_DTYPE_BF16)
+            r = s.V == 4 ? ssd::launch_conv_k<__bf16, 4, true>(p->width, c, st)
+                         : ssd::launch_conv_k<__bf16, 1, true>(p->width, c, st);
+        else
+            r = s.V == 4 ? ssd::launch_conv_k<float, 4, true>(p->width, c, st)
+                         : ssd::launch_conv_k<float, 1, true>(p->width, c, st);
+    }
+    if (r == hipSuccess) {
+        // one row of part per run: D*K weight gradients, then D bias gradients
+        ssd::ColumnSums cs{};
+        cs.part = c.part;
+        cs.out = dweight;
+        cs.out2 = dbias;
+        cs.split = p->channels * p->width;
+        cs.rows = p->batch * s.nrun;
+        cs.cols = p->channels * (p->width + 1);
+        r = ssd::launch_column_sums(cs, st);
+    }
+    return done("backward", p, r);
+}
+
+int ssd_conv_step(const ssd_conv_problem_t* p, const void* x, const float* weight, const float* bias,
+                  const float* state, float* state_out, void* y, void* stream) {
+    if (!p) return SSD_ERR_NULL_POINTER;
+    if (p->seqlen != 1 || p->nseqs != p->batch) return SSD_ERR_BAD_SHAPE;
+    const int v = validate(p);
+    if (v != SSD_OK) return v;
+    if (!weight || (p->batch > 0 && (!x || !state || !state_out || !y))) return SSD_ERR_NULL_POINTER;
+    const uintptr_t e = (uintptr_t)elem_size(p->dtype);
+    if (misaligned(x, e) || misaligned(y, e) || misaligned(weight, 4) || misaligned(bias, 4) || misaligned(state, 4) ||
+        misaligned(state_out, 4))
+        return SSD_ERR_ALIGNMENT;
+    const ConvSizes z = conv_sizes(p);
+    const Buf in[] = {{x, z.x}, {weight, z.w}, {bias, z.bias}, {state == state_out ? nullptr : state, z.state}};
+    const Buf out[] = {{y, z.y}, {state_out, z.state}};
+    const int a = check_alias(in, 4, out, 2);
+    if (a != SSD_OK) return a;
+    const int d = check_device();
+    if (d != SSD_OK) return d;
+    if (p->batch == 0) return SSD_OK;
+    Shape s = shape_of(p, false);
+    ssd::ConvParams c = params_of(p, s);
+    c.x = x;
+    c.w = weight;
+    c.bias = bias;
+    c.init = state;
+    c.fin = state_out;
+    c.y = y;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const int64_t n = p->batch * p->channels;
+    return done("step", p, p->dtype == SSD_DTYPE_BF16 ? ssd::launch_step<__bf16>(p->width, c, n, st)
+                                                      : ssd::launch_step<float>(p->width, c, n, st));
+}
+
+}  // extern "C"

@@ -1,0 +1,556 @@
+// The norms around a Mamba block and their gradients.  C entries of include/ssd.h.
+//
+// Gated norm, after the scan (per row and group of consecutive channels):
+//   gate first:  u = x silu(z),  out = u r w
+//   gate after:  u = x,          out = u r w silu(z)        r = 1 / sqrt(mean(u^2) + eps)
+// Residual norm, before a block (whole rows):
+//   u = residual + scale x,  out = u r w,  u kept in fp32 as the stream
+//
+// Memory-bound.  A row (of a group) is held in registers by a team of TEAM lanes, CH
+// packs of four channels each, so every input is read once; sums of squares are fp32
+// butterflies within a wave and meet in LDS above it.
+//
+// Gradients, with e = dL/d(u r w) and hat = u r:
+//   du = r (e w - hat mean(e w hat)),   dw = sum over rows of e hat.
+// A team walks several rows of one group, with dw (and the residual's dscale) in
+// registers; the teams' sums go to the workspace and are added in a fixed order.
+#include "ssd.h"
+
+#include <algorithm>
+#include <cstdio>
+
+#include "block_common.hpp"
+#include "ssd_host.hpp"
+
+namespace ssd {
+
+struct NormParams {
+    const void *x, *z;               // z: the gate, or the residual stream (fp32)
+    const float *w, *scale;
+    void* out;
+    float* stream;
+    const float *dout, *dstream;
+    float *dx, *dz, *part;           // dz: of the gate, or of the residual
+    int64_t rows, D, ldx, ldz;
+    int size, groups;                // channels per group, groups per row
+    int64_t slots;                   // teams per group (backward)
+    float eps;
+};
+
+constexpr int kV = 4;                // channels per pack
+
+// Sum over the TEAM lanes of a team, in every lane.  Teams above one wave meet in `red`;
+// two sums in turn need one buffer each (between two uses of a buffer lies the other
+// sum's barrier).
+template <int TEAM> __device__ inline float team_sum(float v, float (&red)[16]) {
+#pragma unroll
+    for (int d = 1; d < (TEAM < 64 ? TEAM : 64); d <<= 1) v += __shfl_xor(v, d);
+    if constexpr (TEAM > 64) {
+        const int w = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) red[w] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < TEAM / 64; ++i) v += red[i];
+    }
+    return v;
+}
+
+// Pack c of the team lane: channels 4 (c TEAM + lane) .. +3 of the group, of which
+// `n` exist.  Whole packs load in one piece, the last of an odd group one by one.
+template <typename T> __device__ inline void load_part(const T* p, int n, float (&v)[kV]) {
+    if (n >= kV) {
+        load_f32<kV>(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) v[i] = i < n ? (float)p[i] : 0.f;
+    }
+}
+template <typename T> __device__ inline void store_part(T* p, int n, const float (&v)[kV]) {
+    if (n >= kV) {
+        store_f32<kV>(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+            if (i < n) p[i] = (T)v[i];
+    }
+}
+
+enum { kGateFirst = 0, kGateAfter = 1, kResidual = 2 };
+constexpr int block_of(int team) { return team < 256 ? 256 : team; }
+
+template <typename TX, typename TO, int MODE, int TEAM, int CH>
+__global__ __launch_bounds__(block_of(TEAM)) void norm_forward_kernel(NormParams p) {
+    constexpr int PER = block_of(TEAM) / TEAM;                   // teams per workgroup
+    __shared__ float red[16];
+    const int lane = threadIdx.x % TEAM;
+    const int64_t unit = (int64_t)blockIdx.x * PER + threadIdx.x / TEAM;
+    if (TEAM <= 64 && unit >= p.rows * p.groups) return;         // (larger teams: one unit per workgroup)
+    const int64_t row = unit / p.groups;
+    const int64_t c0 = (unit % p.groups) * p.size;
+    const TX* x = (const TX*)p.x + row * p.ldx + c0;
+    float u[CH][kV], gate[CH][kV];
+    float sq = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int i = (c * TEAM + lane) * kV, n = p.size - i;
+        if (n <= 0) continue;
+        load_part(x + i, n, u[c]);
+        if constexpr (MODE == kResidual) {
+            if (p.z) load_part((const float*)p.z + row * p.ldz + i, n, gate[c]);
+        } else {
+            load_part((const TO*)p.z + row * p.ldz + c0 + i, n, gate[c]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int i = (c * TEAM + lane) * kV, n = p.size - i;
+        if (n <= 0) continue;
+        if constexpr (MODE == kResidual) {
+            if (p.scale) {
+                float g[kV];
+                load_part(p.scale + i, n, g);
+#pragma unroll
+                for (int v = 0; v < kV; ++v) u[c][v] *= g[v];
+            }
+            if (p.z) {
+#pragma unroll
+                for (int v = 0; v < kV; ++v) u[c][v] += gate[c][v];
+            }
+            store_part(p.stream + row * p.D + i, n, u[c]);
+        } else {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                gate[c][v] = silu_for<TO>(gate[c][v]);
+                if (MODE == kGateFirst) u[c][v] *= gate[c][v];
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < kV; ++v)
+            if (v < n) sq = fmaf(u[c][v], u[c][v], sq);
+    }
+    const float r = 1.f / sqrtf(team_sum<TEAM>(sq, red) / (float)p.size + p.eps);
+    TO* out = (TO*)p.out + row * p.D + c0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int i = (c * TEAM + lane) * kV, n = p.size - i;
+        if (n <= 0) continue;
+        float w[kV], o[kV];
+        load_part(p.w + c0 + i, n, w);
+#pragma unroll
+        for (int v = 0; v < kV; ++v) o[v] = u[c][v] * r * w[v] * (MODE == kGateAfter ? gate[c][v] : 1.f);
+        store_part(out + i, n, o);
+    }
+}
+
+template <typename TX, typename TO, int MODE, int TEAM, int CH>
+__global__ __launch_bounds__(block_of(TEAM)) void norm_backward_kernel(NormParams p) {
+    constexpr int PER = block_of(TEAM) / TEAM;
+    __shared__ float red[2][16];
+    const int lane = threadIdx.x % TEAM;
+    const int64_t team = (int64_t)blockIdx.x * PER + threadIdx.x / TEAM;
+    if (TEAM <= 64 && team >= p.slots * p.groups) return;
+    const int64_t slot = team / p.groups, c0 = (team % p.groups) * p.size;
+    float w[CH][kV], dw[CH][kV], ds[CH][kV];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int i = (c * TEAM + lane) * kV, n = p.size - i;
+        if (n > 0) load_part(p.w + c0 + i, n, w[c]);
+#pragma unroll
+        for (int v = 0; v < kV; ++v) dw[c][v] = ds[c][v] = 0.f;
+    }
+    for (int64_t row = slot; row < p.rows; row += p.slots) {
+        // u (residual: the saved stream), e = dL/d(u r w); gate and x kept for dx and dz
+        float u[CH][kV], e[CH][kV], z[CH][kV], x[CH][kV];
+        float sq = 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int i = (c * TEAM + lane) * kV, n = p.size - i;
+            if (n <= 0) continue;
+            load_part(p.dout + row * p.D + c0 + i, n, e[c]);
+            if constexpr (MODE == kResidual) {
+                load_part(p.stream + row * p.D + i, n, u[c]);
+            } else {
+                load_part((const TX*)p.x + row * p.ldx + c0 + i, n, x[c]);
+                load_part((const TO*)p.z + row * p.ldz + c0 + i, n, z[c]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int n = p.size - (c * TEAM + lane) * kV;
+            if (n <= 0) continue;
+            if constexpr (MODE != kResidual) {
+#pragma unroll
+                for (int v = 0; v < kV; ++v) u[c][v] = MODE == kGateFirst ? x[c][v] * silu(z[c][v]) : x[c][v];
+            }
+#pragma unroll
+            for (int v = 0; v < kV; ++v)
+                if (v < n) sq = fmaf(u[c][v], u[c][v], sq);
+        }
+        const float r = 1.f / sqrtf(team_sum<TEAM>(sq, red[0]) / (float)p.size + p.eps);
+        float dot = 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int n = p.size - (c * TEAM + lane) * kV;
+            if (n <= 0) continue;
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                if (v >= n) continue;
+                const float hat = u[c][v] * r;
+                if constexpr (MODE == kGateAfter) {
+                    const float s = sigmoid(z[c][v]), d = e[c][v];
+                    e[c][v] = d * z[c][v] * s;
+                    z[c][v] = d * hat * w[c][v] * silu_slope(z[c][v], s);       // dz
+                }
+                dw[c][v] = fmaf(e[c][v], hat, dw[c][v]);
+                e[c][v] *= w[c][v];
+                dot = fmaf(e[c][v], hat, dot);
+            }
+        }
+        dot = team_sum<TEAM>(dot, red[1]) / (float)p.size;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int i = (c * TEAM + lane) * kV, n = p.size - i;
+            if (n <= 0) continue;
+            float du[kV];
+#pragma unroll
+            for (int v = 0; v < kV; ++v) du[v] = r * (e[c][v] - u[c][v] * r * dot);
+            if constexpr (MODE == kResidual) {
+                if (p.dstream) {
+                    float d[kV];
+                    load_part(p.dstream + row * p.D + i, n, d);
+#pragma unroll
+                    for (int v = 0; v < kV; ++v) du[v] += d[v];
+                }
+                store_part(p.dz + row * p.D + i, n, du);
+                if (p.scale) {
+                    float g[kV], in[kV];
+                    load_part(p.scale + i, n, g);
+                    load_part((const TX*)p.x + row * p.ldx + i, n, in);
+#pragma unroll
+                    for (int v = 0; v < kV; ++v) {
+                        ds[c][v] = fmaf(du[v], in[v], ds[c][v]);
+                        du[v] *= g[v];
+                    }
+                    store_part(p.dx + row * p.D + i, n, du);
+                }
+            } else {
+                if constexpr (MODE == kGateFirst) {
+                    float dz[kV];
+#pragma unroll
+                    for (int v = 0; v < kV; ++v) {
+                        const float s = sigmoid(z[c][v]);
+                        dz[v] = du[v] * x[c][v] * silu_slope(z[c][v], s);
+                        du[v] *= z[c][v] * s;
+                    }
+                    store_part(p.dz + row * p.D + c0 + i, n, dz);
+                } else {
+                    store_part(p.dz + row * p.D + c0 + i, n, z[c]);
+                }
+                store_part(p.dx + row * p.D + c0 + i, n, du);
+            }
+        }
+    }
+    // one row of part per slot: dw, then dscale
+    const bool scaled = MODE == kResidual && p.scale;
+    float* part = p.part + slot * p.D * (scaled ? 2 : 1) + c0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int i = (c * TEAM + lane) * kV, n = p.size - i;
+        if (n <= 0) continue;
+        store_part(part + i, n, dw[c]);
+        if (scaled) store_part(part + p.D + i, n, ds[c]);
+    }
+}
+
+// Lanes per team and packs per lane for a group of `size` channels.
+struct Team {
+    int lanes, ch;
+};
+static Team team_of(int64_t size) {
+    if (size <= 32) return {8, 1};
+    if (size <= 64) return {16, 1};
+    if (size <= 128) return {32, 1};
+    if (size <= 256) return {64, 1};
+    if (size <= 512) return {64, 2};
+    if (size <= 1024) return {256, 1};
+    for (int ch = 2; ch <= 8; ++ch)
+        if (size <= 1024 * ch) return {256, ch};
+    for (int ch = 3; ch <= 8; ++ch)
+        if (size <= 4096 * ch) return {1024, ch};
+    return {0, 0};
+}
+
+template <typename TX, typename TO, int MODE, int TEAM, int CH>
+static void launch_one(bool backward, const NormParams& p, hipStream_t s) {
+    constexpr int PER = block_of(TEAM) / TEAM;
+    const int64_t units = (backward ? p.slots : p.rows) * p.groups;
+    const dim3 grid((unsigned)((units + PER - 1) / PER)), block(block_of(TEAM));
+    if (backward) hipLaunchKernelGGL((norm_backward_kernel<TX, TO, MODE, TEAM, CH>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((norm_forward_kernel<TX, TO, MODE, TEAM, CH>), grid, block, 0, s, p);
+}
+template <typename TX, typename TO, int MODE> static hipError_t launch_norm(bool backward, const NormParams& p, hipStream_t s) {
+    const Team t = team_of(p.size);
+#define SSD_NORM_CASE(L, C) \
+    if (t.lanes == L && t.ch == C) launch_one<TX, TO, MODE, L, C>(backward, p, s);
+    SSD_NORM_CASE(8, 1) SSD_NORM_CASE(16, 1) SSD_NORM_CASE(32, 1) SSD_NORM_CASE(64, 1) SSD_NORM_CASE(64, 2)
+    SSD_NORM_CASE(256, 1) SSD_NORM_CASE(256, 2) SSD_NORM_CASE(256, 3) SSD_NORM_CASE(256, 4) SSD_NORM_CASE(256, 5)
+    SSD_NORM_CASE(256, 6) SSD_NORM_CASE(256, 7) SSD_NORM_CASE(256, 8)
+    SSD_NORM_CASE(1024, 3) SSD_NORM_CASE(1024, 4) SSD_NORM_CASE(1024, 5) SSD_NORM_CASE(1024, 6) SSD_NORM_CASE(1024, 7)
+    SSD_NORM_CASE(1024, 8)
+#undef SSD_NORM_CASE
+    return hipGetLastError();
+}
+
+}  // namespace ssd
+
+namespace {
+
+using namespace ssd_host;
+
+constexpr int64_t kMaxDim = int64_t(1) << 31;
+constexpr int64_t kMaxGroup = 32768;
+
+int validate(const ssd_norm_problem_t* p, bool gated) {
+    if (!p) return SSD_ERR_NULL_POINTER;
+    if (p->rows < 0 || p->channels <= 0 || p->group_size <= 0 || p->channels % p->group_size != 0 ||
+        p->ldx < p->channels || p->ldz < p->channels)
+        return SSD_ERR_BAD_SHAPE;
+    if (p->rows >= kMaxDim || p->channels >= kMaxDim || p->ldx >= kMaxDim || p->ldz >= kMaxDim) return SSD_ERR_BAD_SHAPE;
+    if (!(p->eps >= 0.f) || p->eps > 1e30f) return SSD_ERR_BAD_SHAPE;
+    if ((p->dtype != SSD_DTYPE_BF16 && p->dtype != SSD_DTYPE_F32) ||
+        (p->x_dtype != SSD_DTYPE_BF16 && p->x_dtype != SSD_DTYPE_F32))
+        return SSD_ERR_UNSUPPORTED;
+    if (p->reserved != 0 || p->group_size > kMaxGroup) return SSD_ERR_UNSUPPORTED;
+    if (gated) {
+        if (p->flags & ~uint32_t(SSD_NORM_GATE_FIRST)) return SSD_ERR_UNSUPPORTED;
+        if (p->x_dtype == SSD_DTYPE_BF16 && p->dtype == SSD_DTYPE_F32) return SSD_ERR_UNSUPPORTED;
+    } else {
+        if (p->flags != 0 || p->x_dtype != p->dtype || p->group_size != p->channels) return SSD_ERR_UNSUPPORTED;
+    }
+    // a launch holds fewer than 2^32 lanes
+    if (double(p->rows) * (p->channels / p->group_size) * ssd::team_of(p->group_size).lanes >= 4e9)
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+// Teams per group in the backward: enough to fill the chip (8 waves per SIMD's worth of
+// lanes over all groups), but at least 8 rows each, so that the partial sums stay small
+// beside the rows themselves.
+int64_t slots_of(const ssd_norm_problem_t* p) {
+    const int lanes = ssd::team_of(p->group_size).lanes;
+    const int64_t groups = p->channels / p->group_size;
+    const int64_t fill = std::max<int64_t>(1, (int64_t(1) << 18) / (lanes * groups));
+    return std::max<int64_t>(1, std::min(fill, (p->rows + 7) / 8));
+}
+int64_t backward_bytes(const ssd_norm_problem_t* p, bool scaled) {
+    return p->rows == 0 ? 0 : align256(slots_of(p) * p->channels * 4 * (scaled ? 2 : 1));
+}
+
+int64_t span(int64_t rows, int64_t ld, int64_t cols, int64_t e) { return rows > 0 ? ((rows - 1) * ld + cols) * e : 0; }
+
+ssd::NormParams params_of(const ssd_norm_problem_t* p) {
+    ssd::NormParams n{};
+    n.rows = p->rows;
+    n.D = p->channels;
+    n.ldx = p->ldx;
+    n.ldz = p->ldz;
+    n.size = (int)p->group_size;
+    n.groups = (int)(p->channels / p->group_size);
+    n.eps = p->eps;
+    return n;
+}
+
+struct Buf {
+    const void* ptr;
+    int64_t bytes;
+};
+int check_alias(const Buf* in, int nin, const Buf* out, int nout) {
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j)
+            if (overlap(out[i].ptr, out[i].bytes, in[j].ptr, in[j].bytes)) return SSD_ERR_ALIAS;
+        for (int j = i + 1; j < nout; ++j)
+            if (overlap(out[i].ptr, out[i].bytes, out[j].ptr, out[j].bytes)) return SSD_ERR_ALIAS;
+    }
+    return SSD_OK;
+}
+
+hipError_t run_gated(const ssd_norm_problem_t* p, bool backward, const ssd::NormParams& n, hipStream_t s) {
+    const bool first = (p->flags & SSD_NORM_GATE_FIRST) != 0;
+    if (p->dtype == SSD_DTYPE_F32)
+        return first ? ssd::launch_norm<float, float, ssd::kGateFirst>(backward, n, s)
+                     : ssd::launch_norm<float, float, ssd::kGateAfter>(backward, n, s);
+    if (p->x_dtype == SSD_DTYPE_F32)
+        return first ? ssd::launch_norm<float, __bf16, ssd::kGateFirst>(backward, n, s)
+                     : ssd::launch_norm<float, __bf16, ssd::kGateAfter>(backward, n, s);
+    return first ? ssd::launch_norm<__bf16, __bf16, ssd::kGateFirst>(backward, n, s)
+                 : ssd::launch_norm<__bf16, __bf16, ssd::kGateAfter>(backward, n, s);
+}
+hipError_t run_residual(const ssd_norm_problem_t* p, bool backward, const ssd::NormParams& n, hipStream_t s) {
+    return p->dtype == SSD_DTYPE_BF16 ? ssd::launch_norm<__bf16, __bf16, ssd::kResidual>(backward, n, s)
+                                      : ssd::launch_norm<float, float, ssd::kResidual>(backward, n, s);
+}
+
+int done(const char* what, const ssd_norm_problem_t* p, hipError_t e) {
+    if (log_enabled())
+        std::fprintf(stderr, "[ssd] %s dtype=%d rows=%lld channels=%lld group=%lld -> %s\n", what, p->dtype,
+                     (long long)p->rows, (long long)p->channels, (long long)p->group_size, hipGetErrorString(e));
+    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+// Sums of the teams' dw and dscale; without rows both are zero.
+hipError_t finish(const ssd_norm_problem_t* p, float* dweight, float* dscale, void* workspace, hipStream_t s) {
+    ssd::ColumnSums c{};
+    c.part = static_cast<float*>(workspace);
+    c.out = dweight;
+    c.out2 = dscale;
+    c.split = p->channels;
+    c.rows = slots_of(p);
+    c.cols = p->channels * (dscale ? 2 : 1);
+    return ssd::launch_column_sums(c, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int ssd_gated_norm_forward(const ssd_norm_problem_t* p, const void* x, const void* z, const float* weight, void* out,
+                           void* stream) {
+    const int v = validate(p, true);
+    if (v != SSD_OK) return v;
+    if (!weight || (p->rows > 0 && (!x || !z || !out))) return SSD_ERR_NULL_POINTER;
+    const int64_t ex = elem_size(p->x_dtype), e = elem_size(p->dtype), cb = p->channels * 4;
+    if (misaligned(x, ex) || misaligned(z, e) || misaligned(out, e) || misaligned(weight, 4)) return SSD_ERR_ALIGNMENT;
+    const Buf ins[] = {{x, span(p->rows, p->ldx, p->channels, ex)}, {z, span(p->rows, p->ldz, p->channels, e)}, {weight, cb}};
+    const Buf outs[] = {{out, p->rows * p->channels * e}};
+    const int a = check_alias(ins, 3, outs, 1);
+    if (a != SSD_OK) return a;
+    const int d = check_device();
+    if (d != SSD_OK) return d;
+    if (p->rows == 0) return SSD_OK;
+    ssd::NormParams n = params_of(p);
+    n.x = x;
+    n.z = z;
+    n.w = weight;
+    n.out = out;
+    return done("gated norm", p, run_gated(p, false, n, static_cast<hipStream_t>(stream)));
+}
+
+size_t ssd_gated_norm_backward_workspace_size(const ssd_norm_problem_t* p) {
+    return validate(p, true) == SSD_OK ? (size_t)backward_bytes(p, false) : 0;
+}
+
+int ssd_gated_norm_backward(const ssd_norm_problem_t* p, const void* x, const void* z, const float* weight,
+                            const float* dout, float* dx, float* dz, float* dweight, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    const int v = validate(p, true);
+    if (v != SSD_OK) return v;
+    if (!weight || !dweight || (p->rows > 0 && (!x || !z || !dout || !dx || !dz))) return SSD_ERR_NULL_POINTER;
+    const int64_t wsb = backward_bytes(p, false);
+    if (wsb > 0 && !workspace) return SSD_ERR_WORKSPACE;
+    const int64_t ex = elem_size(p->x_dtype), e = elem_size(p->dtype), cb = p->channels * 4, f = p->rows * cb;
+    if (misaligned(x, ex) || misaligned(z, e) || misaligned(weight, 4) || misaligned(dout, 4) || misaligned(dx, 4) ||
+        misaligned(dz, 4) || misaligned(dweight, 4) || misaligned(workspace, 256))
+        return SSD_ERR_ALIGNMENT;
+    if ((int64_t)workspace_bytes < wsb) return SSD_ERR_WORKSPACE;
+    const Buf ins[] = {{x, span(p->rows, p->ldx, p->channels, ex)}, {z, span(p->rows, p->ldz, p->channels, e)}, {weight, cb}, {dout, f}};
+    const Buf outs[] = {{dx, f}, {dz, f}, {dweight, cb}, {workspace, wsb}};
+    const int a = check_alias(ins, 4, outs, 4);
+    if (a != SSD_OK) return a;
+    const int d = check_device();
+    if (d != SSD_OK) return d;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (p->rows == 0) return done("gated norm backward", p, ssd::launch_fill(dweight, p->channels, s));
+    ssd::NormParams n = params_of(p);
+    n.x = x;
+    n.z = z;
+    n.w = weight;
+    n.dout = dout;
+    n.dx = dx;
+    n.dz = dz;
+    n.part = static_cast<float*>(workspace);
+    n.slots = slots_of(p);
+    hipError_t r = run_gated(p, true, n, s);
+    if (r == hipSuccess) r = finish(p, dweight, nullptr, workspace, s);
+    return done("gated norm backward", p, r);
+}
+
+int ssd_residual_norm_forward(const ssd_norm_problem_t* p, const void* x, const float* residual, const float* weight,
+                              const float* scale, void* out, float* residual_out, void* stream) {
+    const int v = validate(p, false);
+    if (v != SSD_OK) return v;
+    if (!weight || (p->rows > 0 && (!x || !out || !residual_out))) return SSD_ERR_NULL_POINTER;
+    const int64_t e = elem_size(p->dtype), cb = p->channels * 4, f = p->rows * cb;
+    if (misaligned(x, e) || misaligned(out, e) || misaligned(residual, 4) || misaligned(weight, 4) ||
+        misaligned(scale, 4) || misaligned(residual_out, 4))
+        return SSD_ERR_ALIGNMENT;
+    // the stream may be updated in place: a lane reads its channels before it writes them
+    const bool in_place = residual == residual_out && p->ldz == p->channels;
+    const Buf ins[] = {{x, span(p->rows, p->ldx, p->channels, e)}, {weight, cb}, {scale, cb},
+                       {in_place ? nullptr : residual, span(p->rows, p->ldz, p->channels, 4)}};
+    const Buf outs[] = {{out, p->rows * p->channels * e}, {residual_out, f}};
+    const int a = check_alias(ins, 4, outs, 2);
+    if (a != SSD_OK) return a;
+    const int d = check_device();
+    if (d != SSD_OK) return d;
+    if (p->rows == 0) return SSD_OK;
+    ssd::NormParams n = params_of(p);
+    n.x = x;
+    n.z = residual;
+    n.w = weight;
+    n.scale = scale;
+    n.out = out;
+    n.stream = residual_out;
+    return done("residual norm", p, run_residual(p, false, n, static_cast<hipStream_t>(stream)));
+}
+
+size_t ssd_residual_norm_backward_workspace_size(const ssd_norm_problem_t* p, int scaled) {
+    return validate(p, false) == SSD_OK ? (size_t)backward_bytes(p, scaled != 0) : 0;
+}
+
+int ssd_residual_norm_backward(const ssd_norm_problem_t* p, const void* x, const float* residual_out,
+                               const float* weight, const float* scale, const float* dout, const float* dresidual_out,
+                               float* dx, float* dresidual, float* dweight, float* dscale, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    const int v = validate(p, false);
+    if (v != SSD_OK) return v;
+    if (!weight || !dweight || (scale && !dscale) ||
+        (p->rows > 0 && (!residual_out || !dout || !dresidual || (scale && (!x || !dx)))))
+        return SSD_ERR_NULL_POINTER;
+    const int64_t wsb = backward_bytes(p, scale != nullptr);
+    if (wsb > 0 && !workspace) return SSD_ERR_WORKSPACE;
+    const int64_t e = elem_size(p->dtype), cb = p->channels * 4, f = p->rows * cb;
+    if (misaligned(x, e) || misaligned(residual_out, 4) || misaligned(weight, 4) || misaligned(scale, 4) ||
+        misaligned(dout, 4) || misaligned(dresidual_out, 4) || misaligned(dx, 4) || misaligned(dresidual, 4) ||
+        misaligned(dweight, 4) || misaligned(dscale, 4) || misaligned(workspace, 256))
+        return SSD_ERR_ALIGNMENT;
+    if ((int64_t)workspace_bytes < wsb) return SSD_ERR_WORKSPACE;
+    const Buf ins[] = {{scale ? x : nullptr, span(p->rows, p->ldx, p->channels, e)}, {residual_out, f}, {weight, cb}, {scale, cb}, {dout, f}, {dresidual_out, f}};
+    const Buf outs[] = {{scale ? dx : nullptr, f}, {dresidual, f}, {dweight, cb}, {scale ? dscale : nullptr, cb}, {workspace, wsb}};
+    const int a = check_alias(ins, 6, outs, 5);
+    if (a != SSD_OK) return a;
+    const int d = check_device();
+    if (d != SSD_OK) return d;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (p->rows == 0) {
+        hipError_t r = ssd::launch_fill(dweight, p->channels, s);
+        if (r == hipSuccess && scale) r = ssd::launch_fill(dscale, p->channels, s);
+        return done("residual norm backward", p, r);
+    }
+    ssd::NormParams n = params_of(p);
+    n.x = x;
+    n.w = weight;
+    n.scale = scale;
+    n.stream = const_cast<float*>(residual_out);
+    n.dout = dout;
+    n.dstream = dresidual_out;
+    n.dx = dx;
+    n.dz = dresidual;
+    n.part = static_cast<float*>(workspace);
+    n.slots = slots_of(p);
+    hipError_t r = run_residual(p, true, n, s);
+    if (r == hipSuccess) r = finish(p, dweight, scale ? dscale : nullptr, workspace, s);
+    return done("residual norm backward", p, r);
+}
+
+}  // extern "C"

@@ -1,0 +1,253 @@
+"""The causal convolution (whole rows, gradients, single tokens) against its 64-bit form."""
+import pytest
+import torch
+
+import block_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def announce(msg):
+    print("[case] " + msg, flush=True)
+
+
+def make(dt, b, T, D, K, lens=None, state=True, bias=True, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    n = len(ref.sequences(b, T, lens))
+    return {"x": torch.randn(b, T, D, generator=g).to(TYPES[dt]), "w": torch.randn(D, K, generator=g) / K ** 0.5,
+            "bias": torch.randn(D, generator=g) if bias else None,
+            "init": torch.randn(n, K - 1, D, generator=g) if state else None,
+            "dy": torch.randn(b, T, D, generator=g), "dfinal": torch.randn(n, K - 1, D, generator=g) if state else None,
+            "ids": ref.ids_of(b, T, lens), "lens": lens, "n": n, "K": K}
+
+
+def gpu(v):
+    return v.cuda() if torch.is_tensor(v) else v
+
+
+def zero_state(q):
+    return torch.zeros(q["n"], q["K"] - 1, q["x"].shape[2]) if q["init"] is None else q["init"]
+
+
+CASES = [
+    # dtype, rows, tokens, channels, K, sequence lengths, initial state, bias, silu
+    ("bf16", 2, 130, 64, 4, None, True, True, True),
+    ("f32", 2, 130, 64, 4, None, True, True, True),
+    ("bf16", 1, 1, 40, 4, None, True, True, True),             # one token
+    ("f32", 3, 2, 5, 4, None, True, False, False),             # fewer tokens than taps, one tail vector
+    ("f32", 1, 300, 3, 3, None, False, True, True),            # fewer channels than a vector
+    ("bf16", 1, 97, 7, 2, None, True, True, False),
+    ("bf16", 2, 75, 1029, 3, None, False, False, True),        # odd channels: unaligned rows
+    ("f32", 1, 67, 131, 4, [[1, 1, 1, 2, 3, 4, 5, 18, 31, 1]], True, True, True),
+    ("bf16", 2, 70, 72, 4, [[64, 6], [1, 2, 67]], True, True, True),
+    ("bf16", 1, 200, 33, 2, [[3, 61, 64, 72]], False, True, True),
+    ("f32", 2, 40, 24, 3, [[40], [2, 1, 37]], True, True, False),
+    ("bf16", 1, 5000, 16, 4, None, True, True, True),          # many runs of one row
+]
+IDS = ["%s-b%d-T%d-D%d-K%d-%s%s" % (c[0], c[1], c[2], c[3], c[4], "packed" if c[5] else "rows", "" if c[6] else "-nostate")
+       for c in CASES]
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_forward(case):
+    import mamba_ssd_scan_chunked_amd as ssd
+    dt, b, T, D, K, lens, state, bias, act = case
+    announce("conv forward %s" % (case,))
+    q = make(dt, b, T, D, K, lens, state, bias)
+    y, f = ssd.causal_conv(gpu(q["x"]), gpu(q["w"]), gpu(q["bias"]), gpu(q["init"]), gpu(q["ids"]),
+                           q["n"] if lens else None, silu=act)
+    args = [t if t is None else t.double() for t in (q["x"], q["w"], q["bias"], zero_state(q))]
+    yr, fr = ref.conv(*args, lens, act)
+    # each of K + 1 terms of pre passes K roundings; silu has slope below 1.1 and eight of its own
+    size, _ = ref.conv(args[0].abs(), args[1].abs(), None if args[2] is None else args[2].abs(), args[3].abs(), lens, False)
+    ref.check(y, yr, size, 1.1 * K + 8, "y")
+    assert torch.equal(f.cpu().double(), fr), "the final state holds inputs: no rounding"
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_backward(case):
+    import mamba_ssd_scan_chunked_amd as ssd
+    dt, b, T, D, K, lens, state, bias, act = case
+    announce("conv backward %s" % (case,))
+    q = make(dt, b, T, D, K, lens, state, bias, seed=1)
+    got = ssd.causal_conv_backward(gpu(q["x"]), gpu(q["w"]), gpu(q["dy"]), gpu(q["bias"]), gpu(q["init"]),
+                                   gpu(q["dfinal"]), gpu(q["ids"]), q["n"] if lens else None, silu=act)
+    bias_in = torch.zeros(D) if q["bias"] is None else q["bias"]
+    lv = ref.leaves(q["x"], q["w"], bias_in, zero_state(q))
+    y, f = ref.conv(*lv, lens, act)
+    dfin = torch.zeros_like(f) if q["dfinal"] is None else q["dfinal"].double()
+    grads = torch.autograd.grad((y * q["dy"].double()).sum() + (f * dfin).sum(), lv)
+    # magnitudes: the gradient of the same sums with every factor's magnitude and silu's
+    # slope at its most, 1.1.  g = dy silu'(pre): pre is off by K U32 size(pre) and silu''
+    # is below 0.5; size(pre) stays below 16 at these inputs, so 8 K roundings, eight of the
+    # slope itself and K of the sum.  Sums over tokens add at most 64 in a run, then the
+    # runs, 16 at a time over 16 waves.
+    av = ref.leaves(*[t.detach().abs() for t in lv])
+    ya, fa = ref.conv(*av, lens, False)
+    assert float(ya.max()) < 16
+    scales = torch.autograd.grad((1.1 * ya * q["dy"].double().abs()).sum() + (fa * dfin.abs()).sum(), av)
+    runs = b * ((T + 3) // 4)
+    for name, r, s, extra in zip(("dx", "dweight", "dbias", "dinit"), grads, scales, (0, 96 + runs / 16, 96 + runs / 16, 0)):
+        ref.check(got[name], r, s, 9 * K + 8 + extra, name)
+
+
+def test_gradients_against_differences():
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("conv differences")
+    lens = [[1, 2, 30, 7]]
+    q = make("f32", 1, 40, 12, 4, lens, seed=5)
+    got = ssd.causal_conv_backward(gpu(q["x"]), gpu(q["w"]), gpu(q["dy"]), gpu(q["bias"]), gpu(q["init"]),
+                                   gpu(q["dfinal"]), gpu(q["ids"]), q["n"])
+    base = [q[k].double() for k in ("x", "w", "bias", "init")]
+
+    def loss(args):
+        y, f = ref.conv(*args, lens, True)
+        return float((y * q["dy"].double()).sum() + (f * q["dfinal"].double()).sum())
+
+    g = torch.Generator().manual_seed(6)
+    for i, name in enumerate(("dx", "dweight", "dbias", "dinit")):
+        v = torch.randn(base[i].shape, generator=g).double()
+        h = 1e-5
+        lo, hi = list(base), list(base)
+        lo[i], hi[i] = base[i] - h * v, base[i] + h * v
+        slope = (loss(hi) - loss(lo)) / (2 * h)
+        along = float((got[name].cpu().double() * v).sum())
+        # differences: h^2 times the third derivative, and 2^-52 |loss| / h; the kernel: fp32 gradients
+        assert abs(along - slope) <= 1e-5 * float((got[name].cpu().double() * v).abs().sum()), name
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_steps_continue_a_prompt(dt, K, in_place):
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("conv steps %s K=%d" % (dt, K))
+    q = make(dt, 3, 20, 37, K, seed=2)
+    d = {k: gpu(v) for k, v in q.items()}
+    y, f = ssd.causal_conv(d["x"], d["w"], d["bias"], d["init"])
+    _, state = ssd.causal_conv(d["x"][:, :13], d["w"], d["bias"], d["init"])
+    for t in range(13, 20):
+        if in_place:
+            yt = ssd.causal_conv_step(d["x"][:, t], d["w"], d["bias"], state)
+        else:
+            old, new = state.clone(), torch.empty_like(state)
+            yt = ssd.causal_conv_step(d["x"][:, t], d["w"], d["bias"], state, state_out=new)
+            assert torch.equal(state, old)
+            state = new
+        # the same K products, summed in one order in both kernels
+        ref.check(yt, y[:, t].cpu(), y[:, t].cpu().abs() + 8, 2 * K + 8, "y of a step")
+    assert torch.equal(state, f)
+
+
+def test_slices_are_read_in_place():
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("conv slices")
+    q = make("bf16", 2, 50, 48, 4, seed=3)
+    wide = torch.randn(2, 50, 131, device="cuda").to(torch.bfloat16)
+    wide[:, :, 33:81] = q["x"].cuda()
+    part = wide[:, :, 33:81]
+    y, f = ssd.causal_conv(part, gpu(q["w"]), gpu(q["bias"]), gpu(q["init"]))
+    y0, f0 = ssd.causal_conv(gpu(q["x"]), gpu(q["w"]), gpu(q["bias"]), gpu(q["init"]))
+    assert torch.equal(y, y0) and torch.equal(f, f0)
+    a = ssd.causal_conv_backward(part, gpu(q["w"]), gpu(q["dy"]), gpu(q["bias"]), gpu(q["init"]))
+    c = ssd.causal_conv_backward(gpu(q["x"]), gpu(q["w"]), gpu(q["dy"]), gpu(q["bias"]), gpu(q["init"]))
+    assert all(torch.equal(a[k], c[k]) for k in c)
+    # transposed activations and rows in another order are copied first
+    t = q["x"].cuda().transpose(1, 2).contiguous().transpose(1, 2)
+    assert torch.equal(ssd.causal_conv(t, gpu(q["w"]), gpu(q["bias"]), gpu(q["init"]))[0], y0)
+    one = torch.ones(1, 1, 48, device="cuda", dtype=torch.bfloat16).expand(2, 50, 48)
+    assert torch.equal(ssd.causal_conv(one, gpu(q["w"]))[0], ssd.causal_conv(one.contiguous(), gpu(q["w"]))[0])
+
+
+def test_bad_values_stay_in_their_sequence():
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("conv no leak")
+    lens = [[5, 1, 40, 18]]
+    q = make("f32", 1, 64, 20, 4, lens, seed=4)
+    d = {k: gpu(v) for k, v in q.items()}
+    clean = ssd.causal_conv(d["x"], d["w"], d["bias"], d["init"], d["ids"], q["n"])
+    cleang = ssd.causal_conv_backward(d["x"], d["w"], d["dy"], d["bias"], d["init"], d["dfinal"], d["ids"], q["n"])
+    for bad in (float("inf"), float("nan")):
+        x, dy = d["x"].clone(), d["dy"].clone()
+        x[0, 6:46], dy[0, 6:46] = bad, bad
+        y, f = ssd.causal_conv(x, d["w"], d["bias"], d["init"], d["ids"], q["n"])
+        for lo, hi in ((0, 6), (46, 64)):
+            assert torch.equal(y[:, lo:hi], clean[0][:, lo:hi])
+        assert torch.equal(f[[0, 1, 3]], clean[1][[0, 1, 3]])
+        g = ssd.causal_conv_backward(x, d["w"], dy, d["bias"], d["init"], d["dfinal"], d["ids"], q["n"])
+        for lo, hi in ((0, 6), (46, 64)):
+            assert torch.equal(g["dx"][:, lo:hi], cleang["dx"][:, lo:hi])
+        assert torch.equal(g["dinit"][[0, 1, 3]], cleang["dinit"][[0, 1, 3]])
+
+
+def test_absent_sequences_and_empty_rows():
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("conv absent ids")
+    q = make("f32", 1, 6, 10, 4, None, seed=7)
+    ids = torch.tensor([[1, 1, 3, 3, 3, 3]], dtype=torch.int32).cuda()
+    init, dfin = torch.randn(5, 3, 10).cuda(), torch.randn(5, 3, 10).cuda()
+    f = torch.full((5, 3, 10), 7.0).cuda()
+    ssd.causal_conv(gpu(q["x"]), gpu(q["w"]), None, init, ids, 5, final_state=f)
+    assert bool((f[[0, 2, 4]] == 7).all()) and not bool((f[[1, 3]] == 7).any())
+    g = ssd.causal_conv_backward(gpu(q["x"]), gpu(q["w"]), gpu(q["dy"]), None, init, dfin, ids, 5)
+    assert bool((g["dinit"][[0, 2, 4]] == 0).all()) and bool((g["dinit"][[1, 3]] != 0).any())
+    x = torch.empty(2, 0, 10, device="cuda")
+    init, dfin = init[:2].contiguous(), dfin[:2].contiguous()
+    y, f = ssd.causal_conv(x, gpu(q["w"]), None, init)
+    assert y.shape == x.shape and torch.equal(f, init)
+    g = ssd.causal_conv_backward(x, gpu(q["w"]), x, None, init, dfin)
+    assert torch.equal(g["dinit"], dfin) and not bool(g["dweight"].any()) and not bool(g["dbias"].any())
+    g = ssd.causal_conv_backward(x, gpu(q["w"]), x)
+    assert not bool(g["dinit"].any())
+    y, f = ssd.causal_conv(torch.empty(0, 4, 10, device="cuda"), gpu(q["w"]))
+    assert y.shape == (0, 4, 10) and f.shape == (0, 3, 10)
+    assert ssd.causal_conv_step(x[:0, 0:0].reshape(0, 10), gpu(q["w"]), None, init[:0]).shape == (0, 10)
+
+
+def test_graph_replays_equal_eager():
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("conv graph")
+    lens = [[40, 3, 100], [143]]
+    q = make("bf16", 2, 143, 64, 4, lens, seed=8)
+    d = {k: gpu(v) for k, v in q.items()}
+    state = d["init"][:2].contiguous()
+
+    def run(s):
+        y, f = ssd.causal_conv(d["x"], d["w"], d["bias"], d["init"], d["ids"], q["n"])
+        g = ssd.causal_conv_backward(d["x"], d["w"], d["dy"], d["bias"], d["init"], d["dfinal"], d["ids"], q["n"])
+        return [y, f, ssd.causal_conv_step(d["x"][:, 0], d["w"], d["bias"], s)] + [g[k] for k in sorted(g)]
+
+    eager_state = state.clone()
+    eager = run(eager_state)
+    torch.cuda.synchronize()
+    graph_state = state.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run(graph_state)
+    for _ in range(3):
+        for t in outs:
+            t.fill_(float("nan"))
+        graph_state.copy_(state)
+        torch.cuda.synchronize()
+        graph.replay()
+        run(state.clone())
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(outs, eager)) and torch.equal(graph_state, eager_state)
+
+
+def test_another_stream():
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("conv stream")
+    q = make("f32", 2, 300, 50, 4, seed=9)
+    d = {k: gpu(v) for k, v in q.items()}
+    y0, f0 = ssd.causal_conv(d["x"], d["w"], d["bias"], d["init"])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for handle in (s, s.cuda_stream):
+        y, f = ssd.causal_conv(d["x"].transpose(1, 2).contiguous().transpose(1, 2), d["w"], d["bias"], d["init"])
+        torch.cuda.synchronize()
+        y, f = ssd.causal_conv(d["x"], d["w"], d["bias"], d["init"], stream=handle)
+        s.synchronize()
+        assert torch.equal(y, y0) and torch.equal(f, f0)
