@@ -335,6 +335,68 @@ int ssd_conv_backward(const ssd_conv_problem_t* p, const void* x, const float* w
 int ssd_conv_step(const ssd_conv_problem_t* p, const void* x, const float* weight, const float* bias,
                   const float* state, float* state_out, void* y, void* stream);
 
+typedef struct {
+    int64_t batch;      /* rows                                                     */
+    int64_t seqlen;     /* tokens per row (may be 0)                                */
+    int64_t channels;   /* D                                                        */
+    int64_t dstate;     /* N: 8, 16, 32 or 64                                       */
+    int64_t ngroups;    /* G: B/C groups; channel d reads group d / (D / G)         */
+    int64_t nseqs;      /* number of sequences: == batch without seq_idx            */
+    int64_t ldx, lddt, ldz;   /* elements from one token to the next, >= channels   */
+    int64_t ldb, ldc;         /* the same of B and C, >= ngroups * dstate           */
+    int32_t dtype;      /* ssd_dtype_t of x, dt, B, C, z and y                      */
+    uint32_t flags;     /* SSD_FLAG_DT_SOFTPLUS or 0                                */
+    int32_t segments;   /* segments per row, as in ssd_problem_t: 0 lets the library choose */
+    int32_t reserved;   /* must be 0                                                */
+} ssd_selective_problem_t;
+
+/* The selective scan with a decay per channel and state (the scan of the Mamba-1 block;
+ * selective-SSM section of the "Mamba" paper story):
+ *     h_t[d][n] = exp(step_t[d] A[d][n]) h_{t-1}[d][n] + step_t[d] x_t[d] B_t[n],
+ *     y_t[d] = sum_n C_t[n] h_t[d][n] + D[d] x_t[d],   times silu(z_t[d]) with z,
+ * A = -exp(A_log), step = dt + dt_bias, through softplus with SSD_FLAG_DT_SOFTPLUS.
+ *   x, dt       (batch, seqlen, channels)          dtype; tokens ldx, lddt apart
+ *   dt_bias     (channels)                         fp32, or NULL (= 0)
+ *   A_log       (channels, dstate)                 fp32
+ *   B, C        (batch, seqlen, ngroups, dstate)   dtype; tokens ldb, ldc apart
+ *   D           (channels)                         fp32, or NULL for no skip term
+ *   z           (batch, seqlen, channels)          dtype, tokens ldz apart, or NULL for no gate
+ *   init_state  (nseqs, channels, dstate)          fp32, or NULL for zeros
+ *   seq_idx     (batch, seqlen)                    int32 or NULL, as in ssd_forward
+ *   y           (batch, seqlen, channels)          dtype, output
+ *   final_state (nseqs, channels, dstate)          fp32 output, or NULL; rows of ids that do
+ *                                                  not occur are not written
+ *   workspace   >= ssd_selective_workspace_size(p) bytes, 256-byte aligned (NULL / 0 when 0)
+ * The recurrence runs in fp32.  Rows are cut into segments (one launch becomes three) when
+ * there are too few channels and rows to fill the chip.  Outputs must not overlap inputs,
+ * the workspace or each other (SSD_ERR_ALIAS); the state is not carried in place. */
+size_t ssd_selective_workspace_size(const ssd_selective_problem_t* p);
+int ssd_selective_forward(const ssd_selective_problem_t* p, const void* x, const void* dt, const float* dt_bias,
+                          const float* A_log, const void* B, const void* C, const float* D, const void* z,
+                          const float* init_state, const int32_t* seq_idx, void* y, float* final_state, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* One token (decoding): ssd_selective_forward with seqlen 1 and nseqs == batch, from `state`
+ * to `state_out`, which may be the same buffer (in place) or one that does not overlap it.
+ * One launch, bound by reading and writing the state. */
+int ssd_selective_step(const ssd_selective_problem_t* p, const void* x, const void* dt, const float* dt_bias,
+                       const float* A_log, const void* B, const void* C, const float* D, const void* z,
+                       const float* state, float* state_out, void* y, void* stream);
+
+/* Gradients of L for dL/dy = dy (fp32) and dL/dfinal_state = dfinal (fp32, or NULL), all
+ * fp32 and dense, shaped like their inputs: dx, ddt (through softplus if flagged), dA_log,
+ * dB, dC (summed over the channels of a group), dz (required with z), and, each NULL if not
+ * wanted, dD, dinit (at a zero state when init_state is NULL; zero for ids that do not
+ * occur) and ddt_bias.  workspace: >= ssd_selective_backward_workspace_size(p) bytes,
+ * 256-byte aligned: a state every eight tokens, and the channel blocks' parts of dB and dC.
+ * Sums are taken in a fixed order: results are deterministic. */
+size_t ssd_selective_backward_workspace_size(const ssd_selective_problem_t* p);
+int ssd_selective_backward(const ssd_selective_problem_t* p, const void* x, const void* dt, const float* dt_bias,
+                           const float* A_log, const void* B, const void* C, const float* D, const void* z,
+                           const float* init_state, const int32_t* seq_idx, const float* dy, const float* dfinal,
+                           float* dx, float* ddt, float* dA_log, float* dB, float* dC, float* dD, float* dz,
+                           float* dinit, float* ddt_bias, void* workspace, size_t workspace_bytes, void* stream);
+
 /* norm flags */
 enum {
     SSD_NORM_GATE_FIRST = 1u << 0    /* gate before the norm (else after it) */

@@ -25,14 +25,18 @@ from . import block as _block
 from .block import (CONV_SILU, NORM_GATE_FIRST, ConvProblem, NormProblem, causal_conv, causal_conv_backward,
                     causal_conv_step, conv_backward_workspace_size, conv_problem, gated_norm, gated_norm_backward,
                     gated_norm_backward_workspace_size, norm_problem, residual_norm, residual_norm_backward,
-                    residual_norm_backward_workspace_size)
+                    residual_norm_backward_workspace_size, SelectiveProblem, selective_backward_workspace_size,
+                    selective_problem, selective_scan, selective_scan_backward, selective_step,
+                    selective_workspace_size)
 
 __all__ = ["forward", "forward_into", "forward_into_noalloc", "noalloc_scratch_bytes", "step", "backward", "backward_into", "backward_workspace_size", "workspace_size", "validate", "problem", "SSDError",
            "version", "library_path", "load_library", "DTYPE_F32", "DTYPE_BF16", "FLAG_DT_SCALES_X",
            "FLAG_DT_SOFTPLUS", "FLAG_ZOH", "causal_conv", "causal_conv_backward", "causal_conv_step", "conv_problem",
            "conv_backward_workspace_size", "gated_norm", "gated_norm_backward", "residual_norm",
            "residual_norm_backward", "norm_problem", "gated_norm_backward_workspace_size",
-           "residual_norm_backward_workspace_size", "ConvProblem", "NormProblem", "CONV_SILU", "NORM_GATE_FIRST"]
+           "residual_norm_backward_workspace_size", "ConvProblem", "NormProblem", "CONV_SILU", "NORM_GATE_FIRST",
+           "selective_scan", "selective_scan_backward", "selective_step", "selective_problem",
+           "selective_workspace_size", "selective_backward_workspace_size", "SelectiveProblem"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libssd_mi355x.so"

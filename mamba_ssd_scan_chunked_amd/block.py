@@ -1,13 +1,16 @@
 """The operators around the scan in a Mamba layer: the short causal convolution, the
-gated norm after the scan and the residual norm before a block, with their gradients
-and single-token forms, through the C ABI in ``include/ssd.h``.
+selective scan with a decay per channel and state, the gated norm after the scan and
+the residual norm before a block, with their gradients and single-token forms, through
+the C ABI in ``include/ssd.h``.
 
     y, final   = causal_conv(x, weight, bias, init_state, seq_idx, nseqs)
     y          = causal_conv_step(x, weight, bias, state)
+    y, final   = selective_scan(x, dt, A_log, B, C, D, z, init_state, seq_idx, nseqs)
+    y          = selective_step(x, dt, A_log, B, C, D, state, z)
     out        = gated_norm(x, z, weight)
     out, res   = residual_norm(x, residual, weight)
 
-Activations (x, z, y, out) are bf16 or fp32; parameters, states and gradients are
+Activations (x, dt, B, C, z, y, out) are bf16 or fp32; parameters, states and gradients are
 fp32.  Activations may be slices of a projection's output (channels contiguous, one
 distance between all tokens): they are read in place.  Anything else that is not
 contiguous is copied first.  A call runs on ``stream`` (a torch stream or a raw
@@ -32,6 +35,14 @@ class ConvProblem(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32)]
 
 
+class SelectiveProblem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("nseqs", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("lddt", ctypes.c_int64), ("ldz", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("ldc", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("segments", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class NormProblem(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("group_size", ctypes.c_int64),
                 ("ldx", ctypes.c_int64), ("ldz", ctypes.c_int64), ("eps", ctypes.c_float),
@@ -42,12 +53,17 @@ class NormProblem(ctypes.Structure):
 def _declare(lib):
     """Argument types of the library's entry points."""
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
-    conv, norm = ctypes.POINTER(ConvProblem), ctypes.POINTER(NormProblem)
+    conv, norm, sel = (ctypes.POINTER(s) for s in (ConvProblem, NormProblem, SelectiveProblem))
     for name, args, res in (
             ("ssd_conv_forward", [conv] + [vp] * 8, i32),
             ("ssd_conv_backward_workspace_size", [conv], sz),
             ("ssd_conv_backward", [conv] + [vp] * 12 + [sz, vp], i32),
             ("ssd_conv_step", [conv] + [vp] * 7, i32),
+            ("ssd_selective_workspace_size", [sel], sz),
+            ("ssd_selective_forward", [sel] + [vp] * 13 + [sz, vp], i32),
+            ("ssd_selective_step", [sel] + [vp] * 12, i32),
+            ("ssd_selective_backward_workspace_size", [sel], sz),
+            ("ssd_selective_backward", [sel] + [vp] * 22 + [sz, vp], i32),
             ("ssd_gated_norm_forward", [norm] + [vp] * 5, i32),
             ("ssd_gated_norm_backward_workspace_size", [norm], sz),
             ("ssd_gated_norm_backward", [norm] + [vp] * 8 + [sz, vp], i32),
@@ -276,6 +292,150 @@ def _states(state, state_out, shape, dev):
         return state, state
     _check_buffer("state_out", state_out, shape, torch.float32, dev)
     return _given("state", state, shape, torch.float32, dev), state_out
+
+
+# ------------------------------------------------------------------ selective scan
+FLAG_DT_SOFTPLUS = 2
+
+
+def selective_problem(batch, seqlen, channels, dstate, ngroups=1, nseqs=None, dtype=DTYPE_BF16, dt_softplus=False,
+                      segments=0, ldx=None, lddt=None, ldz=None, ldb=None, ldc=None) -> SelectiveProblem:
+    """A problem description; ``segments`` > 0 forces the number of segments each row is
+    cut into (0: the library's choice); it does not change the result."""
+    wide, gn = channels, ngroups * dstate
+    return SelectiveProblem(batch, seqlen, channels, dstate, ngroups, batch if nseqs is None else nseqs,
+                            wide if ldx is None else ldx, wide if lddt is None else lddt, wide if ldz is None else ldz,
+                            gn if ldb is None else ldb, gn if ldc is None else ldc, dtype,
+                            FLAG_DT_SOFTPLUS if dt_softplus else 0, segments, 0)
+
+
+def selective_workspace_size(p: SelectiveProblem) -> int:
+    return int(_lib().ssd_selective_workspace_size(ctypes.byref(p)))
+
+
+def selective_backward_workspace_size(p: SelectiveProblem) -> int:
+    return int(_lib().ssd_selective_backward_workspace_size(ctypes.byref(p)))
+
+
+def _activation(name, t, shape, like):
+    """An activation of x's type and device as rows: (t, ld)."""
+    if t.device != like.device:
+        raise ValueError("%s is on %s, x on %s" % (name, t.device, like.device))
+    if t.dtype != like.dtype:
+        raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return _rows(t)
+
+
+def _selective_arguments(x, dt, A_log, B, C, D, z, init_state, seq_idx, nseqs, dt_bias, dt_softplus, segments):
+    """(problem, pointers' tensors in the order of the C call up to seq_idx)."""
+    import torch
+    if x.dim() != 3 or B.dim() != 4 or A_log.dim() != 2:
+        raise ValueError("x must be (b,T,D), B and C (b,T,G,N) and A_log (D,N)")
+    dev, f32 = x.device, torch.float32
+    b, T, Dc = x.shape
+    G, N = B.shape[2:]
+    code = _dtype("x", x)
+    A_log = _given("A_log", A_log, (Dc, N), f32, dev)
+    D = _given("D", D, (Dc,), f32, dev)
+    dt_bias = _given("dt_bias", dt_bias, (Dc,), f32, dev)
+    seq_idx, ns = _sequences(x, seq_idx, nseqs)
+    init_state = _given("init_state", init_state, (ns, Dc, N), f32, dev)
+    if C.shape != B.shape:
+        raise ValueError("B and C must have one shape")
+    dt, lddt = _activation("dt", dt, x.shape, x)
+    ldz = Dc
+    if z is not None:
+        z, ldz = _activation("z", z, x.shape, x)
+    B, ldb = _activation("B", B.flatten(-2), (b, T, G * N), x)
+    C, ldc = _activation("C", C.flatten(-2), (b, T, G * N), x)
+    x, ldx = _rows(x)
+    p = selective_problem(b, T, Dc, N, G, ns, code, dt_softplus, segments, ldx, lddt, ldz, ldb, ldc)
+    return p, (x, dt, dt_bias, A_log, B, C, D, z, init_state, seq_idx)
+
+
+def selective_scan(x, dt, A_log, B, C, D=None, z=None, init_state=None, seq_idx=None, nseqs: Optional[int] = None,
+                   dt_bias=None, dt_softplus: bool = False, y=None, final_state=None, workspace=None,
+                   return_final: bool = True, stream=None, segments: int = 0):
+    """The selective scan of whole rows through ``ssd_selective_forward``.
+
+    x, dt (b,T,D), B, C (b,T,G,N) and the gate z (b,T,D; None: no gate) in one type;
+    A_log (D,N), D, dt_bias (D) fp32; the state (nseqs,D,N) fp32, N one of 8, 16, 32, 64.
+    The step size is dt + dt_bias, through softplus with ``dt_softplus``; packed sequences
+    and ``segments`` as in :func:`forward`.  Returns (y like x, final_state or None)."""
+    import torch
+    dev = _gpu(x)
+    with _on(dev, stream):
+        p, args = _selective_arguments(x, dt, A_log, B, C, D, z, init_state, seq_idx, nseqs, dt_bias, dt_softplus,
+                                       segments)
+        y = _output("y", y, x.shape, x.dtype, dev)
+        if final_state is not None or return_final:
+            final_state = _output("final_state", final_state, (p.nseqs, p.channels, p.dstate), torch.float32, dev)
+        ws, nbytes = _workspace(workspace, selective_workspace_size(p), dev)
+        _check(_lib().ssd_selective_forward(ctypes.byref(p), *map(_ptr, args), _ptr(y), _ptr(final_state), _ptr(ws),
+                                            nbytes, _current(dev)))
+    return y, final_state
+
+
+def selective_scan_backward(x, dt, A_log, B, C, dy, D=None, z=None, init_state=None, dfinal=None, seq_idx=None,
+                            nseqs: Optional[int] = None, dt_bias=None, dt_softplus: bool = False, workspace=None,
+                            stream=None, segments: int = 0):
+    """Gradients through ``ssd_selective_backward`` of <dy, y> + <dfinal, final_state> for
+    :func:`selective_scan` with the same arguments; dy (b,T,D) and dfinal fp32.  Returns a
+    dict of fp32 tensors dx, ddt, dA_log, dB, dC, dD, dinit, ddt_bias and, with z, dz (dD,
+    dinit and ddt_bias at zero when the input was not given)."""
+    import torch
+    dev, f32 = _gpu(x), torch.float32
+    with _on(dev, stream):
+        p, args = _selective_arguments(x, dt, A_log, B, C, D, z, init_state, seq_idx, nseqs, dt_bias, dt_softplus,
+                                       segments)
+        state = (p.nseqs, p.channels, p.dstate)
+        dy = _given("dy", dy, x.shape, f32, dev)
+        dfinal = _given("dfinal", dfinal, state, f32, dev)
+        shapes = {"dx": x.shape, "ddt": x.shape, "dA_log": A_log.shape, "dB": B.shape, "dC": C.shape,
+                  "dD": (p.channels,), "dz": x.shape, "dinit": state, "ddt_bias": (p.channels,)}
+        if z is None:
+            del shapes["dz"]
+        out = {k: torch.empty(s, dtype=f32, device=dev) for k, s in shapes.items()}
+        ws, nbytes = _workspace(workspace, selective_backward_workspace_size(p), dev)
+        g = out.get
+        _check(_lib().ssd_selective_backward(ctypes.byref(p), *map(_ptr, args), _ptr(dy), _ptr(dfinal), _ptr(g("dx")),
+                                             _ptr(g("ddt")), _ptr(g("dA_log")), _ptr(g("dB")), _ptr(g("dC")),
+                                             _ptr(g("dD")), _ptr(g("dz")), _ptr(g("dinit")), _ptr(g("ddt_bias")),
+                                             _ptr(ws), nbytes, _current(dev)))
+    return out
+
+
+def selective_step(x, dt, A_log, B, C, D, state, z=None, y=None, dt_bias=None, dt_softplus: bool = False,
+                   state_out=None, stream=None):
+    """One token per row through ``ssd_selective_step``: x, dt, z (b,D), B, C (b,G,N),
+    ``state`` (b,D,N) fp32, updated in place or, with ``state_out``, left as it was and the
+    new state written there.  Returns y (b,D)."""
+    import torch
+    dev, f32 = _gpu(x), torch.float32
+    if x.dim() != 2 or B.dim() != 3 or A_log.dim() != 2:
+        raise ValueError("x must be (b,D), B and C (b,G,N) and A_log (D,N)")
+    with _on(dev, stream):
+        b, Dc = x.shape
+        G, N = B.shape[1:]
+        A_log = _given("A_log", A_log, (Dc, N), f32, dev)
+        D = _given("D", D, (Dc,), f32, dev)
+        dt_bias = _given("dt_bias", dt_bias, (Dc,), f32, dev)
+        state, state_out = _states(state, state_out, (b, Dc, N), dev)
+        dt, lddt = _activation("dt", dt, x.shape, x)
+        ldz = Dc
+        if z is not None:
+            z, ldz = _activation("z", z, x.shape, x)
+        B, ldb = _activation("B", B.flatten(-2), (b, G * N), x)
+        C, ldc = _activation("C", C.flatten(-2), (b, G * N), x)
+        y = _output("y", y, (b, Dc), x.dtype, dev)
+        x, ldx = _rows(x)
+        p = selective_problem(b, 1, Dc, N, G, b, _dtype("x", x), dt_softplus, 0, ldx, lddt, ldz, ldb, ldc)
+        _check(_lib().ssd_selective_step(ctypes.byref(p), _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A_log), _ptr(B),
+                                         _ptr(C), _ptr(D), _ptr(z), _ptr(state), _ptr(state_out), _ptr(y),
+                                         _current(dev)))
+    return y
 
 
 # ------------------------------------------------------------------ norms

@@ -32,8 +32,10 @@ __global__ __launch_bounds__(1024) void column_sums_kernel(ColumnSums c) {
         for (int k = 0; k < 16; ++k) total += acc[k][lane];
         if (col < c.split) {
             if (c.out) c.out[col] = total;
-        } else if (c.out2) {
-            c.out2[col - c.split] = total;
+        } else if (col < c.split2) {
+            if (c.out2) c.out2[col - c.split] = total;
+        } else if (c.out3) {
+            c.out3[col - c.split2] = total;
         }
     }
 }

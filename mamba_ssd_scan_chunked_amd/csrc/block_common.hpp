@@ -73,12 +73,12 @@ __device__ inline int64_t clamp_id(int32_t id, int64_t nseqs) {
     return id < 0 ? 0 : (id >= nseqs ? nseqs - 1 : id);
 }
 
-// Column sums of part (rows x cols), rows in a fixed order: columns below `split` go
-// to out, the rest to out2 (either may be null: not wanted).
+// Column sums of part (rows x cols), rows in a fixed order: columns below split go to
+// out, those below split2 to out2 and the rest to out3 (null: not wanted).
 struct ColumnSums {
     const float* part;
-    float *out, *out2;
-    int64_t rows, cols, split;
+    float *out, *out2, *out3;
+    int64_t rows, cols, split, split2;
 };
 hipError_t launch_column_sums(const ColumnSums& c, hipStream_t s);
 hipError_t launch_fill(float* p, int64_t n, hipStream_t s);                          // zeros

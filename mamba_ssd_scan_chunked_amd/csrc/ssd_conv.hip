@@ -557,7 +557,7 @@ int ssd_conv_backward(const ssd_conv_problem_t* p, const void* x, const float* w
         cs.out2 = dbias;
         cs.split = p->channels * p->width;
         cs.rows = p->batch * s.nrun;
-        cs.cols = p->channels * (p->width + 1);
+        cs.cols = cs.split2 = p->channels * (p->width + 1);
         r = ssd::launch_column_sums(cs, st);
     }
     return done("backward", p, r);

@@ -406,7 +406,7 @@ hipError_t finish(const ssd_norm_problem_t* p, float* dweight, float* dscale, vo
     c.out2 = dscale;
     c.split = p->channels;
     c.rows = slots_of(p);
-    c.cols = p->channels * (dscale ? 2 : 1);
+    c.cols = c.split2 = p->channels * (dscale ? 2 : 1);
     return ssd::launch_column_sums(c, s);
 }
 

@@ -1,0 +1,377 @@
+// Host side of the selective scan's entry points (declared in include/ssd.h): argument
+// checks, the workspace layouts and the launches.  Every check runs before the first HIP
+// call.
+#include "ssd.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstdio>
+
+#include "selective.hpp"
+#include "ssd_host.hpp"
+
+namespace {
+
+using namespace ssd_host;
+
+constexpr int64_t kMaxDim = int64_t(1) << 31;
+constexpr int64_t kTile = 16;                // segments are whole tiles of every kernel
+
+int64_t blocks_of(const ssd_selective_problem_t* p) { return (p->channels / p->ngroups + 63) / 64; }
+
+// Segments per row.  A row's channels give batch x groups x blocks workgroups; rows are cut
+// when those do not fill the chip.  A cut costs a local pass (about the scan again without
+// its read-out), so the forward is cut only below `few` workgroups; the backward needs its
+// local pass for the checkpoints anyway.
+struct Segments {
+    int64_t n, len;
+};
+Segments segments_of(const ssd_selective_problem_t* p, bool backward) {
+    const int64_t tiles = std::max<int64_t>(1, (p->seqlen + kTile - 1) / kTile);
+    const int64_t items = std::max<int64_t>(1, p->batch * p->ngroups * blocks_of(p));
+    int64_t n = 1;
+    if (p->segments > 0) {
+        n = p->segments;
+    } else if (backward) {
+        if (items < 2048) n = (2048 + items - 1) / items;
+        n = std::min(n, std::max<int64_t>(1, tiles / 4));
+    } else {
+        if (items < 512) n = 1280 / items;
+        n = std::min(n, std::max<int64_t>(1, tiles / 4));
+    }
+    n = std::max<int64_t>(1, std::min(n, tiles));
+    const int64_t per = (tiles + n - 1) / n;
+    return {(tiles + per - 1) / per, per * kTile};
+}
+
+int validate(const ssd_selective_problem_t* p) {
+    if (!p) return SSD_ERR_NULL_POINTER;
+    if (p->batch < 0 || p->seqlen < 0 || p->channels <= 0 || p->dstate <= 0 || p->ngroups <= 0 || p->nseqs < 0 ||
+        p->segments < 0)
+        return SSD_ERR_BAD_SHAPE;
+    if (p->batch >= kMaxDim || p->seqlen >= kMaxDim || p->channels >= kMaxDim || p->nseqs >= kMaxDim)
+        return SSD_ERR_BAD_SHAPE;
+    if (p->channels % p->ngroups != 0) return SSD_ERR_BAD_SHAPE;
+    if (p->dtype != SSD_DTYPE_BF16 && p->dtype != SSD_DTYPE_F32) return SSD_ERR_UNSUPPORTED;
+    if (p->dstate != 8 && p->dstate != 16 && p->dstate != 32 && p->dstate != 64) return SSD_ERR_UNSUPPORTED;
+    if ((p->flags & ~uint32_t(SSD_FLAG_DT_SOFTPLUS)) || p->reserved != 0) return SSD_ERR_UNSUPPORTED;
+    const int64_t gn = p->ngroups * p->dstate;
+    for (int64_t ld : {p->ldx, p->lddt, p->ldz})
+        if (ld < p->channels || ld >= kMaxDim) return SSD_ERR_BAD_SHAPE;
+    for (int64_t ld : {p->ldb, p->ldc})
+        if (ld < gn || ld >= kMaxDim) return SSD_ERR_BAD_SHAPE;
+    // element counts stay far from int64 overflow, and every launch below 2^32 threads
+    const double tokens = double(p->batch) * double(p->seqlen);
+    if (tokens * double(kMaxDim) > 4e18 && tokens * double(std::max(p->ldx, std::max(p->lddt, p->ldz))) > 4e17)
+        return SSD_ERR_BAD_SHAPE;
+    if (double(p->nseqs) * double(p->channels) * 64 > 4e17) return SSD_ERR_BAD_SHAPE;
+    const double items = double(p->batch) * double(p->ngroups) * double(blocks_of(p));
+    const double most = std::max(segments_of(p, false).n, segments_of(p, true).n);
+    if (items * most * 256 >= 4e9 || double(p->batch) * p->channels * p->dstate >= 4e9 || tokens * gn / 4 >= 4e9)
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+struct Buf {
+    const void* ptr;
+    int64_t bytes;
+};
+int check_alias(const Buf* in, int nin, const Buf* out, int nout) {
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j)
+            if (overlap(out[i].ptr, out[i].bytes, in[j].ptr, in[j].bytes)) return SSD_ERR_ALIAS;
+        for (int j = i + 1; j < nout; ++j)
+            if (overlap(out[i].ptr, out[i].bytes, out[j].ptr, out[j].bytes)) return SSD_ERR_ALIAS;
+    }
+    return SSD_OK;
+}
+
+struct SelSizes {
+    int64_t x, dt, z, b, c, y, f, a, d, state, seq, bc;
+};
+SelSizes sel_sizes(const ssd_selective_problem_t* p) {
+    SelSizes s;
+    const int64_t bt = p->batch * p->seqlen, e = elem_size(p->dtype), gn = p->ngroups * p->dstate;
+    auto span = [&](int64_t ld, int64_t cols) { return bt > 0 ? ((bt - 1) * ld + cols) * e : 0; };
+    s.x = span(p->ldx, p->channels);
+    s.dt = span(p->lddt, p->channels);
+    s.z = span(p->ldz, p->channels);
+    s.b = span(p->ldb, gn);
+    s.c = span(p->ldc, gn);
+    s.y = bt * p->channels * e;
+    s.f = bt * p->channels * 4;
+    s.bc = bt * gn * 4;
+    s.a = p->channels * p->dstate * 4;
+    s.d = p->channels * 4;
+    s.state = p->nseqs * s.a;
+    s.seq = bt * 4;
+    return s;
+}
+
+// Regions of the workspaces, in bytes from their start.
+struct ForwardSpace {
+    int64_t step, total;             // seg_state at 0
+};
+ForwardSpace forward_space(const ssd_selective_problem_t* p) {
+    const int64_t n = p->batch * (segments_of(p, false).n - 1) * p->channels;
+    ForwardSpace w;
+    w.step = align256(n * p->dstate * 4);
+    w.total = n > 0 && p->seqlen > 0 ? w.step + align256(n * 4) : 0;
+    return w;
+}
+struct BackwardSpace {
+    int64_t step, grad, ckpt, ckpt_step, part_b, part_c, sums, total;
+};
+BackwardSpace backward_space(const ssd_selective_problem_t* p) {
+    BackwardSpace w{};
+    if (p->batch == 0 || p->seqlen == 0) return w;
+    const Segments sg = segments_of(p, true);
+    const int64_t n = p->batch * (sg.n - 1) * p->channels, tile = ssd::sel_ckpt_tile();
+    const int64_t tiles = p->batch * ((p->seqlen + tile - 1) / tile) * p->channels;
+    const int64_t bc = align256(blocks_of(p) * p->batch * p->seqlen * p->ngroups * p->dstate * 4);
+    w.step = align256(n * p->dstate * 4);
+    w.grad = w.step + align256(n * 4);
+    w.ckpt = w.grad + align256(n * p->dstate * 4);
+    w.ckpt_step = w.ckpt + align256(tiles * p->dstate * 4);
+    w.part_b = w.ckpt_step + align256(tiles * 4);
+    w.part_c = w.part_b + bc;
+    w.sums = w.part_c + bc;
+    w.total = w.sums + align256(p->batch * sg.n * p->channels * (p->dstate + 2) * 4);
+    return w;
+}
+
+ssd::SelParams params_of(const ssd_selective_problem_t* p, bool backward) {
+    ssd::SelParams s{};
+    const Segments sg = segments_of(p, backward);
+    s.batch = p->batch;
+    s.T = p->seqlen;
+    s.D = p->channels;
+    s.G = p->ngroups;
+    s.nseqs = p->nseqs;
+    s.ldx = p->ldx;
+    s.lddt = p->lddt;
+    s.ldz = p->ldz;
+    s.ldb = p->ldb;
+    s.ldc = p->ldc;
+    s.seg_len = sg.len;
+    s.nseg = (int)sg.n;
+    s.per_group = (int)(p->channels / p->ngroups);
+    s.blocks = (int)blocks_of(p);
+    s.softplus = (p->flags & SSD_FLAG_DT_SOFTPLUS) ? 1 : 0;
+    return s;
+}
+
+template <typename T> T* at(void* base, int64_t off) { return reinterpret_cast<T*>(static_cast<char*>(base) + off); }
+
+int check_sequences(const ssd_selective_problem_t* p, const int32_t* seq_idx) {
+    if (!seq_idx && p->nseqs != p->batch) return SSD_ERR_BAD_SHAPE;
+    if (seq_idx && p->batch * p->seqlen > 0 && p->nseqs < 1) return SSD_ERR_BAD_SHAPE;
+    return SSD_OK;
+}
+
+int done(const char* what, const ssd_selective_problem_t* p, int64_t segs, hipError_t e) {
+    if (log_enabled())
+        std::fprintf(stderr, "[ssd] selective %s dtype=%d batch=%lld T=%lld D=%lld N=%lld G=%lld segments=%lld -> %s\n",
+                     what, p->dtype, (long long)p->batch, (long long)p->seqlen, (long long)p->channels,
+                     (long long)p->dstate, (long long)p->ngroups, (long long)segs, hipGetErrorString(e));
+    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssd_selective_workspace_size(const ssd_selective_problem_t* p) {
+    return validate(p) == SSD_OK ? (size_t)forward_space(p).total : 0;
+}
+size_t ssd_selective_backward_workspace_size(const ssd_selective_problem_t* p) {
+    return validate(p) == SSD_OK ? (size_t)backward_space(p).total : 0;
+}
+
+int ssd_selective_forward(const ssd_selective_problem_t* p, const void* x, const void* dt, const float* dt_bias,
+                          const float* A_log, const void* B, const void* C, const float* D, const void* z,
+                          const float* init_state, const int32_t* seq_idx, void* y, float* final_state, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    const int v = validate(p);
+    if (v != SSD_OK) return v;
+    const bool empty = p->batch == 0 || p->seqlen == 0;
+    if (!A_log || (!empty && (!x || !dt || !B || !C || !y))) return SSD_ERR_NULL_POINTER;
+    const int q = check_sequences(p, seq_idx);
+    if (q != SSD_OK) return q;
+    const ForwardSpace ws = forward_space(p);
+    if (ws.total > 0 && !workspace) return SSD_ERR_WORKSPACE;
+    const uintptr_t e = (uintptr_t)elem_size(p->dtype);
+    if (misaligned(x, e) || misaligned(dt, e) || misaligned(B, e) || misaligned(C, e) || misaligned(z, e) ||
+        misaligned(y, e) || misaligned(dt_bias, 4) || misaligned(A_log, 4) || misaligned(D, 4) ||
+        misaligned(init_state, 4) || misaligned(seq_idx, 4) || misaligned(final_state, 4) || misaligned(workspace, 256))
+        return SSD_ERR_ALIGNMENT;
+    if ((int64_t)workspace_bytes < ws.total) return SSD_ERR_WORKSPACE;
+    const SelSizes s = sel_sizes(p);
+    const Buf in[] = {{x, s.x}, {dt, s.dt}, {dt_bias, s.d}, {A_log, s.a}, {B, s.b}, {C, s.c}, {D, s.d}, {z, s.z},
+                      {init_state, s.state}, {seq_idx, s.seq}};
+    const Buf out[] = {{y, s.y}, {final_state, s.state}, {workspace, ws.total}};
+    const int a = check_alias(in, 10, out, 3);
+    if (a != SSD_OK) return a;
+    const int d = check_device();
+    if (d != SSD_OK) return d;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (empty) {
+        // no token: each row's final state is its initial state
+        if (seq_idx || !final_state) return SSD_OK;
+        return done("forward", p, 0, ssd::launch_copy(final_state, init_state, s.state / 4, st));
+    }
+    ssd::SelParams k = params_of(p, false);
+    k.x = x;
+    k.dt = dt;
+    k.B = B;
+    k.C = C;
+    k.z = z;
+    k.A_log = A_log;
+    k.skip = D;
+    k.dt_bias = dt_bias;
+    k.init = init_state;
+    k.seq_idx = seq_idx;
+    k.y = y;
+    k.fin = final_state;
+    hipError_t r = hipSuccess;
+    if (k.nseg > 1) {
+        k.seg_state = at<float>(workspace, 0);
+        k.seg_step = at<float>(workspace, ws.step);
+        r = ssd::launch_sel_local(k, p->dtype, p->dstate, false, st);
+        if (r == hipSuccess) r = ssd::launch_sel_combine(k, p->dstate, false, st);
+    }
+    if (r == hipSuccess) r = ssd::launch_sel_forward(k, p->dtype, p->dstate, st);
+    return done("forward", p, k.nseg, r);
+}
+
+int ssd_selective_step(const ssd_selective_problem_t* p, const void* x, const void* dt, const float* dt_bias,
+                       const float* A_log, const void* B, const void* C, const float* D, const void* z,
+                       const float* state, float* state_out, void* y, void* stream) {
+    if (!p) return SSD_ERR_NULL_POINTER;
+    if (p->seqlen != 1 || p->nseqs != p->batch) return SSD_ERR_BAD_SHAPE;
+    const int v = validate(p);
+    if (v != SSD_OK) return v;
+    if (!A_log || (p->batch > 0 && (!x || !dt || !B || !C || !state || !state_out || !y))) return SSD_ERR_NULL_POINTER;
+    const uintptr_t e = (uintptr_t)elem_size(p->dtype);
+    if (misaligned(x, e) || misaligned(dt, e) || misaligned(B, e) || misaligned(C, e) || misaligned(z, e) ||
+        misaligned(y, e) || misaligned(dt_bias, 4) || misaligned(A_log, 4) || misaligned(D, 4) || misaligned(state, 4) ||
+        misaligned(state_out, 4))
+        return SSD_ERR_ALIGNMENT;
+    const SelSizes s = sel_sizes(p);
+    const Buf in[] = {{x, s.x}, {dt, s.dt}, {dt_bias, s.d}, {A_log, s.a}, {B, s.b}, {C, s.c}, {D, s.d}, {z, s.z},
+                      {state == state_out ? nullptr : state, s.state}};
+    const Buf out[] = {{y, s.y}, {state_out, s.state}};
+    const int a = check_alias(in, 9, out, 2);
+    if (a != SSD_OK) return a;
+    const int d = check_device();
+    if (d != SSD_OK) return d;
+    if (p->batch == 0) return SSD_OK;
+    ssd::SelParams k = params_of(p, false);
+    k.x = x;
+    k.dt = dt;
+    k.B = B;
+    k.C = C;
+    k.z = z;
+    k.A_log = A_log;
+    k.skip = D;
+    k.dt_bias = dt_bias;
+    k.init = state;
+    k.fin = state_out;
+    k.y = y;
+    return done("step", p, 1, ssd::launch_sel_step(k, p->dtype, p->dstate, static_cast<hipStream_t>(stream)));
+}
+
+int ssd_selective_backward(const ssd_selective_problem_t* p, const void* x, const void* dt, const float* dt_bias,
+                           const float* A_log, const void* B, const void* C, const float* D, const void* z,
+                           const float* init_state, const int32_t* seq_idx, const float* dy, const float* dfinal,
+                           float* dx, float* ddt, float* dA_log, float* dB, float* dC, float* dD, float* dz,
+                           float* dinit, float* ddt_bias, void* workspace, size_t workspace_bytes, void* stream) {
+    const int v = validate(p);
+    if (v != SSD_OK) return v;
+    const bool empty = p->batch == 0 || p->seqlen == 0;
+    if (!A_log || !dA_log || (!empty && (!x || !dt || !B || !C || !dy || !dx || !ddt || !dB || !dC || (z && !dz))))
+        return SSD_ERR_NULL_POINTER;
+    const int q = check_sequences(p, seq_idx);
+    if (q != SSD_OK) return q;
+    const BackwardSpace ws = backward_space(p);
+    if (ws.total > 0 && !workspace) return SSD_ERR_WORKSPACE;
+    const uintptr_t e = (uintptr_t)elem_size(p->dtype);
+    if (misaligned(x, e) || misaligned(dt, e) || misaligned(B, e) || misaligned(C, e) || misaligned(z, e) ||
+        misaligned(dt_bias, 4) || misaligned(A_log, 4) || misaligned(D, 4) || misaligned(init_state, 4) ||
+        misaligned(seq_idx, 4) || misaligned(dy, 4) || misaligned(dfinal, 4) || misaligned(dx, 4) || misaligned(ddt, 4) ||
+        misaligned(dA_log, 4) || misaligned(dB, 4) || misaligned(dC, 4) || misaligned(dD, 4) || misaligned(dz, 4) ||
+        misaligned(dinit, 4) || misaligned(ddt_bias, 4) || misaligned(workspace, 256))
+        return SSD_ERR_ALIGNMENT;
+    if ((int64_t)workspace_bytes < ws.total) return SSD_ERR_WORKSPACE;
+    const SelSizes s = sel_sizes(p);
+    const Buf in[] = {{x, s.x}, {dt, s.dt}, {dt_bias, s.d}, {A_log, s.a}, {B, s.b}, {C, s.c}, {D, s.d}, {z, s.z},
+                      {init_state, s.state}, {seq_idx, s.seq}, {dy, s.f}, {dfinal, s.state}};
+    const Buf out[] = {{dx, s.f}, {ddt, s.f}, {dA_log, s.a}, {dB, s.bc}, {dC, s.bc}, {dD, s.d}, {z ? dz : nullptr, s.f},
+                       {dinit, s.state}, {ddt_bias, s.d}, {workspace, ws.total}};
+    const int a = check_alias(in, 12, out, 10);
+    if (a != SSD_OK) return a;
+    const int d = check_device();
+    if (d != SSD_OK) return d;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t r = hipSuccess;
+    if (empty) {
+        // no token: nothing reaches the parameters, and each row's final state is its initial state
+        r = ssd::launch_fill(dA_log, s.a / 4, st);
+        if (r == hipSuccess) r = ssd::launch_fill(dD, s.d / 4, st);
+        if (r == hipSuccess) r = ssd::launch_fill(ddt_bias, s.d / 4, st);
+        if (r == hipSuccess && dinit) r = ssd::launch_copy(dinit, seq_idx ? nullptr : dfinal, s.state / 4, st);
+        return done("backward", p, 0, r);
+    }
+    ssd::SelParams k = params_of(p, true);
+    k.x = x;
+    k.dt = dt;
+    k.B = B;
+    k.C = C;
+    k.z = z;
+    k.A_log = A_log;
+    k.skip = D;
+    k.dt_bias = dt_bias;
+    k.init = init_state;
+    k.seq_idx = seq_idx;
+    k.dy = dy;
+    k.dfin = dfinal;
+    k.dx = dx;
+    k.ddt = ddt;
+    k.dz = dz;
+    k.dinit = dinit;
+    k.seg_state = at<float>(workspace, 0);
+    k.seg_step = at<float>(workspace, ws.step);
+    k.seg_grad = at<float>(workspace, ws.grad);
+    k.ckpt = at<float>(workspace, ws.ckpt);
+    k.ckpt_step = at<float>(workspace, ws.ckpt_step);
+    k.part_b = at<float>(workspace, ws.part_b);
+    k.part_c = at<float>(workspace, ws.part_c);
+    k.part_sums = at<float>(workspace, ws.sums);
+    // ids that do not occur keep a zero gradient
+    if (seq_idx && dinit) r = ssd::launch_fill(dinit, s.state / 4, st);
+    if (r == hipSuccess) r = ssd::launch_sel_local(k, p->dtype, p->dstate, true, st);
+    if (k.nseg > 1) {
+        if (r == hipSuccess) r = ssd::launch_sel_combine(k, p->dstate, false, st);
+        if (r == hipSuccess) r = ssd::launch_sel_reverse_local(k, p->dtype, p->dstate, st);
+        if (r == hipSuccess) r = ssd::launch_sel_combine(k, p->dstate, true, st);
+    }
+    if (r == hipSuccess) r = ssd::launch_sel_reverse(k, p->dtype, p->dstate, st);
+    if (r == hipSuccess) r = ssd::launch_sel_group_sums(k, p->dstate, dB, dC, st);
+    if (r == hipSuccess) {
+        ssd::ColumnSums c{};
+        c.part = k.part_sums;
+        c.out = dA_log;
+        c.out2 = dD;
+        c.out3 = ddt_bias;
+        c.rows = p->batch * k.nseg;
+        c.cols = p->channels * (p->dstate + 2);
+        c.split = p->channels * p->dstate;
+        c.split2 = c.split + p->channels;
+        r = ssd::launch_column_sums(c, st);
+    }
+    return done("backward", p, k.nseg, r);
+}
+
+}  // extern "C"

@@ -81,3 +81,54 @@ def residual(x, res, w, scale, eps):
 
 def leaves(*ts):
     return [None if t is None else t.detach().double().clone().requires_grad_() for t in ts]
+
+
+def scan(x, dt, A_log, B, C, D, z, init, bias, soft, lens):
+    """(y, final) of the selective scan in the inputs' own precision; B, C (b,T,G,N)."""
+    b, T, Dc = x.shape
+    G, N = B.shape[2:]
+    A = -torch.exp(A_log)
+    rep = Dc // G
+    ys, final = [], []
+    for k, (r, t0, n) in enumerate(sequences(b, T, lens)):
+        h = init[k]
+        for t in range(t0, t0 + n):
+            step = dt[r, t] + bias
+            if soft:
+                step = torch.logaddexp(step, torch.zeros_like(step))
+            Bt, Ct = B[r, t].repeat_interleave(rep, 0), C[r, t].repeat_interleave(rep, 0)
+            h = torch.exp(step[:, None] * A) * h + (step * x[r, t])[:, None] * Bt
+            y = (h * Ct).sum(-1) + D * x[r, t]
+            ys.append(y * silu(z[r, t]) if z is not None else y)
+        final.append(h)
+    return torch.stack(ys).view(b, T, Dc), torch.stack(final)
+
+
+def scan_sizes(x, dt, A_log, B, C, D, z, init, bias, soft, lens):
+    """The same map over magnitudes, with every factor's derivative counted positive: its
+    values and autograd gradients are the sums of magnitudes that the scan's are sums of.
+    x, B, C, D, z and init come as leaves holding magnitudes (z: the gate's value is taken
+    from ``z`` itself, which may be signed)."""
+    b, T, Dc = x.shape
+    G, N = B.shape[2:]
+    A = torch.exp(A_log)
+    rep = Dc // G
+    ys, final = [], []
+    for k, (r, t0, n) in enumerate(sequences(b, T, lens)):
+        h = init[k]
+        for t in range(t0, t0 + n):
+            step = dt[r, t] + bias
+            if soft:
+                step = torch.logaddexp(step, torch.zeros_like(step))
+            arg = step[:, None] * A
+            decay = torch.exp(-arg).detach() * torch.exp(arg - arg.detach())
+            Bt, Ct = B[r, t].repeat_interleave(rep, 0), C[r, t].repeat_interleave(rep, 0)
+            h = decay * h + (step * x[r, t])[:, None] * Bt
+            y = (h * Ct).sum(-1) + D * x[r, t]
+            if z is not None:
+                zt = z[r, t]
+                # silu's slope is below 1.1
+                y = y * (silu(zt).abs().detach() + 1.1 * (zt - zt.detach()))
+            ys.append(y)
+        final.append(h)
+    return torch.stack(ys).view(b, T, Dc), torch.stack(final)

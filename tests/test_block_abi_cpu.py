@@ -153,6 +153,86 @@ def test_binding_refuses_on_the_cpu():
     for f in (lambda: ssd.causal_conv(x, w), lambda: ssd.causal_conv_backward(x, w, x),
               lambda: ssd.causal_conv_step(x[:, 0], w, None, torch.zeros(1, 3, 8)), lambda: ssd.gated_norm(x, x, w[:, 0]),
               lambda: ssd.gated_norm_backward(x, x, w[:, 0], x), lambda: ssd.residual_norm(x, x, w[:, 0]),
-              lambda: ssd.residual_norm_backward(x, x, w[:, 0], x)):
+              lambda: ssd.residual_norm_backward(x, x, w[:, 0], x), lambda: ssd.selective_scan(x, x, w, x, x),
+              lambda: ssd.selective_scan_backward(x, x, w, x, x, x), lambda: ssd.selective_step(x, x, w, x, x, None, x)):
         with pytest.raises(ValueError):
             f()
+
+
+SEL = dict(batch=2, seqlen=40, channels=64, dstate=16)
+SF = ["x", "dt", "dt_bias", "A_log", "B", "C", "D", "z", "init", "seq", "y", "final"]
+SB = ["x", "dt", "dt_bias", "A_log", "B", "C", "D", "z", "init", "seq", "dy", "dfinal", "dx", "ddt", "dA_log", "dB", "dC",
+      "dD", "dz", "dinit", "ddt_bias"]
+SS = ["x", "dt", "dt_bias", "A_log", "B", "C", "D", "z", "state", "state_out", "y"]
+NONE = (None, 0)
+
+
+def sel(**kw):
+    return ssd.selective_problem(**{**SEL, **kw})
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=-1), 2), (dict(seqlen=-1), 2), (dict(channels=0), 2), (dict(dstate=0), 2), (dict(ngroups=0), 2),
+    (dict(ngroups=3), 2), (dict(segments=-1), 2), (dict(nseqs=-1), 2), (dict(seqlen=1 << 31), 2),
+    (dict(ldx=63), 2), (dict(lddt=63), 2), (dict(ldz=63), 2), (dict(ldb=15), 2), (dict(ldc=15), 2), (dict(ldx=1 << 31), 2),
+    (dict(dtype=3), 3), (dict(dstate=12), 3), (dict(dstate=128), 3),
+    (dict(batch=1 << 20, nseqs=1 << 20, channels=1 << 14), 3),
+])
+def test_selective_problems(kw, code):
+    assert call("ssd_selective_forward", sel(**kw), SF, NONE) == code
+    assert ssd.selective_workspace_size(sel(**kw)) == 0 and ssd.selective_backward_workspace_size(sel(**kw)) == 0
+
+
+def test_selective_workspaces():
+    assert ssd.selective_workspace_size(sel(seqlen=16)) == 0                       # one tile: not cut
+    assert ssd.selective_workspace_size(sel(batch=8, channels=8192)) == 0          # the channels fill the chip
+    p = sel(seqlen=100, segments=3)                                                # 7 tiles of 16: segments of 3
+    assert ssd.selective_workspace_size(p) == 2 * 2 * 64 * 16 * 4 + 2 * 2 * 64 * 4
+    assert ssd.selective_backward_workspace_size(sel(seqlen=0)) == 0
+    n = ssd.selective_workspace_size(p)
+    p.nseqs = 3
+    assert call("ssd_selective_forward", p, SF, NONE) == 5
+    assert call("ssd_selective_forward", p, SF, (A + 40 * STEP, n - 1)) == 5
+    assert call("ssd_selective_forward", p, SF, (A + 40 * STEP + 16, n)) == 4
+    assert call("ssd_selective_forward", p, SF, (A, n), y=A + 30 * STEP, x=A) == 6
+
+
+def test_selective_pointers():
+    p = sel(nseqs=3, segments=1)
+    for k in ("x", "dt", "A_log", "B", "C", "y"):
+        assert call("ssd_selective_forward", p, SF, NONE, **{k: None}) == 1
+    assert call("ssd_selective_forward", p, SF, NONE, seq=None) == 2
+    assert call("ssd_selective_forward", sel(nseqs=0, segments=1), SF, NONE) == 2
+    for k in ("x", "dt", "B", "C", "z", "y"):
+        assert call("ssd_selective_forward", p, SF, NONE, **{k: A + 30 * STEP + 1}) == 4
+    same = A + 30 * STEP
+    for a, b in (("y", "x"), ("y", "dt"), ("y", "z"), ("y", "B"), ("final", "init"), ("final", "A_log"), ("y", "final")):
+        assert call("ssd_selective_forward", p, SF, NONE, **{a: same, b: same}) == 6
+    p.flags = 1
+    assert call("ssd_selective_forward", p, SF, NONE) == 3
+    p.flags, p.reserved = 0, 1
+    assert call("ssd_selective_forward", p, SF, NONE) == 3
+
+
+def test_selective_backward_pointers():
+    p = sel(nseqs=3)
+    n = ssd.selective_backward_workspace_size(p)
+    ws = (A + 40 * STEP, n)
+    assert n > 0
+    for k in ("x", "dt", "A_log", "B", "C", "dy", "dx", "ddt", "dA_log", "dB", "dC", "dz"):
+        assert call("ssd_selective_backward", p, SB, ws, **{k: None}) == 1
+    assert call("ssd_selective_backward", p, SB, NONE) == 5
+    assert call("ssd_selective_backward", p, SB, (A + 40 * STEP, n - 1)) == 5
+    same = A + 30 * STEP
+    for a, b in (("dx", "dy"), ("ddt", "dt"), ("dB", "B"), ("dC", "dB"), ("dinit", "dfinal"), ("dz", "z"), ("dA_log", "A_log"),
+                 ("dD", "D"), ("ddt_bias", "dt_bias")):
+        assert call("ssd_selective_backward", p, SB, ws, **{a: same, b: same}) == 6
+
+
+def test_selective_step_pointers():
+    p = sel(seqlen=1)
+    assert call("ssd_selective_step", sel(), SS) == 2 and call("ssd_selective_step", sel(seqlen=1, nseqs=3), SS) == 2
+    for k in ("x", "dt", "A_log", "B", "C", "state", "state_out", "y"):
+        assert call("ssd_selective_step", p, SS, **{k: None}) == 1
+    assert call("ssd_selective_step", p, SS, state_out=A + 9 * STEP + 4) == 6
+    assert call("ssd_selective_step", p, SS, y=A + 9 * STEP) == 6
