@@ -37,17 +37,19 @@ template <int V, typename T> __device__ inline void store_f32(T* p, const float*
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// e^v from the hardware exp2.  The product v log2(e) is split into its rounded value
-// and its remainder, so the error does not grow with |v| (about 1e-7 relative).
-__device__ inline float exp_accurate(float v) {
+// e^v for |v| <= 100 from the hardware exp2.  The product v log2(e) is taken as its rounded
+// value and its remainder, so the error does not grow with |v| (about 1e-7 relative).
+__device__ inline float exp_small(float v) {
     const float hi = v * kLog2e;
-    // an infinite or huge product has no remainder (inf - inf)
-    const float lo = fabsf(hi) < 1e30f ? fmaf(v, 1.925963033500012e-08f, fmaf(v, kLog2e, -hi)) : 0.f;
-    return __builtin_amdgcn_exp2f(hi) * fmaf(lo, kLn2, 1.f);
+    const float lo = fmaf(v, 1.925963033500012e-08f, fmaf(v, kLog2e, -hi));
+    const float e = __builtin_amdgcn_exp2f(hi);
+    return fmaf(e * lo, kLn2, e);
 }
 
-// 1 / (1 + e^-v).  e^-v overflows to inf below v = -88, which gives 0 as it should.
-__device__ inline float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + exp_accurate(-v)); }
+// 1 / (1 + e^-v); v beyond +-100 counts as +-100 (1 and 4e-44).
+__device__ inline float sigmoid(float v) {
+    return __builtin_amdgcn_rcpf(1.f + exp_small(__builtin_amdgcn_fmed3f(-v, -100.f, 100.f)));
+}
 __device__ inline float silu(float v) { return v * sigmoid(v); }
 // The gate of a result that is rounded to T: bf16 takes the plain exp2, whose argument's
 // rounding (2^-24 |v| log2 e) is far below bf16's half step and saves six instructions.
@@ -59,13 +61,22 @@ template <> __device__ inline float silu_for<__bf16>(float v) {
 __device__ inline float silu_slope(float v, float s) { return s * (1.f + v * (1.f - s)); }
 
 // log(1 + e^v) = max(v, 0) + log1p(t), t = e^-|v|, with Goldberg's correction for the
-// rounding of 1 + t ("What every computer scientist should know about floating-point
-// arithmetic", 1991, theorem 4).
-__device__ inline float softplus(float v) {
-    const float t = exp_accurate(-fabsf(v));
-    const float u = 1.f + t;
+// rounding of u = 1 + t ("What every computer scientist should know about floating-point
+// arithmetic", 1991, theorem 4).  The clamp of |v| leaves a NaN in place.
+struct SoftplusParts {
+    float value, t, u;
+};
+__device__ inline SoftplusParts softplus_parts(float v) {
+    const float a = fabsf(v), t = exp_small(a > 100.f ? -100.f : -a), u = 1.f + t;
     const float l = u == 1.f ? t : __builtin_amdgcn_logf(u) * kLn2 * (t * __builtin_amdgcn_rcpf(u - 1.f));
-    return fmaxf(v, 0.f) + l;
+    return {fmaxf(v, 0.f) + l, t, u};
+}
+__device__ inline float softplus(float v) { return softplus_parts(v).value; }
+// softplus and its slope, sigmoid(v) = 1 / u or t / u
+__device__ inline float softplus_slope(float v, float* slope) {
+    const SoftplusParts s = softplus_parts(v);
+    *slope = (v >= 0.f ? 1.f : s.t) * __builtin_amdgcn_rcpf(s.u);
+    return s.value;
 }
 
 // Sequence id of a token, clamped so that a bad id cannot leave the per-sequence arrays.

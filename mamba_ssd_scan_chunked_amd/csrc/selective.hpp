@@ -14,6 +14,8 @@
 #include "block_common.hpp"
 #include "ssd.h"
 
+#include <type_traits>
+
 namespace ssd {
 
 struct SelParams {
@@ -33,18 +35,27 @@ struct SelParams {
     int64_t batch, T, D, G, nseqs, ldx, lddt, ldz, ldb, ldc;
     int64_t seg_len;                 // tokens per segment, a multiple of every tile length
     int nseg;
-    int per_group, blocks;           // channels per group, 64-channel blocks per group
+    int per_group, blocks;           // channels per group, workgroups' channel blocks per group
     int softplus;
 };
 
-// What a workgroup works on: 64 channels of one group (a lane each; lanes past the group's
-// last channel repeat it and store nothing), one segment of one row.
-struct SelPlace {
-    int64_t b, d, g, t0, t1;
-    int seg, block;
-    bool mine;                       // the lane's channel exists
+// How a workgroup shares out its channels and states.  A wave's 64 lanes are M = 64 / CH
+// groups of CH channels, each group with S of the states, and W waves hold the rest:
+// N = W M S.  CH is 16, 32 or 64, so the 16 lanes of a DPP row always hold the same
+// states: B and C are kept one state per lane of the row and reach the multiply-adds as
+// row broadcasts, without an instruction or an LDS read per state of their own.
+template <int N, int CH_, int S_> struct SelShape {
+    static constexpr int CH = CH_, S = S_, M = 64 / CH, W = N / (M * S), THREADS = 64 * W;
+    static_assert(W * M * S == N && S <= 16 && CH >= 16, "shape");
 };
-__device__ inline SelPlace sel_place(const SelParams& p, int lane) {
+
+// What a workgroup works on: CH channels of one group (lanes past the group's last channel
+// repeat it and store nothing), one segment of one row.
+struct SelPlace {
+    int64_t b, d0, g, t0, t1;        // d0: first channel
+    int seg, block, chans;           // chans: channels of d0 .. that exist, up to CH
+};
+template <int CH> __device__ inline SelPlace sel_place(const SelParams& p) {
     SelPlace q;
     const unsigned per_row = (unsigned)(p.G * p.blocks);
     const unsigned cb = blockIdx.x % per_row, rest = blockIdx.x / per_row;
@@ -52,13 +63,43 @@ __device__ inline SelPlace sel_place(const SelParams& p, int lane) {
     q.b = rest / p.nseg;
     q.g = cb / p.blocks;
     q.block = (int)(cb % p.blocks);
-    const int c = q.block * 64 + lane;
-    q.mine = c < p.per_group;
-    q.d = q.g * p.per_group + (q.mine ? c : p.per_group - 1);
+    q.d0 = q.g * p.per_group + q.block * CH;
+    q.chans = p.per_group - q.block * CH < CH ? p.per_group - q.block * CH : CH;
     q.t0 = q.seg * p.seg_len;
     q.t1 = q.t0 + p.seg_len < p.T ? q.t0 + p.seg_len : p.T;
     return q;
 }
+
+// The value that lane I of every row of 16 lanes holds (a DPP operand of the instruction
+// that uses it).
+template <int I> __device__ inline float row_lane(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x150 + I, 0xf, 0xf, true));
+}
+template <int N, typename F, int I = 0> __device__ inline void static_for(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        static_for<N, F, I + 1>(static_cast<F&&>(f));
+    }
+}
+
+// One value per (token, channel) of a tile of TQ tokens, loaded by the workgroup's threads:
+// pair j of a thread is token (tid + THREADS j) / CH, channel (tid + THREADS j) % CH.
+// Offsets are bytes from the tile's first token, so that a load is a scalar base and a
+// 32-bit offset; in a ragged tile the tokens past the end repeat the last one.
+template <typename T, int J, int CH, int THREADS> struct TileLoad {
+    unsigned off[J];
+    __device__ inline void place(int64_t ld, int chans, int tokens) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int k = threadIdx.x + THREADS * j, c = k % CH, i = k / CH;
+            off[j] = (unsigned)(((unsigned)ld * (unsigned)(i < tokens ? i : tokens - 1) + (c < chans ? c : chans - 1)) * sizeof(T));
+        }
+    }
+    __device__ inline void load(const T* base, T (&v)[J]) const {
+#pragma unroll
+        for (int j = 0; j < J; ++j) v[j] = *(const T*)((const char*)base + off[j]);
+    }
+};
 
 // Bits i of the tile's tokens t .. t+TQ-1: a sequence starts at (ends after) the token.
 struct SeqBits {
@@ -83,6 +124,11 @@ template <int S> __device__ inline void load_decay(const SelParams& p, int64_t d
 }
 __device__ inline float decay(float step, float A2) { return __builtin_amdgcn_exp2f(step * A2); }
 
+// S values of LDS at 4 S bytes' alignment.
+template <int S> struct alignas(S < 4 ? 4 * S : 16) States {
+    float v[S];
+};
+
 template <int S> __device__ inline void load_state(const float* p, float (&h)[S]) {
     if (p) {
         load_f32<S>(p, h);
@@ -92,8 +138,13 @@ template <int S> __device__ inline void load_state(const float* p, float (&h)[S]
     }
 }
 
-// Step size before and after its map.
-__device__ inline float step_of(float raw, int soft) { return soft ? softplus(raw) : raw; }
+// Step sizes from dt + bias, in place.
+template <int J> __device__ inline void map_steps(float (&v)[J], int soft) {
+    if (soft) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) v[j] = softplus(v[j]);
+    }
+}
 
 int64_t sel_ckpt_tile();             // tokens per checkpoint of the backward pass
 hipError_t launch_sel_local(const SelParams& p, int dtype, int64_t N, bool checkpoints, hipStream_t s);

@@ -1,111 +1,145 @@
 // Selective scan, forward: the scan over whole rows or segments, the local pass and the
 // combine of split rows, and the single-token step.
 #include "selective.hpp"
+#include <cstdlib>
 
 namespace ssd {
 
 // ---------------------------------------------------------------- scan
-// One workgroup per 64 channels: N/S waves, each with the same 64 channels and S of the
-// states, so B and C are the same for every lane of a wave and y needs one sum over
-// waves per (token, channel) instead of one over lanes.  Per tile of TQ tokens:
-//   - the waves share out the tokens, each computing step and step x once (LDS), and
-//     stage B and C as fp32; the next tile's loads are issued then;
+// Per tile of TQ tokens:
+//   - the threads share out the tile's (token, channel) pairs, each computing step and
+//     step x once (LDS), and stage B and C as fp32; the next tile's loads are issued then;
 //   - every wave walks the tile with its states and leaves its part of y in LDS;
-//   - the waves share out the tokens again, sum the parts, add D x, gate and store.
-template <typename T, int N, int S, bool SEQ> __global__ __launch_bounds__(64 * (N / S))
-void sel_forward_kernel(SelParams p) {
-    constexpr int W = N / S, TQ = 16, J = TQ / W, E = TQ * N / (64 * W);
-    static_assert(TQ % W == 0 && E * 64 * W == TQ * N, "tile shape");
-    __shared__ float2 su[TQ][64];
-    __shared__ float Bs[TQ][N], Cs[TQ][N];
+//   - the threads share out the pairs again, sum the parts, add D x, gate and store.
+template <typename T, int N, int CH, int S, bool SEQ>
+__global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_forward_kernel(SelParams p) {
+    using Sh = SelShape<N, CH, S>;
+    constexpr int W = Sh::W, TH = Sh::THREADS, TQ = 16, J = TQ * CH / TH, E = (TQ * N + TH - 1) / TH;
+    static_assert(J * TH == TQ * CH, "tile shape");
+    __shared__ float2 su[TQ][CH];
+    __shared__ float4 Bs[TQ / 4][N];                             // four tokens of a state together
+    __shared__ __attribute__((aligned(16))) float Cs[TQ][N];     // a token's states together
     __shared__ float part[W][TQ][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const SelPlace q = sel_place(p, lane);
+    const SelPlace q = sel_place<CH>(p);
+    const int ch = lane % CH, n0 = (w * Sh::M + lane / CH) * S;
+    const bool mine = ch < q.chans;
+    const int64_t d = q.d0 + (mine ? ch : q.chans - 1);
     const int32_t* ids = SEQ ? p.seq_idx + q.b * p.T : nullptr;
-    const T* x = (const T*)p.x + q.b * p.T * p.ldx + q.d;
-    const T* dt = (const T*)p.dt + q.b * p.T * p.lddt + q.d;
-    const T* z = p.z ? (const T*)p.z + q.b * p.T * p.ldz + q.d : nullptr;
-    const T* B = (const T*)p.B + q.b * p.T * p.ldb + q.g * N;
-    const T* C = (const T*)p.C + q.b * p.T * p.ldc + q.g * N;
-    T* y = (T*)p.y + q.b * p.T * p.D + q.d;
-    const float bias = p.dt_bias ? p.dt_bias[q.d] : 0.f, skip = p.skip ? p.skip[q.d] : 0.f;
+    const int64_t tok = q.b * p.T + q.t0;
+    const T* x = (const T*)p.x + tok * p.ldx + q.d0;
+    const T* dt = (const T*)p.dt + tok * p.lddt + q.d0;
+    const T* z = (const T*)(p.z ? p.z : p.x) + tok * p.ldz + q.d0;      // (without a gate: read and not used)
+    const T* B = (const T*)p.B + tok * p.ldb + q.g * N;
+    const T* C = (const T*)p.C + tok * p.ldc + q.g * N;
+    T* y = (T*)p.y + tok * p.D + q.d0;
+    // of the thread's own pairs: their channel is the same for every j when CH divides TH
+    const int pc = threadIdx.x % CH;
+    const int64_t pd = q.d0 + (pc < q.chans ? pc : q.chans - 1);
+    const float bias = p.dt_bias ? p.dt_bias[pd] : 0.f, skip = p.skip ? p.skip[pd] : 0.f;
     float A2[S], h[S];
-    load_decay<S>(p, q.d, N, w * S, A2);
-    const int64_t state = q.d * N + w * S, DN = p.D * N;
+    load_decay<S>(p, d, N, n0, A2);
+    const int64_t state = d * N + n0, DN = p.D * N;
     load_state<S>(q.seg > 0 ? p.seg_state + (q.b * (p.nseg - 1) + q.seg - 1) * DN + state
                             : (p.init && !SEQ ? p.init + q.b * DN + state : nullptr), h);
 
+    TileLoad<T, J, CH, TH> lx, ld, lz, ly;
+    TileLoad<T, E, N, TH> lb, lc;
+    ly.place(p.D, q.chans, TQ);
     T xr[J], dr[J], zr[J], br[E], cr[E];
-    auto load = [&](int64_t t) {
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int64_t i = t + w + W * j;
-            if (i < q.t1) {
-                xr[j] = x[i * p.ldx];
-                dr[j] = dt[i * p.lddt];
-                if (z) zr[j] = z[i * p.ldz];
-            }
+    auto load = [&](int64_t left) {
+        if (left < TQ || left == q.t1 - q.t0) {
+            const int tokens = left < TQ ? (int)left : TQ;
+            lx.place(p.ldx, q.chans, tokens);
+            ld.place(p.lddt, q.chans, tokens);
+            lz.place(p.ldz, q.chans, tokens);
+            lb.place(p.ldb, N, tokens);
+            lc.place(p.ldc, N, tokens);
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int k = threadIdx.x + 64 * W * e;
-            const int64_t i = t + k / N;
-            if (i < q.t1) {
-                br[e] = B[i * p.ldb + k % N];
-                cr[e] = C[i * p.ldc + k % N];
-            }
-        }
+        lx.load(x, xr);
+        ld.load(dt, dr);
+        if (p.z) lz.load(z, zr);
+        lb.load(B, br);
+        lc.load(C, cr);
+        x += TQ * p.ldx;
+        dt += TQ * p.lddt;
+        z += TQ * p.ldz;
+        B += TQ * p.ldb;
+        C += TQ * p.ldc;
     };
-    load(q.t0);
-    for (int64_t t = q.t0; t < q.t1; t += TQ) {
-        float xk[J], zk[J];
+    load(q.t1 - q.t0);
+    for (int64_t t = q.t0; t < q.t1; t += TQ, y += TQ * p.D) {
+        const int tokens = q.t1 - t < TQ ? (int)(q.t1 - t) : TQ;
+        float xk[J], zk[J], step[J];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
+            xk[j] = (float)xr[j];
+            zk[j] = (float)zr[j];
+            step[j] = (float)dr[j] + bias;
+        }
+        map_steps(step, p.softplus);
+        if (tokens < TQ) {
             // tokens past the end take a zero step: they leave the state as it is
-            const bool in = t + w + W * j < q.t1;
-            const float step = in ? step_of((float)dr[j] + bias, p.softplus) : 0.f;
-            xk[j] = in ? (float)xr[j] : 0.f;
-            zk[j] = in && z ? (float)zr[j] : 0.f;
-            su[w + W * j][lane] = make_float2(step, step * xk[j]);
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if ((threadIdx.x + TH * j) / CH >= tokens) step[j] = xk[j] = 0.f;
         }
 #pragma unroll
+        for (int j = 0; j < J; ++j) su[(threadIdx.x + TH * j) / CH][pc] = make_float2(step[j], step[j] * xk[j]);
+#pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int k = threadIdx.x + 64 * W * e;
-            const bool in = t + k / N < q.t1;
-            Bs[k / N][k % N] = in ? (float)br[e] : 0.f;
-            Cs[k / N][k % N] = in ? (float)cr[e] : 0.f;
+            const int k = threadIdx.x + TH * e, i = k / N;
+            if (E * TH > TQ * N && i >= TQ) continue;
+            (&Bs[i / 4][k % N].x)[i % 4] = i < tokens ? (float)br[e] : 0.f;
+            Cs[i][k % N] = i < tokens ? (float)cr[e] : 0.f;
         }
         __syncthreads();
-        if (t + TQ < q.t1) load(t + TQ);
+        if (t + TQ < q.t1) load(q.t1 - t - TQ);
         SeqBits bits{};
         if (SEQ) bits = seq_bits<TQ>(ids, t, p.T, lane);
 #pragma unroll
-        for (int i = 0; i < TQ; ++i) {
-            if (SEQ && (bits.starts >> i & 1))
-                load_state<S>(p.init ? p.init + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, h);
-            const float2 s = su[i][lane];
-            float acc = 0.f;
+        for (int i4 = 0; i4 < TQ / 4; ++i4) {
+            const float4 B4 = Bs[i4][n0 + lane % S];
+            const float Bv[4] = {B4.x, B4.y, B4.z, B4.w};
 #pragma unroll
-            for (int n = 0; n < S; ++n) {
-                h[n] = fmaf(decay(s.x, A2[n]), h[n], s.y * Bs[i][w * S + n]);
-                acc = fmaf(h[n], Cs[i][w * S + n], acc);
+            for (int k = 0; k < 4; ++k) {
+                const int i = 4 * i4 + k;
+                if (SEQ && (bits.starts >> i & 1))
+                    load_state<S>(p.init ? p.init + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, h);
+                const float2 s = su[i][ch];
+                const States<S> Cv = *(const States<S>*)&Cs[i][n0];
+                float acc = 0.f;
+                static_for<S>([&](auto I) {
+                    constexpr int n = decltype(I)::value;
+                    h[n] = fmaf(decay(s.x, A2[n]), h[n], row_lane<n>(Bv[k]) * s.y);
+                    acc = fmaf(Cv.v[n], h[n], acc);
+                });
+                part[w][i][lane] = acc;
+                if (SEQ && (bits.ends >> i & 1) && p.fin && mine)
+                    store_f32<S>(p.fin + clamp_id(ids[t + i], p.nseqs) * DN + state, h);
             }
-            part[w][i][lane] = acc;
-            if (SEQ && (bits.ends >> i & 1) && p.fin && q.mine)
-                store_f32<S>(p.fin + clamp_id(ids[t + i], p.nseqs) * DN + state, h);
         }
         __syncthreads();
+        float out[J];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int i = w + W * j;
-            float out = skip * xk[j];
+            out[j] = skip * xk[j];
 #pragma unroll
-            for (int k = 0; k < W; ++k) out += part[k][i][lane];
-            if (z) out *= silu_for<T>(zk[j]);
-            if (q.mine && t + i < q.t1) y[(t + i) * p.D] = (T)out;
+            for (int v = 0; v < W; ++v)
+#pragma unroll
+                for (int g = 0; g < Sh::M; ++g) out[j] += part[v][(threadIdx.x + TH * j) / CH][g * CH + pc];
+        }
+        if (p.z) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) out[j] *= silu_for<T>(zk[j]);
+        }
+        if (pc < q.chans) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (tokens == TQ || (threadIdx.x + TH * j) / CH < tokens) *(T*)((char*)y + ly.off[j]) = (T)out[j];
         }
     }
-    if (!SEQ && q.seg == p.nseg - 1 && p.fin && q.mine) store_f32<S>(p.fin + q.b * DN + state, h);
+    if (!SEQ && q.seg == p.nseg - 1 && p.fin && mine) store_f32<S>(p.fin + q.b * DN + state, h);
 }
 
 // ---------------------------------------------------------------- local pass of split rows
@@ -114,80 +148,105 @@ void sel_forward_kernel(SelParams p) {
 // decay exp(A sum) is what an incoming state would still weigh; infinite when a sequence
 // starts inside, so that nothing comes through.  For the backward pass (CKPT) the same
 // two are also kept before every tile.  A wave on its own, up to 16 states a lane.
-template <typename T, int N, int S, bool SEQ, bool CKPT, int TQ> __global__ __launch_bounds__(64 * (N / S))
-void sel_local_kernel(SelParams p) {
-    constexpr int W = N / S, J = TQ / W, E = TQ * N / (64 * W);
-    static_assert(TQ % W == 0 && E * 64 * W == TQ * N, "tile shape");
-    __shared__ float2 su[TQ][64];
-    __shared__ float Bs[TQ][N];
+template <typename T, int N, int CH, int S, bool SEQ, bool CKPT, int TQ>
+__global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_local_kernel(SelParams p) {
+    using Sh = SelShape<N, CH, S>;
+    constexpr int TH = Sh::THREADS, J = TQ * CH / TH, E = (TQ * N + TH - 1) / TH;
+    static_assert(J * TH == TQ * CH, "tile shape");
+    __shared__ float2 su[TQ][CH];
+    __shared__ float4 Bs[TQ / 4][N];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const SelPlace q = sel_place(p, lane);
+    const SelPlace q = sel_place<CH>(p);
     if (!CKPT && q.seg == p.nseg - 1) return;
+    const int ch = lane % CH, n0 = (w * Sh::M + lane / CH) * S;
+    const bool mine = ch < q.chans;
+    const int64_t d = q.d0 + (mine ? ch : q.chans - 1);
     const int32_t* ids = SEQ ? p.seq_idx + q.b * p.T : nullptr;
-    const T* x = (const T*)p.x + q.b * p.T * p.ldx + q.d;
-    const T* dt = (const T*)p.dt + q.b * p.T * p.lddt + q.d;
-    const T* B = (const T*)p.B + q.b * p.T * p.ldb + q.g * N;
-    const float bias = p.dt_bias ? p.dt_bias[q.d] : 0.f;
+    const int64_t tok = q.b * p.T + q.t0;
+    const T* x = (const T*)p.x + tok * p.ldx + q.d0;
+    const T* dt = (const T*)p.dt + tok * p.lddt + q.d0;
+    const T* B = (const T*)p.B + tok * p.ldb + q.g * N;
+    const int pc = threadIdx.x % CH;
+    const float bias = p.dt_bias ? p.dt_bias[q.d0 + (pc < q.chans ? pc : q.chans - 1)] : 0.f;
     float A2[S], h[S], sum = 0.f;
-    load_decay<S>(p, q.d, N, w * S, A2);
-    const int64_t state = q.d * N + w * S, DN = p.D * N;
+    load_decay<S>(p, d, N, n0, A2);
+    const int64_t state = d * N + n0, DN = p.D * N;
     load_state<S>(q.seg == 0 && p.init && !SEQ ? p.init + q.b * DN + state : nullptr, h);
+    TileLoad<T, J, CH, TH> lx, ld;
+    TileLoad<T, E, N, TH> lb;
     T xr[J], dr[J], br[E];
-    auto load = [&](int64_t t) {
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int64_t i = t + w + W * j;
-            if (i < q.t1) {
-                xr[j] = x[i * p.ldx];
-                dr[j] = dt[i * p.lddt];
-            }
+    auto load = [&](int64_t left) {
+        if (left < TQ || left == q.t1 - q.t0) {
+            const int tokens = left < TQ ? (int)left : TQ;
+            lx.place(p.ldx, q.chans, tokens);
+            ld.place(p.lddt, q.chans, tokens);
+            lb.place(p.ldb, N, tokens);
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int k = threadIdx.x + 64 * W * e;
-            if (t + k / N < q.t1) br[e] = B[(t + k / N) * p.ldb + k % N];
-        }
+        lx.load(x, xr);
+        ld.load(dt, dr);
+        lb.load(B, br);
+        x += TQ * p.ldx;
+        dt += TQ * p.lddt;
+        B += TQ * p.ldb;
     };
-    load(q.t0);
+    load(q.t1 - q.t0);
     const int64_t tiles = (p.T + TQ - 1) / TQ;
     for (int64_t t = q.t0; t < q.t1; t += TQ) {
-        if (CKPT && q.mine) {
-            const int64_t at = (q.b * tiles + t / TQ) * p.D + q.d;
-            store_f32<S>(p.ckpt + at * N + w * S, h);
-            if (w == 0) p.ckpt_step[at] = sum;
+        const int tokens = q.t1 - t < TQ ? (int)(q.t1 - t) : TQ;
+        if (CKPT && mine) {
+            const int64_t at = (q.b * tiles + t / TQ) * p.D + d;
+            store_f32<S>(p.ckpt + at * N + n0, h);
+            if (n0 == 0) p.ckpt_step[at] = sum;
         }
         __syncthreads();
+        float step[J], xk[J];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const bool in = t + w + W * j < q.t1;
-            const float step = in ? step_of((float)dr[j] + bias, p.softplus) : 0.f;
-            su[w + W * j][lane] = make_float2(step, in ? step * (float)xr[j] : 0.f);
+            xk[j] = (float)xr[j];
+            step[j] = (float)dr[j] + bias;
+        }
+        map_steps(step, p.softplus);
+        if (tokens < TQ) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if ((threadIdx.x + TH * j) / CH >= tokens) step[j] = xk[j] = 0.f;
         }
 #pragma unroll
+        for (int j = 0; j < J; ++j) su[(threadIdx.x + TH * j) / CH][pc] = make_float2(step[j], step[j] * xk[j]);
+#pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int k = threadIdx.x + 64 * W * e;
-            Bs[k / N][k % N] = t + k / N < q.t1 ? (float)br[e] : 0.f;
+            const int k = threadIdx.x + TH * e, i = k / N;
+            if (E * TH > TQ * N && i >= TQ) continue;
+            (&Bs[i / 4][k % N].x)[i % 4] = i < tokens ? (float)br[e] : 0.f;
         }
         __syncthreads();
-        if (t + TQ < q.t1) load(t + TQ);
+        if (t + TQ < q.t1) load(q.t1 - t - TQ);
         SeqBits bits{};
         if (SEQ) bits = seq_bits<TQ>(ids, t, p.T, lane);
 #pragma unroll
-        for (int i = 0; i < TQ; ++i) {
-            if (SEQ && (bits.starts >> i & 1)) {
-                load_state<S>(p.init ? p.init + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, h);
-                sum = __builtin_inff();
-            }
-            const float2 s = su[i][lane];
-            sum += s.x;
+        for (int i4 = 0; i4 < TQ / 4; ++i4) {
+            const float4 B4 = Bs[i4][n0 + lane % S];
+            const float Bv[4] = {B4.x, B4.y, B4.z, B4.w};
 #pragma unroll
-            for (int n = 0; n < S; ++n) h[n] = fmaf(decay(s.x, A2[n]), h[n], s.y * Bs[i][w * S + n]);
+            for (int k = 0; k < 4; ++k) {
+                const int i = 4 * i4 + k;
+                if (SEQ && (bits.starts >> i & 1)) {
+                    load_state<S>(p.init ? p.init + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, h);
+                    sum = __builtin_inff();
+                }
+                const float2 s = su[i][ch];
+                sum += s.x;
+                static_for<S>([&](auto I) {
+                    constexpr int n = decltype(I)::value;
+                    h[n] = fmaf(decay(s.x, A2[n]), h[n], row_lane<n>(Bv[k]) * s.y);
+                });
+            }
         }
     }
-    if (q.seg < p.nseg - 1 && q.mine) {
-        const int64_t at = (q.b * (p.nseg - 1) + q.seg) * p.D + q.d;
-        store_f32<S>(p.seg_state + at * N + w * S, h);
-        if (w == 0) p.seg_step[at] = sum;
+    if (q.seg < p.nseg - 1 && mine) {
+        const int64_t at = (q.b * (p.nseg - 1) + q.seg) * p.D + d;
+        store_f32<S>(p.seg_state + at * N + n0, h);
+        if (n0 == 0) p.seg_step[at] = sum;
     }
 }
 
@@ -241,7 +300,9 @@ template <typename T, int N> __global__ __launch_bounds__(256) void sel_step_ker
     load_f32<4>((const T*)p.B + b * p.ldb + g * N + 4 * c, Bv);
     load_f32<4>((const T*)p.C + b * p.ldc + g * N + 4 * c, Cv);
     const float x = (float)((const T*)p.x)[b * p.ldx + d];
-    const float step = step_of((float)((const T*)p.dt)[b * p.lddt + d] + (p.dt_bias ? p.dt_bias[d] : 0.f), p.softplus);
+    float steps[1] = {(float)((const T*)p.dt)[b * p.lddt + d] + (p.dt_bias ? p.dt_bias[d] : 0.f)};
+    map_steps(steps, p.softplus);
+    const float step = steps[0];
     float acc = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -259,18 +320,34 @@ template <typename T, int N> __global__ __launch_bounds__(256) void sel_step_ker
 }
 
 // ---------------------------------------------------------------- launches
-static unsigned sel_grid(const SelParams& p) { return (unsigned)(p.batch * p.nseg * p.G * p.blocks); }
-
-template <typename T, int N> static void forward_n(const SelParams& p, hipStream_t s) {
-    constexpr int S = N <= 16 ? 4 : N / 4;
-    if (p.seq_idx) hipLaunchKernelGGL((sel_forward_kernel<T, N, S, true>), dim3(sel_grid(p)), dim3(64 * (N / S)), 0, s, p);
-    else hipLaunchKernelGGL((sel_forward_kernel<T, N, S, false>), dim3(sel_grid(p)), dim3(64 * (N / S)), 0, s, p);
+// `blocks` counts the workgroups' channel blocks, which differ between kernels.
+static SelParams blocked(const SelParams& p, int ch) {
+    SelParams q = p;
+    q.blocks = (p.per_group + ch - 1) / ch;
+    return q;
 }
-template <typename T, int N, bool CKPT> static void local_n(const SelParams& p, hipStream_t s) {
-    constexpr int S = N <= 16 ? N : 16, TQ = CKPT ? 8 : 16;
-    const dim3 grid(sel_grid(p)), block(64 * (N / S));
-    if (p.seq_idx) hipLaunchKernelGGL((sel_local_kernel<T, N, S, true, CKPT, TQ>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((sel_local_kernel<T, N, S, false, CKPT, TQ>), grid, block, 0, s, p);
+static dim3 sel_grid(const SelParams& p) { return dim3((unsigned)(p.batch * p.nseg * p.G * p.blocks)); }
+
+template <typename T, int N, int CH, int S> static void forward_shape(const SelParams& p0, hipStream_t s) {
+    const SelParams p = blocked(p0, CH);
+    const dim3 block(SelShape<N, CH, S>::THREADS);
+    if (p.seq_idx) hipLaunchKernelGGL((sel_forward_kernel<T, N, CH, S, true>), sel_grid(p), block, 0, s, p);
+    else hipLaunchKernelGGL((sel_forward_kernel<T, N, CH, S, false>), sel_grid(p), block, 0, s, p);
+}
+template <typename T, int N> static void forward_n(const SelParams& p, hipStream_t s) {
+    static const int v = getenv("SEL_V") ? atoi(getenv("SEL_V")) : 0;
+    if (v == 0) forward_shape<T, N, 32, N / 8>(p, s);
+    if (v == 1) forward_shape<T, N, 16, N / 4>(p, s);
+    if (v == 2) forward_shape<T, N, 64, (N < 16 ? N : 16)>(p, s);
+    if (v == 3) forward_shape<T, N, 64, N / 4>(p, s);
+    if (v == 4) forward_shape<T, N, 16, (N / 8)>(p, s);
+}
+template <typename T, int N, bool CKPT> static void local_n(const SelParams& p0, hipStream_t s) {
+    constexpr int CH = 64, S = N <= 16 ? N : 16, TQ = CKPT ? 8 : 16;
+    const SelParams p = blocked(p0, CH);
+    const dim3 block(SelShape<N, CH, S>::THREADS);
+    if (p.seq_idx) hipLaunchKernelGGL((sel_local_kernel<T, N, CH, S, true, CKPT, TQ>), sel_grid(p), block, 0, s, p);
+    else hipLaunchKernelGGL((sel_local_kernel<T, N, CH, S, false, CKPT, TQ>), sel_grid(p), block, 0, s, p);
 }
 
 int64_t sel_ckpt_tile() { return 8; }

@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstdio>
+#include <cstdlib>
 
 #include "selective.hpp"
 #include "ssd_host.hpp"
@@ -35,10 +36,12 @@ Segments segments_of(const ssd_selective_problem_t* p, bool backward) {
     if (p->segments > 0) {
         n = p->segments;
     } else if (backward) {
-        if (items < 2048) n = (2048 + items - 1) / items;
+        static const int64_t slots = getenv("SEL_SLOTS") ? atoi(getenv("SEL_SLOTS")) : 768;
+        n = slots / items;
         n = std::min(n, std::max<int64_t>(1, tiles / 4));
     } else {
-        if (items < 512) n = 1280 / items;
+        static const int64_t fs = getenv("SEL_FS") ? atoi(getenv("SEL_FS")) : 2048;
+        if (items < 256) n = fs / items;
         n = std::min(n, std::max<int64_t>(1, tiles / 4));
     }
     n = std::max<int64_t>(1, std::min(n, tiles));

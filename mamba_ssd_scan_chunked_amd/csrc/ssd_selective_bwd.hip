@@ -16,41 +16,35 @@ constexpr int kTile = 8;
 
 // Sums over the 64 lanes of S values at once: at every level a lane keeps half of the
 // values and hands the other half to its partner (swaps of 32 and 16 lanes, then lanes of
-// a row), so S values cost about 2 S instructions instead of 6 S.  Returns, in every lane,
-// the sum of value sum_index<S>(lane).
+// a row), so four values cost 10 instructions and eight 24, instead of 24 and 48.  Returns,
+// in every lane, the sum of value sum_index<S>(lane).
 template <int CTRL> __device__ inline float dpp_mov(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
-template <int S> __device__ inline int sum_index(int lane) {
-    return S == 16 ? (lane >> 2 & 1) + 2 * (lane >> 3 & 1) + 4 * (lane >> 4) : (lane >> 3 & 1) + 2 * (lane >> 4);
-}
+template <int S> __device__ inline int sum_index(int lane) { return S == 4 ? lane >> 4 : (lane >> 3 & 1) + 2 * (lane >> 4); }
 template <int S> __device__ inline float lane_sums(const float (&v)[S], int lane) {
-    static_assert(S == 8 || S == 16, "values");
-    constexpr int H = S / 2, Q = S / 4;
-    float a[H], b[Q];
+    static_assert(S == 4 || S == 8, "values");
+    float a[S / 2], b[S / 4];
 #pragma unroll
-    for (int k = 0; k < H; ++k) {
-        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[k]), __float_as_uint(v[k + H]), false, false);
+    for (int k = 0; k < S / 2; ++k) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[k]), __float_as_uint(v[k + S / 2]), false, false);
         a[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
     }
 #pragma unroll
-    for (int k = 0; k < Q; ++k) {
-        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a[k]), __float_as_uint(a[k + Q]), false, false);
+    for (int k = 0; k < S / 4; ++k) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a[k]), __float_as_uint(a[k + S / 4]), false, false);
         b[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
     }
-    const bool hi = lane & 8;
-    float c[Q / 2];
-#pragma unroll
-    for (int k = 0; k < Q / 2; ++k) c[k] = (hi ? b[k + Q / 2] : b[k]) + dpp_mov<0x140>(hi ? b[k] : b[k + Q / 2]);   // row_mirror
     float s;
-    if constexpr (S == 16) {
-        const bool up = lane & 4;
-        s = (up ? c[1] : c[0]) + dpp_mov<0x141>(up ? c[0] : c[1]);                       // row_half_mirror
+    if constexpr (S == 8) {
+        const bool hi = lane & 8;
+        s = (hi ? b[1] : b[0]) + dpp_mov<0x140>(hi ? b[0] : b[1]);        // row_mirror
     } else {
-        s = c[0] + dpp_mov<0x141>(c[0]);
+        s = b[0] + dpp_mov<0x140>(b[0]);
     }
-    s += dpp_mov<0xb1>(s);      // quad_perm 1,0,3,2
-    s += dpp_mov<0x4e>(s);      // quad_perm 2,3,0,1
+    s += dpp_mov<0x141>(s);                                               // row_half_mirror
+    s += dpp_mov<0xb1>(s);                                                // quad_perm 1,0,3,2
+    s += dpp_mov<0x4e>(s);                                                // quad_perm 2,3,0,1
     return s;
 }
 
@@ -59,121 +53,167 @@ __device__ inline int64_t last_tile(const SelPlace& q) { return q.t0 + (q.t1 - q
 // ---------------------------------------------------------------- local reverse pass
 // For rows in segments: what a segment's own tokens send back through its first token, q
 // from zero (the row's last segment: from dfinal).  Kept for segments 1 .. nseg-1.
-template <typename T, int N, int S, bool SEQ> __global__ __launch_bounds__(64 * (N / S))
-void sel_reverse_local_kernel(SelParams p) {
-    constexpr int W = N / S, TQ = kTile, J = TQ / W, E = TQ * N / (64 * W);
-    __shared__ float2 sg[TQ][64];
-    __shared__ float Cs[TQ][N];
+template <typename T, int N, int CH, int S, bool SEQ>
+__global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_reverse_local_kernel(SelParams p) {
+    using Sh = SelShape<N, CH, S>;
+    constexpr int TQ = kTile, TH = Sh::THREADS, J = TQ * CH / TH, E = (TQ * N + TH - 1) / TH;
+    static_assert(J * TH == TQ * CH, "tile shape");
+    __shared__ float2 sg[TQ][CH];
+    __shared__ float4 Cs[TQ / 4][N];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const SelPlace q = sel_place(p, lane);
+    const SelPlace q = sel_place<CH>(p);
     if (q.seg == 0) return;
+    const int ch = lane % CH, n0 = (w * Sh::M + lane / CH) * S, pc = threadIdx.x % CH;
+    const bool mine = ch < q.chans;
+    const int64_t d = q.d0 + (mine ? ch : q.chans - 1);
     const int32_t* ids = SEQ ? p.seq_idx + q.b * p.T : nullptr;
-    const T* dt = (const T*)p.dt + q.b * p.T * p.lddt + q.d;
-    const T* z = p.z ? (const T*)p.z + q.b * p.T * p.ldz + q.d : nullptr;
-    const T* C = (const T*)p.C + q.b * p.T * p.ldc + q.g * N;
-    const float* dy = p.dy + q.b * p.T * p.D + q.d;
-    const float bias = p.dt_bias ? p.dt_bias[q.d] : 0.f;
+    const float bias = p.dt_bias ? p.dt_bias[q.d0 + (pc < q.chans ? pc : q.chans - 1)] : 0.f;
     float A2[S], grad[S];
-    load_decay<S>(p, q.d, N, w * S, A2);
-    const int64_t state = q.d * N + w * S, DN = p.D * N;
+    load_decay<S>(p, d, N, n0, A2);
+    const int64_t state = d * N + n0, DN = p.D * N;
     load_state<S>(!SEQ && q.seg == p.nseg - 1 && p.dfin ? p.dfin + q.b * DN + state : nullptr, grad);
-    for (int64_t t = last_tile(q); t >= q.t0; t -= TQ) {
+    const int64_t first = last_tile(q), tok = q.b * p.T + first;
+    const T* dt = (const T*)p.dt + tok * p.lddt + q.d0;
+    const T* z = (const T*)(p.z ? p.z : p.dt) + tok * p.ldz + q.d0;       // (without a gate: not read)
+    const T* C = (const T*)p.C + tok * p.ldc + q.g * N;
+    const float* dy = p.dy + tok * p.D + q.d0;
+    TileLoad<T, J, CH, TH> ld, lz;
+    TileLoad<float, J, CH, TH> ly;
+    TileLoad<T, E, N, TH> lc;
+    T dr[J], zr[J], cr[E];
+    float yr[J];
+    auto load = [&](int64_t t) {
+        if (t == first || t + TQ == first) {
+            const int tokens = q.t1 - t < TQ ? (int)(q.t1 - t) : TQ;
+            ld.place(p.lddt, q.chans, tokens);
+            lz.place(p.ldz, q.chans, tokens);
+            ly.place(p.D, q.chans, tokens);
+            lc.place(p.ldc, N, tokens);
+        }
+        ld.load(dt, dr);
+        if (p.z) lz.load(z, zr);
+        ly.load(dy, yr);
+        lc.load(C, cr);
+        dt -= TQ * p.lddt;
+        z -= TQ * p.ldz;
+        C -= TQ * p.ldc;
+        dy -= TQ * p.D;
+    };
+    load(first);
+    for (int64_t t = first; t >= q.t0; t -= TQ) {
+        const int tokens = q.t1 - t < TQ ? (int)(q.t1 - t) : TQ;
+        __syncthreads();
         float step[J], g[J];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int64_t i = t + w + W * j;
-            step[j] = g[j] = 0.f;
-            if (i < q.t1) {
-                step[j] = step_of((float)dt[i * p.lddt] + bias, p.softplus);
-                g[j] = dy[i * p.D] * (z ? silu((float)z[i * p.ldz]) : 1.f);
-            }
+            step[j] = (float)dr[j] + bias;
+            g[j] = yr[j];
         }
-        float cv[E];
+        map_steps(step, p.softplus);
+        if (p.z) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) g[j] *= silu((float)zr[j]);
+        }
+        if (tokens < TQ) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if ((threadIdx.x + TH * j) / CH >= tokens) step[j] = g[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) sg[(threadIdx.x + TH * j) / CH][pc] = make_float2(step[j], g[j]);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int k = threadIdx.x + 64 * W * e;
-            cv[e] = t + k / N < q.t1 ? (float)C[(t + k / N) * p.ldc + k % N] : 0.f;
+            const int k = threadIdx.x + TH * e, i = k / N;
+            if (E * TH > TQ * N && i >= TQ) continue;
+            (&Cs[i / 4][k % N].x)[i % 4] = i < tokens ? (float)cr[e] : 0.f;
         }
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < J; ++j) sg[w + W * j][lane] = make_float2(step[j], g[j]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int k = threadIdx.x + 64 * W * e;
-            Cs[k / N][k % N] = cv[e];
-        }
-        __syncthreads();
+        if (t > q.t0) load(t - TQ);
         SeqBits bits{};
         if (SEQ) bits = seq_bits<TQ>(ids, t, p.T, lane);
 #pragma unroll
-        for (int i = TQ - 1; i >= 0; --i) {
-            if (SEQ && (bits.ends >> i & 1))
-                load_state<S>(p.dfin ? p.dfin + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, grad);
-            const float2 s = sg[i][lane];
+        for (int i4 = TQ / 4 - 1; i4 >= 0; --i4) {
+            const float4 C4 = Cs[i4][n0 + lane % S];
+            const float Cv[4] = {C4.x, C4.y, C4.z, C4.w};
 #pragma unroll
-            for (int n = 0; n < S; ++n) grad[n] = decay(s.x, A2[n]) * fmaf(s.y, Cs[i][w * S + n], grad[n]);
-            // what leaves a sequence's first token goes to its initial state, not to the segment before
-            if (SEQ && (bits.starts >> i & 1)) load_state<S>(nullptr, grad);
+            for (int k = 3; k >= 0; --k) {
+                const int i = 4 * i4 + k;
+                if (SEQ && (bits.ends >> i & 1))
+                    load_state<S>(p.dfin ? p.dfin + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, grad);
+                const float2 s = sg[i][ch];
+                static_for<S>([&](auto I) {
+                    constexpr int n = decltype(I)::value;
+                    grad[n] = decay(s.x, A2[n]) * (grad[n] + row_lane<n>(Cv[k]) * s.y);
+                });
+                // what leaves a sequence's first token goes to its initial state, not to the segment before
+                if (SEQ && (bits.starts >> i & 1)) load_state<S>(nullptr, grad);
+            }
         }
     }
-    if (q.mine) store_f32<S>(p.seg_grad + (q.b * (p.nseg - 1) + q.seg - 1) * DN + state, grad);
+    if (mine) store_f32<S>(p.seg_grad + (q.b * (p.nseg - 1) + q.seg - 1) * DN + state, grad);
 }
 
 // ---------------------------------------------------------------- reverse pass
-// One workgroup per 64 channels and segment, N/S waves with S <= 16 states each (one wave
-// for N <= 16: no partial sums over waves, no barriers).
-template <typename T, int N, int S, bool SEQ> __global__ __launch_bounds__(64 * (N / S), 2)
-void sel_reverse_kernel(SelParams p) {
-    constexpr int W = N / S, TQ = kTile, J = TQ / W, E = TQ * N / (64 * W), HOLD = 64 / S;   // HOLD tokens per store
-    __shared__ float2 su[TQ][64];
-    __shared__ float gs[TQ][64];
-    __shared__ float Bs[TQ][N], Cs[TQ][N];
-    __shared__ float parts[3][W][TQ][64];                        // of y, d(step x) and dstep
+// One workgroup per 64 channels and segment, N/S waves with S states each (four: the
+// tile's p then takes 32 registers and five waves fit a SIMD).  The sums over states of a
+// token (for y, d(step x) and dstep) meet in LDS, the sums over channels (for dB and dC)
+// within the wave and then, over channel blocks, in part_b and part_c.
+template <typename T, int N, int S, bool SEQ>
+__global__ __launch_bounds__((SelShape<N, 64, S>::THREADS)) void sel_reverse_kernel(SelParams p) {
+    constexpr int CH = 64, W = N / S, TH = 64 * W, TQ = kTile, J = TQ / W;
+    static_assert(W * J == TQ && TH >= TQ * N, "tile shape");     // a B and a C value per thread
+    __shared__ float2 su[TQ][CH];
+    __shared__ float gs[TQ][CH];
+    __shared__ float4 Bs[TQ / 4][N], Cs[TQ / 4][N];
+    __shared__ float parts[3][W][TQ][CH];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const SelPlace q = sel_place(p, lane);
+    const SelPlace q = sel_place<CH>(p);
+    const bool mine = lane < q.chans;
+    const int64_t d = q.d0 + (mine ? lane : q.chans - 1);
+    const int n0 = w * S;
     const int32_t* ids = SEQ ? p.seq_idx + q.b * p.T : nullptr;
-    const T* x = (const T*)p.x + q.b * p.T * p.ldx + q.d;
-    const T* dt = (const T*)p.dt + q.b * p.T * p.lddt + q.d;
-    const T* z = p.z ? (const T*)p.z + q.b * p.T * p.ldz + q.d : nullptr;
-    const T* B = (const T*)p.B + q.b * p.T * p.ldb + q.g * N;
-    const T* C = (const T*)p.C + q.b * p.T * p.ldc + q.g * N;
-    const int64_t row = q.b * p.T * p.D + q.d;
-    const float bias = p.dt_bias ? p.dt_bias[q.d] : 0.f, skip = p.skip ? p.skip[q.d] : 0.f;
+    const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.skip ? p.skip[d] : 0.f;
     float A2[S], grad[S], dA[S], sum_skip = 0.f, sum_bias = 0.f;
-    load_decay<S>(p, q.d, N, w * S, A2);
-    const int64_t state = q.d * N + w * S, DN = p.D * N;
+    load_decay<S>(p, d, N, n0, A2);
+    const int64_t state = d * N + n0, DN = p.D * N;
     load_state<S>(q.seg < p.nseg - 1 ? p.seg_grad + (q.b * (p.nseg - 1) + q.seg) * DN + state
                                      : (!SEQ && p.dfin ? p.dfin + q.b * DN + state : nullptr), grad);
 #pragma unroll
     for (int n = 0; n < S; ++n) dA[n] = 0.f;
     const float* before = q.seg > 0 ? p.seg_state + (q.b * (p.nseg - 1) + q.seg - 1) * DN + state : nullptr;
     const int64_t tiles = (p.T + TQ - 1) / TQ;
-    // part_b and part_c: (block, batch, T, G, N); the lane's value and token of a store
-    const int64_t part0 = (((int64_t)q.block * p.batch + q.b) * p.T * p.G + q.g) * N + w * S + sum_index<S>(lane);
-    const int hold = lane % HOLD;
-    for (int64_t t = last_tile(q); t >= q.t0; t -= TQ) {
-        float xk[J], zk[J], dyk[J], slope[J], bv[E], cv[E], h[S];
+
+    const int64_t first = last_tile(q), tok = q.b * p.T + first;
+    const T* x = (const T*)p.x + tok * p.ldx + q.d0;
+    const T* dt = (const T*)p.dt + tok * p.lddt + q.d0;
+    const T* z = (const T*)(p.z ? p.z : p.x) + tok * p.ldz + q.d0;        // (without a gate: not read)
+    const T* B = (const T*)p.B + tok * p.ldb + q.g * N;
+    const T* C = (const T*)p.C + tok * p.ldc + q.g * N;
+    int64_t row = tok * p.D + d;                                          // of the tile in dy, dx, ddt, dz
+    const float* dy = p.dy + tok * p.D + q.d0;
+    const unsigned col = mine ? lane : q.chans - 1;
+    // part_b and part_c: (block, batch, T, G, N); after lane_sums 64 / S lanes hold a value
+    // each, and keep that of token `hold` of the tile
+    const int hold = lane % (64 / S);
+    int64_t part = ((((int64_t)q.block * p.batch + q.b) * p.T + first + hold) * p.G + q.g) * N + n0 + sum_index<S>(lane);
+    for (int64_t t = first; t >= q.t0; t -= TQ) {
+        const int tokens = q.t1 - t < TQ ? (int)(q.t1 - t) : TQ;
+        T xr[J], dr[J], zr[J];
+        float dyk[J], h[S];
+        // a wave's tokens are its own, so their rows are scalar addresses
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int64_t i = t + w + W * j;
-            xk[j] = zk[j] = dyk[j] = slope[j] = 0.f;
-            if (i < q.t1) {
-                xk[j] = (float)x[i * p.ldx];
-                slope[j] = (float)dt[i * p.lddt] + bias;
-                dyk[j] = p.dy[row + i * p.D];
-                if (z) zk[j] = (float)z[i * p.ldz];
-            }
+            const int i = w + W * j < tokens ? w + W * j : tokens - 1;
+            xr[j] = (x + i * p.ldx)[col];
+            dr[j] = (dt + i * p.lddt)[col];
+            if (p.z) zr[j] = (z + i * p.ldz)[col];
+            dyk[j] = (dy + i * p.D)[col];
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int k = threadIdx.x + 64 * W * e;
-            const bool in = t + k / N < q.t1;
-            bv[e] = in ? (float)B[(t + k / N) * p.ldb + k % N] : 0.f;
-            cv[e] = in ? (float)C[(t + k / N) * p.ldc + k % N] : 0.f;
-        }
+        const int bi = threadIdx.x / N, bt = bi < tokens ? bi : tokens - 1;       // (threads past the tile repeat it)
+        const T br = B[bt * p.ldb + threadIdx.x % N], cr = C[bt * p.ldc + threadIdx.x % N];
         {
-            const int64_t at = (q.b * tiles + t / TQ) * p.D + q.d;
-            load_f32<S>(p.ckpt + at * N + w * S, h);
+            const int64_t at = (q.b * tiles + t / TQ) * p.D + d;
+            load_f32<S>(p.ckpt + at * N + n0, h);
             if (before) {
                 const float sum = p.ckpt_step[at];
                 float in[S];
@@ -184,21 +224,43 @@ void sel_reverse_kernel(SelParams p) {
                 }
             }
         }
+        float xk[J], zk[J], sz[J], slope[J], step[J], g[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            xk[j] = (float)xr[j];
+            step[j] = (float)dr[j] + bias;
+            g[j] = dyk[j];
+            slope[j] = 1.f;
+        }
+        if (p.softplus) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) step[j] = softplus_slope(step[j], &slope[j]);
+        }
+        if (p.z) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                zk[j] = (float)zr[j];
+                sz[j] = sigmoid(zk[j]);
+                g[j] *= zk[j] * sz[j];
+            }
+        }
+        if (tokens < TQ) {
+            // tokens past the end: a zero step leaves the state and its gradient as they are
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (w + W * j >= tokens) step[j] = xk[j] = g[j] = 0.f;
+        }
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const bool in = t + w + W * j < q.t1;
-            const float raw = slope[j], step = in ? step_of(raw, p.softplus) : 0.f;
             // lanes without a channel of their own add nothing to dB and dC
-            su[w + W * j][lane] = make_float2(step, q.mine ? step * xk[j] : 0.f);
-            gs[w + W * j][lane] = q.mine ? dyk[j] * (z ? silu(zk[j]) : 1.f) : 0.f;
-            slope[j] = p.softplus ? sigmoid(raw) : 1.f;
+            su[w + W * j][lane] = make_float2(step[j], mine ? step[j] * xk[j] : 0.f);
+            gs[w + W * j][lane] = mine ? g[j] : 0.f;
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int k = threadIdx.x + 64 * W * e;
-            Bs[k / N][k % N] = bv[e];
-            Cs[k / N][k % N] = cv[e];
+        if (TH == TQ * N || bi < TQ) {
+            const int n = threadIdx.x % N;
+            (&Bs[bi / 4][n].x)[bi % 4] = bi < tokens ? (float)br : 0.f;
+            (&Cs[bi / 4][n].x)[bi % 4] = bi < tokens ? (float)cr : 0.f;
         }
         __syncthreads();
         SeqBits bits{};
@@ -206,55 +268,70 @@ void sel_reverse_kernel(SelParams p) {
 
         float pr[TQ][S], held = 0.f;
 #pragma unroll
-        for (int i = 0; i < TQ; ++i) {
-            if (SEQ && (bits.starts >> i & 1))
-                load_state<S>(p.init ? p.init + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, h);
-            const float2 s = su[i][lane];
-            const float g = gs[i][lane];
-            float acc = 0.f, v[S];
+        for (int i4 = 0; i4 < TQ / 4; ++i4) {
+            const float4 B4 = Bs[i4][n0 + lane % S], C4 = Cs[i4][n0 + lane % S];
+            const float Bv[4] = {B4.x, B4.y, B4.z, B4.w}, Cv[4] = {C4.x, C4.y, C4.z, C4.w};
 #pragma unroll
-            for (int n = 0; n < S; ++n) {
-                pr[i][n] = decay(s.x, A2[n]) * h[n];
-                h[n] = fmaf(s.y, Bs[i][w * S + n], pr[i][n]);
-                acc = fmaf(h[n], Cs[i][w * S + n], acc);
-                v[n] = g * h[n];
+            for (int k = 0; k < 4; ++k) {
+                const int i = 4 * i4 + k;
+                if (SEQ && (bits.starts >> i & 1))
+                    load_state<S>(p.init ? p.init + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, h);
+                const float2 s = su[i][lane];
+                const float g = gs[i][lane];
+                float acc = 0.f, v[S];
+                static_for<S>([&](auto I) {
+                    constexpr int n = decltype(I)::value;
+                    pr[i][n] = decay(s.x, A2[n]) * h[n];
+                    h[n] = pr[i][n] + row_lane<n>(Bv[k]) * s.y;
+                    acc += row_lane<n>(Cv[k]) * h[n];
+                    v[n] = g * h[n];
+                });
+                parts[0][w][i][lane] = acc;
+                const float c = lane_sums<S>(v, lane);
+                held = hold == i ? c : held;
+                __builtin_amdgcn_sched_barrier(0);       // (hoisting later tokens' decays costs the occupancy)
             }
-            parts[0][w][i][lane] = acc;
-            const float c = lane_sums<S>(v, lane);
-            held = hold == i % HOLD ? c : held;
-            if (i % HOLD == HOLD - 1 && t + i - (HOLD - 1) + hold < q.t1)
-                p.part_c[part0 + (t + i - (HOLD - 1) + hold) * p.G * N] = held;
         }
+        if (hold < tokens) p.part_c[part] = held;
+        // the way back reads the tile from LDS again: without this the compiler keeps every
+        // step size and decay of the way out in registers (120 spilled)
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int i = TQ - 1; i >= 0; --i) {
-            if (SEQ && (bits.ends >> i & 1))
-                load_state<S>(p.dfin ? p.dfin + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, grad);
-            const float2 s = su[i][lane];
-            const float g = gs[i][lane];
-            float du = 0.f, ds = 0.f, v[S];
+        for (int i4 = TQ / 4 - 1; i4 >= 0; --i4) {
+            const float4 B4 = Bs[i4][n0 + lane % S], C4 = Cs[i4][n0 + lane % S];
+            const float Bv[4] = {B4.x, B4.y, B4.z, B4.w}, Cv[4] = {C4.x, C4.y, C4.z, C4.w};
 #pragma unroll
-            for (int n = 0; n < S; ++n) {
-                const float G = fmaf(g, Cs[i][w * S + n], grad[n]);
-                const float m = G * pr[i][n];
-                v[n] = G * s.y;
-                du = fmaf(G, Bs[i][w * S + n], du);
-                ds = fmaf(m, A2[n], ds);
-                dA[n] = fmaf(m, s.x, dA[n]);
-                grad[n] = decay(s.x, A2[n]) * G;
+            for (int k = 3; k >= 0; --k) {
+                const int i = 4 * i4 + k;
+                if (SEQ && (bits.ends >> i & 1))
+                    load_state<S>(p.dfin ? p.dfin + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, grad);
+                const float2 s = su[i][lane];
+                const float g = gs[i][lane];
+                float du = 0.f, ds = 0.f, v[S];
+                static_for<S>([&](auto I) {
+                    constexpr int n = decltype(I)::value;
+                    const float G = grad[n] + row_lane<n>(Cv[k]) * g;
+                    const float m = G * pr[i][n];
+                    v[n] = G * s.y;
+                    du += row_lane<n>(Bv[k]) * G;
+                    ds = fmaf(m, A2[n], ds);
+                    dA[n] = fmaf(m, s.x, dA[n]);
+                    grad[n] = decay(s.x, A2[n]) * G;
+                });
+                parts[1][w][i][lane] = du;
+                parts[2][w][i][lane] = ds;
+                const float c = lane_sums<S>(v, lane);
+                held = hold == i ? c : held;
+                if (SEQ && (bits.starts >> i & 1) && p.dinit && mine)
+                    store_f32<S>(p.dinit + clamp_id(ids[t + i], p.nseqs) * DN + state, grad);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            parts[1][w][i][lane] = du;
-            parts[2][w][i][lane] = ds;
-            const float c = lane_sums<S>(v, lane);
-            held = hold == i % HOLD ? c : held;
-            if (i % HOLD == 0 && t + i + hold < q.t1) p.part_b[part0 + (t + i + hold) * p.G * N] = held;
-            if (SEQ && (bits.starts >> i & 1) && p.dinit && q.mine)
-                store_f32<S>(p.dinit + clamp_id(ids[t + i], p.nseqs) * DN + state, grad);
         }
+        if (hold < tokens) p.part_b[part] = held;
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const int i = w + W * j;
-            if (t + i >= q.t1) continue;
             float y = skip * xk[j], du = 0.f, ds = 0.f;
 #pragma unroll
             for (int k = 0; k < W; ++k) {
@@ -262,41 +339,45 @@ void sel_reverse_kernel(SelParams p) {
                 du += parts[1][k][i][lane];
                 ds += parts[2][k][i][lane];
             }
-            const float step = su[i][lane].x, g = gs[i][lane];
             const float draw = fmaf(xk[j], du, ds * kLn2) * slope[j];       // ds was taken with A in log2 units
-            sum_skip = fmaf(g, xk[j], sum_skip);
+            if (i >= tokens || !mine) continue;
+            sum_skip = fmaf(g[j], xk[j], sum_skip);
             sum_bias += draw;
-            if (!q.mine) continue;
-            const int64_t at = row + (t + i) * p.D;
-            p.dx[at] = fmaf(step, du, skip * g);
+            const int64_t at = row + i * p.D;
+            p.dx[at] = fmaf(step[j], du, skip * g[j]);
             p.ddt[at] = draw;
-            if (z) {
-                const float s = sigmoid(zk[j]);
-                p.dz[at] = dyk[j] * y * silu_slope(zk[j], s);
-            }
+            if (p.z) p.dz[at] = dyk[j] * y * silu_slope(zk[j], sz[j]);
         }
+        x -= TQ * p.ldx;
+        dt -= TQ * p.lddt;
+        z -= TQ * p.ldz;
+        B -= TQ * p.ldb;
+        C -= TQ * p.ldc;
+        dy -= TQ * p.D;
+        row -= TQ * p.D;
+        part -= TQ * p.G * N;
     }
-    if (!SEQ && q.seg == 0 && p.dinit && q.mine) store_f32<S>(p.dinit + q.b * DN + state, grad);
+    if (!SEQ && q.seg == 0 && p.dinit && mine) store_f32<S>(p.dinit + q.b * DN + state, grad);
     float* sums = p.part_sums + (q.b * p.nseg + q.seg) * (DN + 2 * p.D);
 #pragma unroll
     for (int n = 0; n < S; ++n) dA[n] *= A2[n] * kLn2;           // dA_log = dA A
-    if (q.mine) store_f32<S>(sums + state, dA);
+    if (mine) store_f32<S>(sums + state, dA);
     if constexpr (W > 1) {
         __syncthreads();
         parts[0][w][0][lane] = sum_skip;
-        parts[0][w][1][lane] = sum_bias;
+        parts[1][w][0][lane] = sum_bias;
         __syncthreads();
         if (w == 0) {
 #pragma unroll
             for (int k = 1; k < W; ++k) {
                 sum_skip += parts[0][k][0][lane];
-                sum_bias += parts[0][k][1][lane];
+                sum_bias += parts[1][k][0][lane];
             }
         }
     }
-    if (w == 0 && q.mine) {
-        sums[DN + q.d] = sum_skip;
-        sums[DN + p.D + q.d] = sum_bias;
+    if (w == 0 && mine) {
+        sums[DN + d] = sum_skip;
+        sums[DN + p.D + d] = sum_bias;
     }
 }
 
@@ -328,13 +409,16 @@ __global__ __launch_bounds__(256) void sel_group_sums_kernel(const float* pb, co
 
 template <typename T, int N> static void reverse_n(const SelParams& p, bool local, hipStream_t s) {
     constexpr int S = N <= 16 ? N : 16;
-    const dim3 grid((unsigned)(p.batch * p.nseg * p.G * p.blocks)), block(64 * (N / S));
+    const dim3 grid((unsigned)(p.batch * p.nseg * p.G * p.blocks));
     if (local) {
-        if (p.seq_idx) hipLaunchKernelGGL((sel_reverse_local_kernel<T, N, S, true>), grid, block, 0, s, p);
-        else hipLaunchKernelGGL((sel_reverse_local_kernel<T, N, S, false>), grid, block, 0, s, p);
+        const dim3 block(SelShape<N, 64, S>::THREADS);
+        if (p.seq_idx) hipLaunchKernelGGL((sel_reverse_local_kernel<T, N, 64, S, true>), grid, block, 0, s, p);
+        else hipLaunchKernelGGL((sel_reverse_local_kernel<T, N, 64, S, false>), grid, block, 0, s, p);
     } else {
-        if (p.seq_idx) hipLaunchKernelGGL((sel_reverse_kernel<T, N, S, true>), grid, block, 0, s, p);
-        else hipLaunchKernelGGL((sel_reverse_kernel<T, N, S, false>), grid, block, 0, s, p);
+        constexpr int R = N <= 32 ? 4 : 8;
+        const dim3 block(SelShape<N, 64, R>::THREADS);
+        if (p.seq_idx) hipLaunchKernelGGL((sel_reverse_kernel<T, N, R, true>), grid, block, 0, s, p);
+        else hipLaunchKernelGGL((sel_reverse_kernel<T, N, R, false>), grid, block, 0, s, p);
     }
 }
 static hipError_t reverse(const SelParams& p, int dtype, int64_t N, bool local, hipStream_t s) {
