@@ -60,23 +60,19 @@ template <> __device__ inline float silu_for<__bf16>(float v) {
 // d silu / dv = s (1 + v (1 - s)), s = sigmoid(v)
 __device__ inline float silu_slope(float v, float s) { return s * (1.f + v * (1.f - s)); }
 
-// log(1 + e^v) = max(v, 0) + log1p(t), t = e^-|v|, with Goldberg's correction for the
-// rounding of u = 1 + t ("What every computer scientist should know about floating-point
-// arithmetic", 1991, theorem 4).  The clamp of |v| leaves a NaN in place.
-struct SoftplusParts {
-    float value, t, u;
-};
-__device__ inline SoftplusParts softplus_parts(float v) {
-    const float a = fabsf(v), t = exp_small(a > 100.f ? -100.f : -a), u = 1.f + t;
-    const float l = u == 1.f ? t : __builtin_amdgcn_logf(u) * kLn2 * (t * __builtin_amdgcn_rcpf(u - 1.f));
-    return {fmaxf(v, 0.f) + l, t, u};
-}
-__device__ inline float softplus(float v) { return softplus_parts(v).value; }
-// softplus and its slope, sigmoid(v) = 1 / u or t / u
+// log(1 + e^v) = max(v, 0) + log1p(t), t = e^-|v|.  With u = 1 + t rounded and e = t - (u - 1)
+// what the rounding lost, log1p(t) = log(u) + e / u to first order, which keeps the relative
+// error of a tiny t (u = 1, e = t).  slope: sigmoid(v) = 1 / u or t / u.  Relative error below
+// 2^-24 |v| plus a few roundings, from the argument of the exp2.
 __device__ inline float softplus_slope(float v, float* slope) {
-    const SoftplusParts s = softplus_parts(v);
-    *slope = (v >= 0.f ? 1.f : s.t) * __builtin_amdgcn_rcpf(s.u);
-    return s.value;
+    const float t = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e), u = 1.f + t;
+    const float r = __builtin_amdgcn_rcpf(u), e = t - (u - 1.f);
+    *slope = (v >= 0.f ? 1.f : t) * r;
+    return fmaxf(v, 0.f) + fmaf(__builtin_amdgcn_logf(u), kLn2, e * r);
+}
+__device__ inline float softplus(float v) {
+    float slope;
+    return softplus_slope(v, &slope);
 }
 
 // Sequence id of a token, clamped so that a bad id cannot leave the per-sequence arrays.

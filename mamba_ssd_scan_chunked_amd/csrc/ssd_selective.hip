@@ -1,7 +1,6 @@
 // Selective scan, forward: the scan over whole rows or segments, the local pass and the
 // combine of split rows, and the single-token step.
 #include "selective.hpp"
-#include <cstdlib>
 
 namespace ssd {
 
@@ -14,7 +13,7 @@ namespace ssd {
 template <typename T, int N, int CH, int S, bool SEQ>
 __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_forward_kernel(SelParams p) {
     using Sh = SelShape<N, CH, S>;
-    constexpr int W = Sh::W, TH = Sh::THREADS, TQ = 16, J = TQ * CH / TH, E = (TQ * N + TH - 1) / TH;
+    constexpr int W = Sh::W, TH = Sh::THREADS, TQ = 32, J = TQ * CH / TH, E = (TQ * N + TH - 1) / TH;
     static_assert(J * TH == TQ * CH, "tile shape");
     __shared__ float2 su[TQ][CH];
     __shared__ float4 Bs[TQ / 4][N];                             // four tokens of a state together
@@ -335,12 +334,8 @@ template <typename T, int N, int CH, int S> static void forward_shape(const SelP
     else hipLaunchKernelGGL((sel_forward_kernel<T, N, CH, S, false>), sel_grid(p), block, 0, s, p);
 }
 template <typename T, int N> static void forward_n(const SelParams& p, hipStream_t s) {
-    static const int v = getenv("SEL_V") ? atoi(getenv("SEL_V")) : 0;
-    if (v == 0) forward_shape<T, N, 32, N / 8>(p, s);
-    if (v == 1) forward_shape<T, N, 16, N / 4>(p, s);
-    if (v == 2) forward_shape<T, N, 64, (N < 16 ? N : 16)>(p, s);
-    if (v == 3) forward_shape<T, N, 64, N / 4>(p, s);
-    if (v == 4) forward_shape<T, N, 16, (N / 8)>(p, s);
+    if (p.nseg > 1) forward_shape<T, N, 64, N / 4>(p, s);
+    else forward_shape<T, N, 32, N / 8>(p, s);
 }
 template <typename T, int N, bool CKPT> static void local_n(const SelParams& p0, hipStream_t s) {
     constexpr int CH = 64, S = N <= 16 ? N : 16, TQ = CKPT ? 8 : 16;

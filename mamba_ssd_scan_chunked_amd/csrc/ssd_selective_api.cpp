@@ -8,7 +8,6 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstdio>
-#include <cstdlib>
 
 #include "selective.hpp"
 #include "ssd_host.hpp"
@@ -18,35 +17,37 @@ namespace {
 using namespace ssd_host;
 
 constexpr int64_t kMaxDim = int64_t(1) << 31;
-constexpr int64_t kTile = 16;                // segments are whole tiles of every kernel
+// Segments are whole tiles of the kernels that walk them.
+constexpr int64_t kForwardTile = 32, kBackwardTile = 8;
 
 int64_t blocks_of(const ssd_selective_problem_t* p) { return (p->channels / p->ngroups + 63) / 64; }
 
-// Segments per row.  A row's channels give batch x groups x blocks workgroups; rows are cut
-// when those do not fill the chip.  A cut costs a local pass (about the scan again without
-// its read-out), so the forward is cut only below `few` workgroups; the backward needs its
-// local pass for the checkpoints anyway.
+// Segments per row.  A row's 64-channel blocks give `items` workgroups' worth of work; a row
+// is cut to fill the chip.  Forward, a cut adds the local pass (nearly the scan again): on
+// an MI355X (2048 tokens, 16 states, bf16) 10 items take 160 us whole and 38 us in segments
+// of 64 tokens, 80 items 158 and 93, 160 items 190 and 158, 240 items 188 and 221; 80 items
+// of 512 tokens 44 and 40, 16 items of 300 tokens 30 and 32.  Backward, the local pass is
+// needed for its checkpoints anyway and the segments only add the reverse one: 10 items 1552
+// us whole and 92 us in segments of 32 tokens, 320 items 1945 and (16 segments) 1101, 640
+// items 2582 and (8 segments) 2122.
 struct Segments {
     int64_t n, len;
 };
 Segments segments_of(const ssd_selective_problem_t* p, bool backward) {
-    const int64_t tiles = std::max<int64_t>(1, (p->seqlen + kTile - 1) / kTile);
+    const int64_t tile = backward ? kBackwardTile : kForwardTile;
+    const int64_t tiles = std::max<int64_t>(1, (p->seqlen + tile - 1) / tile);
     const int64_t items = std::max<int64_t>(1, p->batch * p->ngroups * blocks_of(p));
     int64_t n = 1;
     if (p->segments > 0) {
         n = p->segments;
     } else if (backward) {
-        static const int64_t slots = getenv("SEL_SLOTS") ? atoi(getenv("SEL_SLOTS")) : 768;
-        n = slots / items;
-        n = std::min(n, std::max<int64_t>(1, tiles / 4));
-    } else {
-        static const int64_t fs = getenv("SEL_FS") ? atoi(getenv("SEL_FS")) : 2048;
-        if (items < 256) n = fs / items;
-        n = std::min(n, std::max<int64_t>(1, tiles / 4));
+        n = std::min(4096 / items, p->seqlen / 32);
+    } else if (items <= 192 && p->seqlen >= 512) {
+        n = std::min(4096 / items, p->seqlen / 64);
     }
     n = std::max<int64_t>(1, std::min(n, tiles));
     const int64_t per = (tiles + n - 1) / n;
-    return {(tiles + per - 1) / per, per * kTile};
+    return {(tiles + per - 1) / per, per * tile};
 }
 
 int validate(const ssd_selective_problem_t* p) {

@@ -164,7 +164,8 @@ __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS)) void sel_reverse_ker
     static_assert(W * J == TQ && TH >= TQ * N, "tile shape");     // a B and a C value per thread
     __shared__ float2 su[TQ][CH];
     __shared__ float gs[TQ][CH];
-    __shared__ float4 Bs[TQ / 4][N], Cs[TQ / 4][N];
+    __shared__ float4 Bq[TQ / 4][N];                             // four tokens of a state together
+    __shared__ __attribute__((aligned(16))) float Bs[TQ][N], Cs[TQ][N];    // a token's states together
     __shared__ float parts[3][W][TQ][CH];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const SelPlace q = sel_place<CH>(p);
@@ -259,8 +260,10 @@ __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS)) void sel_reverse_ker
         }
         if (TH == TQ * N || bi < TQ) {
             const int n = threadIdx.x % N;
-            (&Bs[bi / 4][n].x)[bi % 4] = bi < tokens ? (float)br : 0.f;
-            (&Cs[bi / 4][n].x)[bi % 4] = bi < tokens ? (float)cr : 0.f;
+            const float b = bi < tokens ? (float)br : 0.f;
+            (&Bq[bi / 4][n].x)[bi % 4] = b;
+            Bs[bi][n] = b;
+            Cs[bi][n] = bi < tokens ? (float)cr : 0.f;
         }
         __syncthreads();
         SeqBits bits{};
@@ -269,8 +272,8 @@ __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS)) void sel_reverse_ker
         float pr[TQ][S], held = 0.f;
 #pragma unroll
         for (int i4 = 0; i4 < TQ / 4; ++i4) {
-            const float4 B4 = Bs[i4][n0 + lane % S], C4 = Cs[i4][n0 + lane % S];
-            const float Bv[4] = {B4.x, B4.y, B4.z, B4.w}, Cv[4] = {C4.x, C4.y, C4.z, C4.w};
+            const float4 B4 = Bq[i4][n0 + lane % S];
+            const float Bv[4] = {B4.x, B4.y, B4.z, B4.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int i = 4 * i4 + k;
@@ -278,12 +281,13 @@ __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS)) void sel_reverse_ker
                     load_state<S>(p.init ? p.init + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, h);
                 const float2 s = su[i][lane];
                 const float g = gs[i][lane];
+                const States<S> Cv = *(const States<S>*)&Cs[i][n0];
                 float acc = 0.f, v[S];
                 static_for<S>([&](auto I) {
                     constexpr int n = decltype(I)::value;
                     pr[i][n] = decay(s.x, A2[n]) * h[n];
                     h[n] = pr[i][n] + row_lane<n>(Bv[k]) * s.y;
-                    acc += row_lane<n>(Cv[k]) * h[n];
+                    acc = fmaf(Cv.v[n], h[n], acc);
                     v[n] = g * h[n];
                 });
                 parts[0][w][i][lane] = acc;
@@ -298,8 +302,6 @@ __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS)) void sel_reverse_ker
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
         for (int i4 = TQ / 4 - 1; i4 >= 0; --i4) {
-            const float4 B4 = Bs[i4][n0 + lane % S], C4 = Cs[i4][n0 + lane % S];
-            const float Bv[4] = {B4.x, B4.y, B4.z, B4.w}, Cv[4] = {C4.x, C4.y, C4.z, C4.w};
 #pragma unroll
             for (int k = 3; k >= 0; --k) {
                 const int i = 4 * i4 + k;
@@ -307,13 +309,14 @@ __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS)) void sel_reverse_ker
                     load_state<S>(p.dfin ? p.dfin + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, grad);
                 const float2 s = su[i][lane];
                 const float g = gs[i][lane];
+                const States<S> Bv = *(const States<S>*)&Bs[i][n0], Cv = *(const States<S>*)&Cs[i][n0];
                 float du = 0.f, ds = 0.f, v[S];
                 static_for<S>([&](auto I) {
                     constexpr int n = decltype(I)::value;
-                    const float G = grad[n] + row_lane<n>(Cv[k]) * g;
+                    const float G = fmaf(Cv.v[n], g, grad[n]);
                     const float m = G * pr[i][n];
                     v[n] = G * s.y;
-                    du += row_lane<n>(Bv[k]) * G;
+                    du = fmaf(Bv.v[n], G, du);
                     ds = fmaf(m, A2[n], ds);
                     dA[n] = fmaf(m, s.x, dA[n]);
                     grad[n] = decay(s.x, A2[n]) * G;
