@@ -75,6 +75,27 @@ __device__ inline float softplus(float v) {
     return softplus_slope(v, &slope);
 }
 
+// Sum over teams of LANES neighbouring lanes (4 to 64, a power of two), in every lane: DPP
+// moves within a row of 16, then the row and half-wave swaps.
+template <int CTRL> __device__ inline float dpp_mov(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+template <int LANES> __device__ inline float lane_team_sum(float v) {
+    v += dpp_mov<0xb1>(v);                             // quad_perm 1,0,3,2
+    v += dpp_mov<0x4e>(v);                             // quad_perm 2,3,0,1
+    if constexpr (LANES > 4) v += dpp_mov<0x141>(v);   // row_half_mirror
+    if constexpr (LANES > 8) v += dpp_mov<0x140>(v);   // row_mirror
+    if constexpr (LANES > 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if constexpr (LANES > 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    return v;
+}
+
 // Sequence id of a token, clamped so that a bad id cannot leave the per-sequence arrays.
 __device__ inline int64_t clamp_id(int32_t id, int64_t nseqs) {
     return id < 0 ? 0 : (id >= nseqs ? nseqs - 1 : id);

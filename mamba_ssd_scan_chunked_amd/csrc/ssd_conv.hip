@@ -28,26 +28,29 @@ struct ConvParams {
     const float *dy, *dfin;
     float *dx, *dinit, *part;
     int64_t T, D, nseqs, ldx;
-    unsigned total, nvec, nrun, L;
+    unsigned nvec, nblk, nrun, L;    // vectors, workgroups over them, runs per row, tokens per run
     int silu;
 };
 
-// Channels of the thread: V from c0.  The last vector of a row is moved back to end
-// with the row (D >= V), so it repeats channels of its neighbour with equal results
-// and no access needs a bound per element.
+// A workgroup is one wave on 64 vectors of V channels and one run of tokens, so that every
+// decision about tokens and sequences is a scalar one.  The last vector of a row is moved
+// back to end with the row (D >= V): it repeats channels of its neighbour with equal
+// results, and no access needs a bound per element.
 struct Place {
     int64_t c0, b, t0, t1;
     unsigned run;
+    bool active;
 };
-template <int V> __device__ inline Place place_of(const ConvParams& p, unsigned idx) {
+template <int V> __device__ inline Place place_of(const ConvParams& p) {
     Place q;
-    const unsigned cv = idx % p.nvec, rest = idx / p.nvec;
-    q.run = rest;
-    q.b = rest / p.nrun;
-    q.t0 = (int64_t)(rest % p.nrun) * p.L;
+    const unsigned cv = blockIdx.x % p.nblk * 64 + threadIdx.x;
+    q.run = blockIdx.x / p.nblk;
+    q.b = q.run / p.nrun;
+    q.t0 = (int64_t)(q.run % p.nrun) * p.L;
     q.t1 = q.t0 + p.L < p.T ? q.t0 + p.L : p.T;
     const int64_t c = (int64_t)cv * V;
     q.c0 = c + V <= p.D ? c : p.D - V;
+    q.active = cv < p.nvec;
     return q;
 }
 
@@ -110,10 +113,9 @@ template <int V, int K> __device__ inline void push(float (&win)[K - 1][V], cons
 
 constexpr int kAhead = 4;      // tokens whose loads are issued together
 
-template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(256) void conv_forward_kernel(ConvParams p) {
-    const unsigned idx = blockIdx.x * 256u + threadIdx.x;
-    if (idx >= p.total) return;
-    const Place q = place_of<V>(p, idx);
+template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(64, 4) void conv_forward_kernel(ConvParams p) {
+    const Place q = place_of<V>(p);
+    if (!q.active) return;
     const int32_t* ids = SEQ ? p.seq_idx + q.b * p.T : nullptr;
     float w[K][V], bias[V], win[K - 1][V];
     load_weights<V, K>(p, q.c0, w);
@@ -126,11 +128,19 @@ template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(256) 
     open_window<T, V, K, SEQ>(p, q, ids, win);
     const T* x = (const T*)p.x + q.b * p.T * p.ldx + q.c0;
     T* y = (T*)p.y + q.b * p.T * p.D + q.c0;
-    for (int64_t t = q.t0; t < q.t1; t += kAhead) {
-        Pack<T, V> raw[kAhead];
+    Pack<T, V> next[kAhead];
+    auto fetch = [&](int64_t t) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-            if (t + u < q.t1) raw[u] = load_pack<V>(x + (t + u) * p.ldx);
+            if (t + u < q.t1) next[u] = load_pack<V>(x + (t + u) * p.ldx);
+    };
+    fetch(q.t0);
+    for (int64_t t = q.t0; t < q.t1; t += kAhead) {
+        // the next tokens' loads are in flight while these are worked on
+        Pack<T, V> raw[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) raw[u] = next[u];
+        fetch(t + kAhead);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (t + u >= q.t1) break;
@@ -168,10 +178,9 @@ template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(256) 
 // the rows before its run to the run before.  Rows before a sequence's first token are
 // those of its initial state and go to dinit.  dw and dbias are summed per run into
 // `part` (K+1 arrays of runs x D), then over runs in a fixed order.
-template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(256) void conv_backward_kernel(ConvParams p) {
-    const unsigned idx = blockIdx.x * 256u + threadIdx.x;
-    if (idx >= p.total) return;
-    const Place q = place_of<V>(p, idx);
+template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(64, 3) void conv_backward_kernel(ConvParams p) {
+    const Place q = place_of<V>(p);
+    if (!q.active) return;
     const int32_t* ids = SEQ ? p.seq_idx + q.b * p.T : nullptr;
     float w[K][V], bias[V], win[K - 1][V], acc[K][V], dw[K][V], db[V];
     load_weights<V, K>(p, q.c0, w);
@@ -204,16 +213,28 @@ template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(256) 
         }
     };
 
+    // the next tokens' loads are in flight while these are worked on
+    Pack<T, V> next[kAhead];
+    Pack<float, V> next_dy[kAhead];
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (t + u < end) {
+                next[u] = load_pack<V>(x + (t + u) * p.ldx);
+                next_dy[u] = load_pack<V>(dy + (t + u) * p.D);
+            }
+    };
+    fetch(q.t0);
     bool open = true;                     // the run's last sequence goes on past the run
     for (int64_t t = q.t0; t < end && open; t += kAhead) {
         Pack<T, V> raw[kAhead];
         Pack<float, V> dyr[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (t + u < end) {
-                raw[u] = load_pack<V>(x + (t + u) * p.ldx);
-                dyr[u] = load_pack<V>(dy + (t + u) * p.D);
-            }
+        for (int u = 0; u < kAhead; ++u) {
+            raw[u] = next[u];
+            dyr[u] = next_dy[u];
+        }
+        fetch(t + kAhead);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int64_t tt = t + u;
@@ -303,8 +324,8 @@ template <typename T, int K> __global__ __launch_bounds__(256) void conv_step_ke
     ((T*)p.y)[i] = (T)(p.silu ? silu_for<T>(acc) : acc);
 }
 
-template <typename T, int V, int K, bool BACK> static void launch_conv(const ConvParams& p, hipStream_t s) {
-    const dim3 grid((p.total + 255) / 256), block(256);
+template <typename T, int V, int K, bool BACK> static void launch_conv(const ConvParams& p, int64_t batch, hipStream_t s) {
+    const dim3 grid((unsigned)(p.nblk * p.nrun * batch)), block(64);
     if constexpr (BACK) {
         if (p.seq_idx) hipLaunchKernelGGL((conv_backward_kernel<T, V, K, true>), grid, block, 0, s, p);
         else hipLaunchKernelGGL((conv_backward_kernel<T, V, K, false>), grid, block, 0, s, p);
@@ -313,10 +334,11 @@ template <typename T, int V, int K, bool BACK> static void launch_conv(const Con
         else hipLaunchKernelGGL((conv_forward_kernel<T, V, K, false>), grid, block, 0, s, p);
     }
 }
-template <typename T, int V, bool BACK> static hipError_t launch_conv_k(int K, const ConvParams& p, hipStream_t s) {
-    if (K == 2) launch_conv<T, V, 2, BACK>(p, s);
-    else if (K == 3) launch_conv<T, V, 3, BACK>(p, s);
-    else launch_conv<T, V, 4, BACK>(p, s);
+template <typename T, int V, bool BACK>
+static hipError_t launch_conv_k(int K, const ConvParams& p, int64_t batch, hipStream_t s) {
+    if (K == 2) launch_conv<T, V, 2, BACK>(p, batch, s);
+    else if (K == 3) launch_conv<T, V, 3, BACK>(p, batch, s);
+    else launch_conv<T, V, 4, BACK>(p, batch, s);
     return hipGetLastError();
 }
 template <typename T> static hipError_t launch_step(int K, const ConvParams& p, int64_t n, hipStream_t s) {
@@ -338,7 +360,7 @@ constexpr int64_t kMaxDim = int64_t(1) << 31;
 // Channels per thread and tokens per run.
 struct Shape {
     int V;
-    int64_t nvec, L, nrun, total;
+    int64_t nvec, nblk, L, nrun;
 };
 Shape shape_of(const ssd_conv_problem_t* p, bool backward) {
     Shape s;
@@ -347,15 +369,19 @@ Shape shape_of(const ssd_conv_problem_t* p, bool backward) {
     s.V = backward ? 4 : (p->dtype == SSD_DTYPE_BF16 ? 8 : 4);
     if (p->channels < s.V) s.V = 1;
     s.nvec = (p->channels + s.V - 1) / s.V;
-    // Runs as long as the chip stays full (about 1 << 18 threads): a run re-reads K-1
-    // rows, so longer runs read less.
-    const int64_t want = int64_t(1) << 18;
-    const int64_t longest = backward ? 64 : 32;
-    const int64_t rows = std::max<int64_t>(1, p->batch * s.nvec);
-    const int64_t runs = std::max<int64_t>(1, want / rows);
-    s.L = std::min(longest, std::max<int64_t>(4, (p->seqlen + runs - 1) / runs));
+    s.nblk = (s.nvec + 63) / 64;
+    // Runs: as many waves as the chip holds at once (three per SIMD backward, four forward),
+    // or a whole number of times that when runs would get longer than `longest`: a run
+    // re-reads K-1 rows, but a last round of few waves costs a whole one (4 x 4096 tokens of
+    // 5376 channels backward: runs of 64 tokens, 1.75 rounds, 266 us; of 96, 1.2 rounds, 311;
+    // of 128, 0.9 rounds, 254).
+    const int64_t longest = backward ? 128 : 32, resident = (backward ? 3 : 4) * 1024;
+    const int64_t columns = std::max<int64_t>(1, p->batch * s.nblk);
+    const int64_t least = (p->seqlen + longest - 1) / longest;                      // runs per row
+    const int64_t rounds = (int64_t)(double(least) * double(columns) / resident) + 1;
+    const int64_t runs = std::max(std::max<int64_t>(1, least), rounds * resident / columns);
+    s.L = std::max<int64_t>(4, (p->seqlen + runs - 1) / runs);
     s.nrun = std::max<int64_t>(1, (p->seqlen + s.L - 1) / s.L);
-    s.total = s.nvec * s.nrun * p->batch;
     return s;
 }
 
@@ -371,10 +397,11 @@ int validate(const ssd_conv_problem_t* p) {
         return SSD_ERR_UNSUPPORTED;
     const double elems = double(p->batch) * double(p->seqlen) * double(p->ldx);
     if (elems > 4e17 || double(p->nseqs) * p->channels * 3 > 4e17) return SSD_ERR_BAD_SHAPE;
-    // threads are numbered in 32 bits
-    if (double(shape_of(p, false).nvec) * shape_of(p, false).nrun * p->batch >= 4e9 ||
-        double(shape_of(p, true).nvec) * shape_of(p, true).nrun * p->batch >= 4e9)
-        return SSD_ERR_UNSUPPORTED;
+    // a launch holds fewer than 2^32 threads
+    for (bool backward : {false, true}) {
+        const Shape s = shape_of(p, backward);
+        if (double(s.nblk) * s.nrun * p->batch * 64 >= 4e9) return SSD_ERR_UNSUPPORTED;
+    }
     return SSD_OK;
 }
 
@@ -421,8 +448,8 @@ ssd::ConvParams params_of(const ssd_conv_problem_t* p, const Shape& s) {
     c.D = p->channels;
     c.nseqs = p->nseqs;
     c.ldx = p->ldx;
-    c.total = (unsigned)s.total;
     c.nvec = (unsigned)s.nvec;
+    c.nblk = (unsigned)s.nblk;
     c.nrun = (unsigned)s.nrun;
     c.L = (unsigned)s.L;
     c.silu = (p->flags & SSD_CONV_SILU) ? 1 : 0;
@@ -485,11 +512,11 @@ int ssd_conv_forward(const ssd_conv_problem_t* p, const void* x, const float* we
     c.fin = final_state;
     hipError_t r;
     if (p->dtype == SSD_DTYPE_BF16)
-        r = s.V == 8 ? ssd::launch_conv_k<__bf16, 8, false>(p->width, c, st)
-                     : ssd::launch_conv_k<__bf16, 1, false>(p->width, c, st);
+        r = s.V == 8 ? ssd::launch_conv_k<__bf16, 8, false>(p->width, c, p->batch, st)
+                     : ssd::launch_conv_k<__bf16, 1, false>(p->width, c, p->batch, st);
     else
-        r = s.V == 4 ? ssd::launch_conv_k<float, 4, false>(p->width, c, st)
-                     : ssd::launch_conv_k<float, 1, false>(p->width, c, st);
+        r = s.V == 4 ? ssd::launch_conv_k<float, 4, false>(p->width, c, p->batch, st)
+                     : ssd::launch_conv_k<float, 1, false>(p->width, c, p->batch, st);
     return done("forward", p, r);
 }
 
@@ -543,11 +570,11 @@ int ssd_conv_backward(const ssd_conv_problem_t* p, const void* x, const float* w
     if (seq_idx && dinit) r = ssd::launch_fill(dinit, z.state / 4, st);
     if (r == hipSuccess) {
         if (p->dtype == SSD_DTYPE_BF16)
-            r = s.V == 4 ? ssd::launch_conv_k<__bf16, 4, true>(p->width, c, st)
-                         : ssd::launch_conv_k<__bf16, 1, true>(p->width, c, st);
+            r = s.V == 4 ? ssd::launch_conv_k<__bf16, 4, true>(p->width, c, p->batch, st)
+                         : ssd::launch_conv_k<__bf16, 1, true>(p->width, c, p->batch, st);
         else
-            r = s.V == 4 ? ssd::launch_conv_k<float, 4, true>(p->width, c, st)
-                         : ssd::launch_conv_k<float, 1, true>(p->width, c, st);
+            r = s.V == 4 ? ssd::launch_conv_k<float, 4, true>(p->width, c, p->batch, st)
+                         : ssd::launch_conv_k<float, 1, true>(p->width, c, p->batch, st);
     }
     if (r == hipSuccess) {
         // one row of part per run: D*K weight gradients, then D bias gradients

@@ -12,7 +12,7 @@
 //
 // Gradients, with e = dL/d(u r w) and hat = u r:
 //   du = r (e w - hat mean(e w hat)),   dw = sum over rows of e hat.
-// A team walks several rows of one group, with dw (and the residual's dscale) in
+// A team walks several rows of one group (as it does forward), with dw (and the residual's dscale) in
 // registers; the teams' sums go to the workspace and are added in a fixed order.
 #include "ssd.h"
 
@@ -39,24 +39,29 @@ struct NormParams {
 
 constexpr int kV = 4;                // channels per pack
 
-// Sum over the TEAM lanes of a team, in every lane.  Teams above one wave meet in `red`;
-// two sums in turn need one buffer each (between two uses of a buffer lies the other
-// sum's barrier).
+// Lanes of a team: TEAM of them (several teams in a workgroup of 256 when that is less), or,
+// TEAM 0, a whole workgroup of as many waves as the row needs.
+template <int TEAM> __device__ inline int team_lanes() { return TEAM ? TEAM : (int)blockDim.x; }
+template <int TEAM> __device__ inline int team_lane() { return TEAM ? threadIdx.x % (TEAM ? TEAM : 1) : threadIdx.x; }
+template <int TEAM> __device__ inline unsigned team_index() {
+    return TEAM ? blockIdx.x * (256 / (TEAM ? TEAM : 1)) + threadIdx.x / (TEAM ? TEAM : 1) : blockIdx.x;
+}
+
+// Sum over the lanes of a team, in every lane.  The waves of a workgroup-sized team meet in
+// `red`; two sums in turn need one buffer each (between two uses of a buffer lies the
+// other sum's barrier).
 template <int TEAM> __device__ inline float team_sum(float v, float (&red)[16]) {
-#pragma unroll
-    for (int d = 1; d < (TEAM < 64 ? TEAM : 64); d <<= 1) v += __shfl_xor(v, d);
-    if constexpr (TEAM > 64) {
-        const int w = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) red[w] = v;
+    v = lane_team_sum<(TEAM == 0 || TEAM > 64 ? 64 : TEAM)>(v);
+    if constexpr (TEAM == 0 || TEAM > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
         __syncthreads();
-        v = 0.f;
-#pragma unroll
-        for (int i = 0; i < TEAM / 64; ++i) v += red[i];
+        const int w = threadIdx.x & 15;
+        v = lane_team_sum<16>(w < (int)blockDim.x / 64 ? red[w] : 0.f);
     }
     return v;
 }
 
-// Pack c of the team lane: channels 4 (c TEAM + lane) .. +3 of the group, of which
+// Pack c of the team lane: channels 4 (c lanes + lane) .. +3 of the group, of which
 // `n` exist.  Whole packs load in one piece, the last of an odd group one by one.
 template <typename T> __device__ inline void load_part(const T* p, int n, float (&v)[kV]) {
     if (n >= kV) {
@@ -77,25 +82,21 @@ template <typename T> __device__ inline void store_part(T* p, int n, const float
 }
 
 enum { kGateFirst = 0, kGateAfter = 1, kResidual = 2 };
-constexpr int block_of(int team) { return team < 256 ? 256 : team; }
-
+// One row (of a group) per team: rows in flight hide each other's latency.
 template <typename TX, typename TO, int MODE, int TEAM, int CH>
-__global__ __launch_bounds__(block_of(TEAM)) void norm_forward_kernel(NormParams p) {
-    constexpr int PER = block_of(TEAM) / TEAM;                   // teams per workgroup
+__global__ __launch_bounds__(TEAM ? 256 : 1024) void norm_forward_kernel(NormParams p) {
     __shared__ float red[16];
-    const int lane = threadIdx.x % TEAM;
-    const int64_t unit = (int64_t)blockIdx.x * PER + threadIdx.x / TEAM;
-    if (TEAM <= 64 && unit >= p.rows * p.groups) return;         // (larger teams: one unit per workgroup)
-    const int64_t row = unit / p.groups;
-    const int64_t c0 = (unit % p.groups) * p.size;
-    const TX* x = (const TX*)p.x + row * p.ldx + c0;
+    const int lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
+    const unsigned unit = team_index<TEAM>();
+    if (TEAM && TEAM < 256 && unit >= p.rows * p.groups) return;
+    const int64_t row = unit / (unsigned)p.groups, c0 = (int64_t)(unit % (unsigned)p.groups) * p.size;
     float u[CH][kV], gate[CH][kV];
     float sq = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int i = (c * TEAM + lane) * kV, n = p.size - i;
+        const int i = (c * lanes + lane) * kV, n = p.size - i;
         if (n <= 0) continue;
-        load_part(x + i, n, u[c]);
+        load_part((const TX*)p.x + row * p.ldx + c0 + i, n, u[c]);
         if constexpr (MODE == kResidual) {
             if (p.z) load_part((const float*)p.z + row * p.ldz + i, n, gate[c]);
         } else {
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(block_of(TEAM)) void norm_forward_kernel(NormParams
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int i = (c * TEAM + lane) * kV, n = p.size - i;
+        const int i = (c * lanes + lane) * kV, n = p.size - i;
         if (n <= 0) continue;
         if constexpr (MODE == kResidual) {
             if (p.scale) {
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(block_of(TEAM)) void norm_forward_kernel(NormParams
     TO* out = (TO*)p.out + row * p.D + c0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int i = (c * TEAM + lane) * kV, n = p.size - i;
+        const int i = (c * lanes + lane) * kV, n = p.size - i;
         if (n <= 0) continue;
         float w[kV], o[kV];
         load_part(p.w + c0 + i, n, w);
@@ -143,41 +144,63 @@ __global__ __launch_bounds__(block_of(TEAM)) void norm_forward_kernel(NormParams
     }
 }
 
+// Waves per SIMD that the backward is built for (about 45 registers a pack); teams are
+// launched to fill them, and walk the rows.
+constexpr int backward_waves(int team, int ch) { return ch <= 1 ? 5 : (ch <= 2 || team == 0 ? 4 : (ch <= 3 ? 3 : 2)); }
+
 template <typename TX, typename TO, int MODE, int TEAM, int CH>
-__global__ __launch_bounds__(block_of(TEAM)) void norm_backward_kernel(NormParams p) {
-    constexpr int PER = block_of(TEAM) / TEAM;
+__global__ __launch_bounds__(TEAM ? 256 : 1024, backward_waves(TEAM, CH)) void norm_backward_kernel(NormParams p) {
     __shared__ float red[2][16];
-    const int lane = threadIdx.x % TEAM;
-    const int64_t team = (int64_t)blockIdx.x * PER + threadIdx.x / TEAM;
-    if (TEAM <= 64 && team >= p.slots * p.groups) return;
-    const int64_t slot = team / p.groups, c0 = (team % p.groups) * p.size;
-    float w[CH][kV], dw[CH][kV], ds[CH][kV];
+    const int lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
+    const unsigned team = team_index<TEAM>();
+    if (TEAM && team >= p.slots * p.groups) return;
+    const int64_t slot = team / (unsigned)p.groups, c0 = (int64_t)(team % (unsigned)p.groups) * p.size;
+    // w and the scale once: a load of them in the loop would wait for the next row's loads before it
+    float w[CH][kV], g[CH][kV], dw[CH][kV], ds[CH][kV];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int i = (c * TEAM + lane) * kV, n = p.size - i;
+        const int i = (c * lanes + lane) * kV, n = p.size - i;
         if (n > 0) load_part(p.w + c0 + i, n, w[c]);
+        if (MODE == kResidual && p.scale && n > 0) load_part(p.scale + i, n, g[c]);
 #pragma unroll
         for (int v = 0; v < kV; ++v) dw[c][v] = ds[c][v] = 0.f;
     }
+    // u (residual: the saved stream), e = dL/d(u r w); the gate (residual: dL/dstream) in z
+    float nu[CH][kV], ne[CH][kV], nz[CH][kV], nx[CH][kV];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int i = (c * lanes + lane) * kV, n = p.size - i;
+            if (n <= 0) continue;
+            load_part(p.dout + row * p.D + c0 + i, n, ne[c]);
+            if constexpr (MODE == kResidual) {
+                load_part(p.stream + row * p.D + i, n, nu[c]);
+                if (p.dstream) load_part(p.dstream + row * p.D + i, n, nz[c]);
+                if (p.scale) load_part((const TX*)p.x + row * p.ldx + i, n, nx[c]);
+            } else {
+                load_part((const TX*)p.x + row * p.ldx + c0 + i, n, nx[c]);
+                load_part((const TO*)p.z + row * p.ldz + c0 + i, n, nz[c]);
+            }
+        }
+    };
+    if (slot < p.rows) fetch(slot);
     for (int64_t row = slot; row < p.rows; row += p.slots) {
-        // u (residual: the saved stream), e = dL/d(u r w); gate and x kept for dx and dz
         float u[CH][kV], e[CH][kV], z[CH][kV], x[CH][kV];
         float sq = 0.f;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int i = (c * TEAM + lane) * kV, n = p.size - i;
-            if (n <= 0) continue;
-            load_part(p.dout + row * p.D + c0 + i, n, e[c]);
-            if constexpr (MODE == kResidual) {
-                load_part(p.stream + row * p.D + i, n, u[c]);
-            } else {
-                load_part((const TX*)p.x + row * p.ldx + c0 + i, n, x[c]);
-                load_part((const TO*)p.z + row * p.ldz + c0 + i, n, z[c]);
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                u[c][v] = nu[c][v];
+                e[c][v] = ne[c][v];
+                z[c][v] = nz[c][v];
+                x[c][v] = nx[c][v];
             }
-        }
+        // the next row's loads are in flight while this one is worked on
+        if (row + p.slots < p.rows) fetch(row + p.slots);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int n = p.size - (c * TEAM + lane) * kV;
+            const int n = p.size - (c * lanes + lane) * kV;
             if (n <= 0) continue;
             if constexpr (MODE != kResidual) {
 #pragma unroll
@@ -191,7 +214,7 @@ __global__ __launch_bounds__(block_of(TEAM)) void norm_backward_kernel(NormParam
         float dot = 0.f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int n = p.size - (c * TEAM + lane) * kV;
+            const int n = p.size - (c * lanes + lane) * kV;
             if (n <= 0) continue;
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
@@ -210,27 +233,22 @@ __global__ __launch_bounds__(block_of(TEAM)) void norm_backward_kernel(NormParam
         dot = team_sum<TEAM>(dot, red[1]) / (float)p.size;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int i = (c * TEAM + lane) * kV, n = p.size - i;
+            const int i = (c * lanes + lane) * kV, n = p.size - i;
             if (n <= 0) continue;
             float du[kV];
 #pragma unroll
             for (int v = 0; v < kV; ++v) du[v] = r * (e[c][v] - u[c][v] * r * dot);
             if constexpr (MODE == kResidual) {
                 if (p.dstream) {
-                    float d[kV];
-                    load_part(p.dstream + row * p.D + i, n, d);
 #pragma unroll
-                    for (int v = 0; v < kV; ++v) du[v] += d[v];
+                    for (int v = 0; v < kV; ++v) du[v] += z[c][v];
                 }
                 store_part(p.dz + row * p.D + i, n, du);
                 if (p.scale) {
-                    float g[kV], in[kV];
-                    load_part(p.scale + i, n, g);
-                    load_part((const TX*)p.x + row * p.ldx + i, n, in);
 #pragma unroll
                     for (int v = 0; v < kV; ++v) {
-                        ds[c][v] = fmaf(du[v], in[v], ds[c][v]);
-                        du[v] *= g[v];
+                        ds[c][v] = fmaf(du[v], x[c][v], ds[c][v]);
+                        du[v] *= g[c][v];
                     }
                     store_part(p.dx + row * p.D + i, n, du);
                 }
@@ -256,48 +274,61 @@ __global__ __launch_bounds__(block_of(TEAM)) void norm_backward_kernel(NormParam
     float* part = p.part + slot * p.D * (scaled ? 2 : 1) + c0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int i = (c * TEAM + lane) * kV, n = p.size - i;
+        const int i = (c * lanes + lane) * kV, n = p.size - i;
         if (n <= 0) continue;
         store_part(part + i, n, dw[c]);
         if (scaled) store_part(part + p.D + i, n, ds[c]);
     }
 }
 
-// Lanes per team and packs per lane for a group of `size` channels.
+// Lanes per team and packs per lane for a group of `size` channels: a wave or less up to
+// 1024 channels, which needs no barrier.  Above, forward, four waves with up to eight packs
+// a lane (5120 channels in four waves of five packs: 150 us for 16384 rows of the gated norm,
+// in ten waves of two 192, in ten persistent waves with the next row's loads ahead 175);
+// backward, just enough waves with one or two packs (2560 channels in ten waves of one pack:
+// 174 us for the residual norm's 16384 rows, in five waves of two 297).  Past 8192 channels
+// 16 waves with more packs.
 struct Team {
-    int lanes, ch;
+    int team, lanes, ch;
 };
-static Team team_of(int64_t size) {
-    if (size <= 32) return {8, 1};
-    if (size <= 64) return {16, 1};
-    if (size <= 128) return {32, 1};
-    if (size <= 256) return {64, 1};
-    if (size <= 512) return {64, 2};
-    if (size <= 1024) return {256, 1};
-    for (int ch = 2; ch <= 8; ++ch)
-        if (size <= 1024 * ch) return {256, ch};
-    for (int ch = 3; ch <= 8; ++ch)
-        if (size <= 4096 * ch) return {1024, ch};
-    return {0, 0};
+static Team team_of(int64_t size, bool backward) {
+    for (int lanes = 8; lanes <= 32; lanes *= 2)
+        if (size <= 4 * lanes) return {lanes, lanes, 1};
+    if (size <= 1024) return {64, 64, (int)((size + 255) / 256)};
+    if (size > 8192) return {0, 1024, (int)((size + 4095) / 4096)};
+    if (!backward) return {256, 256, (int)((size + 1023) / 1024)};
+    const int ch = size <= 4096 ? 1 : 2;
+    return {0, (int)((size + 256 * ch - 1) / (256 * ch)) * 64, ch};
+}
+// Teams per group in the backward: as many as stay on the chip together, but at least 8
+// rows each, so that the partial sums stay small beside the rows.
+static int64_t slots_of(int64_t size, int64_t groups, int64_t rows) {
+    const Team t = team_of(size, true);
+    const int64_t waves = backward_waves(t.team, t.ch);
+    const int64_t teams = t.team ? 1024 * 64 * waves / t.lanes : 256 * std::max<int64_t>(1, 4 * waves / (t.lanes / 64));
+    return std::max<int64_t>(1, std::min((teams + groups - 1) / groups, (rows + 7) / 8));
 }
 
 template <typename TX, typename TO, int MODE, int TEAM, int CH>
-static void launch_one(bool backward, const NormParams& p, hipStream_t s) {
-    constexpr int PER = block_of(TEAM) / TEAM;
-    const int64_t units = (backward ? p.slots : p.rows) * p.groups;
-    const dim3 grid((unsigned)((units + PER - 1) / PER)), block(block_of(TEAM));
-    if (backward) hipLaunchKernelGGL((norm_backward_kernel<TX, TO, MODE, TEAM, CH>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((norm_forward_kernel<TX, TO, MODE, TEAM, CH>), grid, block, 0, s, p);
+static void launch_one(bool backward, const NormParams& p, int lanes, hipStream_t s) {
+    const int64_t units = (backward ? p.slots : p.rows) * p.groups, per = TEAM ? 256 / (TEAM ? TEAM : 1) : 1;
+    const dim3 grid((unsigned)((units + per - 1) / per)), block(TEAM ? 256 : lanes);
+    if (backward) {
+        if constexpr (TEAM < 256) hipLaunchKernelGGL((norm_backward_kernel<TX, TO, MODE, TEAM, CH>), grid, block, 0, s, p);
+    } else if constexpr (TEAM != 0 || CH > 2) {
+        hipLaunchKernelGGL((norm_forward_kernel<TX, TO, MODE, TEAM, CH>), grid, block, 0, s, p);
+    }
 }
 template <typename TX, typename TO, int MODE> static hipError_t launch_norm(bool backward, const NormParams& p, hipStream_t s) {
-    const Team t = team_of(p.size);
+    const Team t = team_of(p.size, backward);
 #define SSD_NORM_CASE(L, C) \
-    if (t.lanes == L && t.ch == C) launch_one<TX, TO, MODE, L, C>(backward, p, s);
-    SSD_NORM_CASE(8, 1) SSD_NORM_CASE(16, 1) SSD_NORM_CASE(32, 1) SSD_NORM_CASE(64, 1) SSD_NORM_CASE(64, 2)
-    SSD_NORM_CASE(256, 1) SSD_NORM_CASE(256, 2) SSD_NORM_CASE(256, 3) SSD_NORM_CASE(256, 4) SSD_NORM_CASE(256, 5)
-    SSD_NORM_CASE(256, 6) SSD_NORM_CASE(256, 7) SSD_NORM_CASE(256, 8)
-    SSD_NORM_CASE(1024, 3) SSD_NORM_CASE(1024, 4) SSD_NORM_CASE(1024, 5) SSD_NORM_CASE(1024, 6) SSD_NORM_CASE(1024, 7)
-    SSD_NORM_CASE(1024, 8)
+    if (t.team == L && t.ch == C) launch_one<TX, TO, MODE, L, C>(backward, p, t.lanes, s);
+    SSD_NORM_CASE(8, 1) SSD_NORM_CASE(16, 1) SSD_NORM_CASE(32, 1)
+    SSD_NORM_CASE(64, 1) SSD_NORM_CASE(64, 2) SSD_NORM_CASE(64, 3) SSD_NORM_CASE(64, 4)
+    SSD_NORM_CASE(256, 2) SSD_NORM_CASE(256, 3) SSD_NORM_CASE(256, 4) SSD_NORM_CASE(256, 5) SSD_NORM_CASE(256, 6)
+    SSD_NORM_CASE(256, 7) SSD_NORM_CASE(256, 8)
+    SSD_NORM_CASE(0, 1) SSD_NORM_CASE(0, 2) SSD_NORM_CASE(0, 3) SSD_NORM_CASE(0, 4) SSD_NORM_CASE(0, 5) SSD_NORM_CASE(0, 6)
+    SSD_NORM_CASE(0, 7) SSD_NORM_CASE(0, 8)
 #undef SSD_NORM_CASE
     return hipGetLastError();
 }
@@ -329,19 +360,13 @@ int validate(const ssd_norm_problem_t* p, bool gated) {
         if (p->flags != 0 || p->x_dtype != p->dtype || p->group_size != p->channels) return SSD_ERR_UNSUPPORTED;
     }
     // a launch holds fewer than 2^32 lanes
-    if (double(p->rows) * (p->channels / p->group_size) * ssd::team_of(p->group_size).lanes >= 4e9)
+    if (double(std::max<int64_t>(1, p->rows)) * (p->channels / p->group_size) * ssd::team_of(p->group_size, false).lanes >= 4e9)
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 
-// Teams per group in the backward: enough to fill the chip (8 waves per SIMD's worth of
-// lanes over all groups), but at least 8 rows each, so that the partial sums stay small
-// beside the rows themselves.
 int64_t slots_of(const ssd_norm_problem_t* p) {
-    const int lanes = ssd::team_of(p->group_size).lanes;
-    const int64_t groups = p->channels / p->group_size;
-    const int64_t fill = std::max<int64_t>(1, (int64_t(1) << 18) / (lanes * groups));
-    return std::max<int64_t>(1, std::min(fill, (p->rows + 7) / 8));
+    return ssd::slots_of(p->group_size, p->channels / p->group_size, p->rows);
 }
 int64_t backward_bytes(const ssd_norm_problem_t* p, bool scaled) {
     return p->rows == 0 ? 0 : align256(slots_of(p) * p->channels * 4 * (scaled ? 2 : 1));

@@ -18,9 +18,6 @@ constexpr int kTile = 8;
 // values and hands the other half to its partner (swaps of 32 and 16 lanes, then lanes of
 // a row), so four values cost 10 instructions and eight 24, instead of 24 and 48.  Returns,
 // in every lane, the sum of value sum_index<S>(lane).
-template <int CTRL> __device__ inline float dpp_mov(float v) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
-}
 template <int S> __device__ inline int sum_index(int lane) { return S == 4 ? lane >> 4 : (lane >> 3 & 1) + 2 * (lane >> 4); }
 template <int S> __device__ inline float lane_sums(const float (&v)[S], int lane) {
     static_assert(S == 4 || S == 8, "values");

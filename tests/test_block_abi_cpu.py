@@ -103,7 +103,7 @@ def stream(**kw):
     (dict(rows=-1), 2), (dict(channels=0, group_size=1), 2), (dict(group_size=0), 2), (dict(group_size=48), 2),
     (dict(ldx=63), 2), (dict(ldz=63), 2), (dict(eps=-1.0), 2), (dict(eps=float("nan")), 2), (dict(rows=1 << 31), 2),
     (dict(x_dtype=5), 3), (dict(dtype=5), 3), (dict(x_dtype=1, dtype=0), 3),
-    (dict(channels=40000, group_size=40000), 3), (dict(rows=1 << 30, channels=4096, group_size=4096), 3),
+    (dict(channels=40000, group_size=40000), 3), (dict(rows=1 << 24, channels=4096, group_size=4096), 3), (dict(channels=1 << 30, group_size=1), 3),
 ])
 def test_norm_problems(kw, code):
     assert call("ssd_gated_norm_forward", norm(**kw), GF) == code
