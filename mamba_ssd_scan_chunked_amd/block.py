@@ -21,7 +21,10 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import sys
 from typing import Optional
+
+_pkg = sys.modules[__package__]       # its loader, error and buffer checks
 
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
@@ -75,14 +78,12 @@ def _declare(lib):
 
 
 def _lib():
-    from . import load_library
-    return load_library()
+    return _pkg.load_library()
 
 
 def _check(code):
     if code:
-        from . import SSDError
-        raise SSDError(code, _lib().ssd_strerror(code).decode())
+        raise _pkg.SSDError(code, _lib().ssd_strerror(code).decode())
 
 
 def _ptr(t):
@@ -105,8 +106,11 @@ def _on(dev, stream):
 
 
 def _current(dev):
+    """The current stream's handle: straight from torch's binding where it has one, since
+    the stream object that the public call builds takes as long as the launch."""
     import torch
-    return torch.cuda.current_stream(dev).cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev.index) if raw else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _gpu(x):
@@ -142,8 +146,7 @@ def _output(name, t, shape, dtype, dev):
     if t is None:
         import torch
         return torch.empty(shape, dtype=dtype, device=dev)
-    from . import _check_buffer
-    _check_buffer(name, t, shape, dtype, dev)
+    _pkg._check_buffer(name, t, shape, dtype, dev)
     return t
 
 
@@ -171,10 +174,9 @@ def _rows(t):
 
 def _workspace(ws, nbytes, dev):
     import torch
-    from . import _check_workspace
     if ws is None and nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _check_workspace(ws, nbytes, dev)
+    _pkg._check_workspace(ws, nbytes, dev)
     return ws, 0 if ws is None else ws.numel()
 
 
@@ -286,11 +288,10 @@ def causal_conv_step(x, weight, bias, state, y=None, silu: bool = True, state_ou
 def _states(state, state_out, shape, dev):
     """The state a step reads and the one it writes (the same without ``state_out``)."""
     import torch
-    from . import _check_buffer
     if state_out is None:
-        _check_buffer("state", state, shape, torch.float32, dev)
+        _pkg._check_buffer("state", state, shape, torch.float32, dev)
         return state, state
-    _check_buffer("state_out", state_out, shape, torch.float32, dev)
+    _pkg._check_buffer("state_out", state_out, shape, torch.float32, dev)
     return _given("state", state, shape, torch.float32, dev), state_out
 
 

@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstdlib>
 
@@ -37,9 +38,14 @@ inline bool log_enabled() {
     return on;
 }
 
+// Whether there is a device.  A positive answer is kept: devices do not go away, and a call
+// for a single token would otherwise spend a fair share of its time asking.
 inline int check_device() {
+    static std::atomic<bool> found{false};
+    if (found.load(std::memory_order_relaxed)) return SSD_OK;
     int n = 0;
     if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) return SSD_ERR_NO_DEVICE;
+    found.store(true, std::memory_order_relaxed);
     return SSD_OK;
 }
 
