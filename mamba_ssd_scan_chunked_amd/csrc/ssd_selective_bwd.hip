@@ -14,12 +14,17 @@ namespace ssd {
 
 constexpr int kTile = 8;
 
-// Sums over the 64 lanes of S values at once: at every level a lane keeps half of the
-// values and hands the other half to its partner (swaps of 32 and 16 lanes, then lanes of
-// a row), so four values cost 10 instructions and eight 24, instead of 24 and 48.  Returns,
-// in every lane, the sum of value sum_index<S>(lane).
+// Sums over the 64 lanes of S values for each of the tile's eight tokens.  At every level a
+// lane keeps half of what it holds and hands the other half to its partner, so that a level
+// halves the work of the next: a token's values first (swaps of 32 and 16 lanes, for eight
+// values also lanes of a row), then, as tokens come, pairs of tokens, pairs of pairs and the
+// two halves of the tile.  64 sums of four values cost 102 instructions instead of 768.  In
+// the end a lane holds the sum of value sum_index<S>(lane) of token sum_token<S>(lane).
 template <int S> __device__ inline int sum_index(int lane) { return S == 4 ? lane >> 4 : (lane >> 3 & 1) + 2 * (lane >> 4); }
-template <int S> __device__ inline float lane_sums(const float (&v)[S], int lane) {
+template <int S> __device__ inline int sum_token(int lane) {
+    return S == 4 ? (lane >> 3 & 1) + (lane >> 1 & 2) + (lane << 1 & 4) : (lane >> 2 & 1) + (lane & 2) + (lane << 2 & 4);
+}
+template <int S> __device__ inline float value_sums(const float (&v)[S], int lane) {
     static_assert(S == 4 || S == 8, "values");
     float a[S / 2], b[S / 4];
 #pragma unroll
@@ -32,18 +37,54 @@ template <int S> __device__ inline float lane_sums(const float (&v)[S], int lane
         const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a[k]), __float_as_uint(a[k + S / 4]), false, false);
         b[k] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
     }
-    float s;
     if constexpr (S == 8) {
         const bool hi = lane & 8;
-        s = (hi ? b[1] : b[0]) + dpp_mov<0x140>(hi ? b[0] : b[1]);        // row_mirror
+        return (hi ? b[1] : b[0]) + dpp_mov<0x140>(hi ? b[0] : b[1]);     // row_mirror
     } else {
-        s = b[0] + dpp_mov<0x140>(b[0]);
+        return b[0];
     }
-    s += dpp_mov<0x141>(s);                                               // row_half_mirror
-    s += dpp_mov<0xb1>(s);                                                // quad_perm 1,0,3,2
-    s += dpp_mov<0x4e>(s);                                                // quad_perm 2,3,0,1
-    return s;
 }
+// Level L of the tokens: lanes with the bit clear go on with `even`, the others with `odd`.
+template <int S, int L> __device__ inline float token_sums(float even, float odd, int lane) {
+    constexpr int BIT = S == 4 ? 8 >> L : 4 >> L;
+    // the partner: row_mirror, row_half_mirror, quad_perm 3,2,1,0 or 1,0,3,2
+    constexpr int CTRL = BIT == 8 ? 0x140 : (BIT == 4 ? 0x141 : (BIT == 2 ? 0x1b : 0xb1));
+    const bool up = lane & BIT;
+    return (up ? odd : even) + dpp_mov<CTRL>(up ? even : odd);
+}
+// What is kept between tokens: the last unpaired token, pair and half of the tile.
+template <int S> struct TileSums {
+    float token, pair, half, all;
+    template <int I> __device__ inline void forwards(float r, int lane) {
+        if constexpr (I & 1) {
+            r = token_sums<S, 0>(token, r, lane);
+            if constexpr (I & 2) {
+                r = token_sums<S, 1>(pair, r, lane);
+                if constexpr (I & 4) all = token_sums<S, 2>(half, r, lane);
+                else half = r;
+            } else {
+                pair = r;
+            }
+        } else {
+            token = r;
+        }
+    }
+    template <int I> __device__ inline void backwards(float r, int lane) {
+        if constexpr (!(I & 1)) {
+            r = token_sums<S, 0>(r, token, lane);
+            if constexpr (!(I & 2)) {
+                r = token_sums<S, 1>(r, pair, lane);
+                if constexpr (!(I & 4)) all = token_sums<S, 2>(r, half, lane);
+                else half = r;
+            } else {
+                pair = r;
+            }
+        } else {
+            token = r;
+        }
+    }
+    __device__ inline float result() const { return S == 4 ? all + dpp_mov<0xb1>(all) : all; }
+};
 
 __device__ inline int64_t last_tile(const SelPlace& q) { return q.t0 + (q.t1 - q.t0 - 1) / kTile * kTile; }
 
@@ -156,7 +197,7 @@ __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_reverse_loc
 // token (for y, d(step x) and dstep) meet in LDS, the sums over channels (for dB and dC)
 // within the wave and then, over channel blocks, in part_b and part_c.
 template <typename T, int N, int S, bool SEQ>
-__global__ __launch_bounds__((SelShape<N, 64, S>::THREADS)) void sel_reverse_kernel(SelParams p) {
+__global__ __launch_bounds__((SelShape<N, 64, S>::THREADS), (N <= 32 ? 3 : 2)) void sel_reverse_kernel(SelParams p) {
     constexpr int CH = 64, W = N / S, TH = 64 * W, TQ = kTile, J = TQ / W;
     static_assert(W * J == TQ && TH >= TQ * N, "tile shape");     // a B and a C value per thread
     __shared__ float2 su[TQ][CH];
@@ -190,9 +231,10 @@ __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS)) void sel_reverse_ker
     int64_t row = tok * p.D + d;                                          // of the tile in dy, dx, ddt, dz
     const float* dy = p.dy + tok * p.D + q.d0;
     const unsigned col = mine ? lane : q.chans - 1;
-    // part_b and part_c: (block, batch, T, G, N); after lane_sums 64 / S lanes hold a value
-    // each, and keep that of token `hold` of the tile
-    const int hold = lane % (64 / S);
+    // part_b and part_c: (block, batch, T, G, N); the lane's value and token after TileSums
+    // (with four values two lanes hold the same one, and the even lane stores it)
+    const int hold = sum_token<S>(lane);
+    const bool stores = S == 8 || lane % 2 == 0;
     int64_t part = ((((int64_t)q.block * p.batch + q.b) * p.T + first + hold) * p.G + q.g) * N + n0 + sum_index<S>(lane);
     for (int64_t t = first; t >= q.t0; t -= TQ) {
         const int tokens = q.t1 - t < TQ ? (int)(q.t1 - t) : TQ;
@@ -266,14 +308,14 @@ __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS)) void sel_reverse_ker
         SeqBits bits{};
         if (SEQ) bits = seq_bits<TQ>(ids, t, p.T, lane);
 
-        float pr[TQ][S], held = 0.f;
-#pragma unroll
-        for (int i4 = 0; i4 < TQ / 4; ++i4) {
-            const float4 B4 = Bq[i4][n0 + lane % S];
-            const float Bv[4] = {B4.x, B4.y, B4.z, B4.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int i = 4 * i4 + k;
+        float pr[TQ][S], ar[TQ][S];
+        TileSums<S> sums_c, sums_b;
+        float4 B4;
+        static_for<TQ>([&](auto I8) {
+            constexpr int i = decltype(I8)::value;
+            if (i % 4 == 0) B4 = Bq[i / 4][n0 + lane % S];
+            const float Bv = i % 4 == 0 ? B4.x : (i % 4 == 1 ? B4.y : (i % 4 == 2 ? B4.z : B4.w));
+            {
                 if (SEQ && (bits.starts >> i & 1))
                     load_state<S>(p.init ? p.init + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, h);
                 const float2 s = su[i][lane];
@@ -282,26 +324,25 @@ __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS)) void sel_reverse_ker
                 float acc = 0.f, v[S];
                 static_for<S>([&](auto I) {
                     constexpr int n = decltype(I)::value;
-                    pr[i][n] = decay(s.x, A2[n]) * h[n];
-                    h[n] = pr[i][n] + row_lane<n>(Bv[k]) * s.y;
+                    ar[i][n] = decay(s.x, A2[n]);
+                    pr[i][n] = ar[i][n] * h[n];
+                    h[n] = pr[i][n] + row_lane<n>(Bv) * s.y;
                     acc = fmaf(Cv.v[n], h[n], acc);
                     v[n] = g * h[n];
                 });
                 parts[0][w][i][lane] = acc;
-                const float c = lane_sums<S>(v, lane);
-                held = hold == i ? c : held;
+                sums_c.template forwards<i>(value_sums<S>(v, lane), lane);
                 __builtin_amdgcn_sched_barrier(0);       // (hoisting later tokens' decays costs the occupancy)
             }
-        }
-        if (hold < tokens) p.part_c[part] = held;
+        });
+        const float total_c = sums_c.result();
+        if (stores && hold < tokens) p.part_c[part] = total_c;
         // the way back reads the tile from LDS again: without this the compiler keeps every
         // step size and decay of the way out in registers (120 spilled)
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-        for (int i4 = TQ / 4 - 1; i4 >= 0; --i4) {
-#pragma unroll
-            for (int k = 3; k >= 0; --k) {
-                const int i = 4 * i4 + k;
+        static_for<TQ>([&](auto I8) {
+            constexpr int i = TQ - 1 - decltype(I8)::value;
+            {
                 if (SEQ && (bits.ends >> i & 1))
                     load_state<S>(p.dfin ? p.dfin + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, grad);
                 const float2 s = su[i][lane];
@@ -316,18 +357,18 @@ __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS)) void sel_reverse_ker
                     du = fmaf(Bv.v[n], G, du);
                     ds = fmaf(m, A2[n], ds);
                     dA[n] = fmaf(m, s.x, dA[n]);
-                    grad[n] = decay(s.x, A2[n]) * G;
+                    grad[n] = ar[i][n] * G;
                 });
                 parts[1][w][i][lane] = du;
                 parts[2][w][i][lane] = ds;
-                const float c = lane_sums<S>(v, lane);
-                held = hold == i ? c : held;
+                sums_b.template backwards<i>(value_sums<S>(v, lane), lane);
                 if (SEQ && (bits.starts >> i & 1) && p.dinit && mine)
                     store_f32<S>(p.dinit + clamp_id(ids[t + i], p.nseqs) * DN + state, grad);
                 __builtin_amdgcn_sched_barrier(0);
             }
-        }
-        if (hold < tokens) p.part_b[part] = held;
+        });
+        const float total_b = sums_b.result();
+        if (stores && hold < tokens) p.part_b[part] = total_b;
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < J; ++j) {
