@@ -41,7 +41,10 @@ Segments segments_of(const ssd_selective_problem_t* p, bool backward) {
     if (p->segments > 0) {
         n = p->segments;
     } else if (backward) {
-        n = std::min(4096 / items, p->seqlen / 32);
+        // whole rounds of the reverse pass's workgroups, as many as stay on the chip together
+        const int64_t resident = p->dstate == 8 ? 1536 : (p->dstate == 16 ? 768 : (p->dstate == 32 ? 512 : 256));
+        const int64_t rounds = std::max<int64_t>(1, std::min<int64_t>(5, p->seqlen / 32 * items / resident));
+        n = std::min(rounds * resident / items, p->seqlen / 32);
     } else if (items <= 192 && p->seqlen >= 512) {
         n = std::min(4096 / items, p->seqlen / 64);
     }

@@ -197,7 +197,7 @@ __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_reverse_loc
 // token (for y, d(step x) and dstep) meet in LDS, the sums over channels (for dB and dC)
 // within the wave and then, over channel blocks, in part_b and part_c.
 template <typename T, int N, int S, bool SEQ>
-__global__ __launch_bounds__((SelShape<N, 64, S>::THREADS), (N <= 32 ? 3 : 2)) void sel_reverse_kernel(SelParams p) {
+__global__ __launch_bounds__((SelShape<N, 64, S>::THREADS), (N == 32 ? 4 : (N < 32 ? 3 : 2))) void sel_reverse_kernel(SelParams p) {
     constexpr int CH = 64, W = N / S, TH = 64 * W, TQ = kTile, J = TQ / W;
     static_assert(W * J == TQ && TH >= TQ * N, "tile shape");     // a B and a C value per thread
     __shared__ float2 su[TQ][CH];
