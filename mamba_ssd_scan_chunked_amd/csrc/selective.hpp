@@ -114,9 +114,13 @@ template <int TQ> __device__ inline SeqBits seq_bits(const int32_t* ids, int64_t
     return SeqBits{__ballot(first), __ballot(last)};
 }
 
-// A in log2 units: exp(step A) = exp2(step A2).  Kept finite, so that the zero steps that
-// pad a tile leave the state as it is whatever A_log holds.
-__device__ inline float decay_rate(float A_log) { return fmaxf(-expf(A_log) * kLog2e, -3e38f); }
+// A in log2 units: exp(step A) = exp2(step A2).  Kept finite (A_log above 88 counts as 88:
+// any step then decays to nothing), so that the zero steps that pad a tile leave the state
+// as it is; a NaN stays one.
+__device__ inline float decay_rate(float A_log) {
+    const float a = -exp_small(__builtin_amdgcn_fmed3f(A_log, -100.f, 88.f)) * kLog2e;
+    return A_log == A_log ? a : A_log;
+}
 template <int S> __device__ inline void load_decay(const SelParams& p, int64_t d, int64_t N, int n0, float (&A2)[S]) {
     load_f32<S>(p.A_log + d * N + n0, A2);
 #pragma unroll
