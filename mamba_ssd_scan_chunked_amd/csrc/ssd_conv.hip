@@ -26,7 +26,8 @@ struct ConvParams {
     void* y;
     float* fin;
     const float *dy, *dfin;
-    float *dx, *dinit, *part;
+    float *dx, *dinit;
+    float *part, *part_bias;         // runs' sums of dw and dbias, rows of D (K + 1)
     int64_t T, D, nseqs, ldx;
     unsigned nvec, nblk, nrun, L;    // vectors, workgroups over them, runs per row, tokens per run
     int silu;
@@ -295,12 +296,12 @@ template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(64, 3
             if (place < K - 1) ++place;
         }
     }
-    float* part = p.part + (int64_t)q.run * p.D * (K + 1);
+    const int64_t row = (int64_t)q.run * p.D * (K + 1);
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int k = 0; k < K; ++k) part[(q.c0 + v) * K + k] = dw[k][v];
-    store_f32<V>(part + p.D * K + q.c0, db);
+        for (int k = 0; k < K; ++k) p.part[row + (q.c0 + v) * K + k] = dw[k][v];
+    if (p.part_bias) store_f32<V>(p.part_bias + row + q.c0, db);
 }
 
 // One token: a thread per (row, channel); state_out may be state (each element is read
@@ -456,9 +457,10 @@ ssd::ConvParams params_of(const ssd_conv_problem_t* p, const Shape& s) {
     return c;
 }
 
+// A single run writes dw and dbias themselves.
 int64_t backward_bytes(const ssd_conv_problem_t* p) {
-    const Shape s = shape_of(p, true);
-    return p->seqlen == 0 || p->batch == 0 ? 0 : align256(p->batch * s.nrun * p->channels * (p->width + 1) * 4);
+    const int64_t runs = p->batch * shape_of(p, true).nrun;
+    return p->seqlen == 0 || runs <= 1 ? 0 : align256(runs * p->channels * (p->width + 1) * 4);
 }
 
 int done(const char* what, const ssd_conv_problem_t* p, hipError_t e) {
@@ -565,7 +567,9 @@ int ssd_conv_backward(const ssd_conv_problem_t* p, const void* x, const float* w
     c.dfin = dfinal;
     c.dx = dx;
     c.dinit = dinit;
-    c.part = static_cast<float*>(workspace);
+    const bool direct = wsb == 0;
+    c.part = direct ? dweight : static_cast<float*>(workspace);
+    c.part_bias = direct ? dbias : c.part + p->channels * p->width;
     // ids that do not occur keep a zero gradient
     if (seq_idx && dinit) r = ssd::launch_fill(dinit, z.state / 4, st);
     if (r == hipSuccess) {
@@ -576,7 +580,7 @@ int ssd_conv_backward(const ssd_conv_problem_t* p, const void* x, const float* w
             r = s.V == 4 ? ssd::launch_conv_k<float, 4, true>(p->width, c, p->batch, st)
                          : ssd::launch_conv_k<float, 1, true>(p->width, c, p->batch, st);
     }
-    if (r == hipSuccess) {
+    if (r == hipSuccess && !direct) {
         // one row of part per run: D*K weight gradients, then D bias gradients
         ssd::ColumnSums cs{};
         cs.part = c.part;

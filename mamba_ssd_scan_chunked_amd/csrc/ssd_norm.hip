@@ -30,7 +30,9 @@ struct NormParams {
     void* out;
     float* stream;
     const float *dout, *dstream;
-    float *dx, *dz, *part;           // dz: of the gate, or of the residual
+    float *dx, *dz;                  // dz: of the gate, or of the residual
+    float *part, *part_scale;        // teams' sums of dw and dscale, rows of part_stride
+    int64_t part_stride;
     int64_t rows, D, ldx, ldz;
     int size, groups;                // channels per group, groups per row
     int64_t slots;                   // teams per group (backward)
@@ -269,15 +271,12 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024, backward_waves(TEAM, CH)) void n
             }
         }
     }
-    // one row of part per slot: dw, then dscale
-    const bool scaled = MODE == kResidual && p.scale;
-    float* part = p.part + slot * p.D * (scaled ? 2 : 1) + c0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int i = (c * lanes + lane) * kV, n = p.size - i;
         if (n <= 0) continue;
-        store_part(part + i, n, dw[c]);
-        if (scaled) store_part(part + p.D + i, n, ds[c]);
+        store_part(p.part + slot * p.part_stride + c0 + i, n, dw[c]);
+        if (MODE == kResidual && p.scale) store_part(p.part_scale + slot * p.part_stride + c0 + i, n, ds[c]);
     }
 }
 
@@ -368,8 +367,9 @@ int validate(const ssd_norm_problem_t* p, bool gated) {
 int64_t slots_of(const ssd_norm_problem_t* p) {
     return ssd::slots_of(p->group_size, p->channels / p->group_size, p->rows);
 }
+// A single team per group writes dw and dscale themselves.
 int64_t backward_bytes(const ssd_norm_problem_t* p, bool scaled) {
-    return p->rows == 0 ? 0 : align256(slots_of(p) * p->channels * 4 * (scaled ? 2 : 1));
+    return p->rows == 0 || slots_of(p) == 1 ? 0 : align256(slots_of(p) * p->channels * 4 * (scaled ? 2 : 1));
 }
 
 int64_t span(int64_t rows, int64_t ld, int64_t cols, int64_t e) { return rows > 0 ? ((rows - 1) * ld + cols) * e : 0; }
@@ -423,15 +423,23 @@ int done(const char* what, const ssd_norm_problem_t* p, hipError_t e) {
     return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
-// Sums of the teams' dw and dscale; without rows both are zero.
-hipError_t finish(const ssd_norm_problem_t* p, float* dweight, float* dscale, void* workspace, hipStream_t s) {
+// Where the teams' sums go, and their sums over teams.
+void place_sums(const ssd_norm_problem_t* p, ssd::NormParams* n, float* dweight, float* dscale, void* workspace) {
+    n->slots = slots_of(p);
+    const bool direct = n->slots == 1;
+    n->part = direct ? dweight : static_cast<float*>(workspace);
+    n->part_scale = direct ? dscale : n->part + p->channels;
+    n->part_stride = p->channels * (dscale ? 2 : 1);
+}
+hipError_t finish(const ssd_norm_problem_t* p, const ssd::NormParams& n, float* dweight, float* dscale, hipStream_t s) {
+    if (n.slots == 1) return hipSuccess;
     ssd::ColumnSums c{};
-    c.part = static_cast<float*>(workspace);
+    c.part = n.part;
     c.out = dweight;
     c.out2 = dscale;
     c.split = p->channels;
-    c.rows = slots_of(p);
-    c.cols = c.split2 = p->channels * (dscale ? 2 : 1);
+    c.rows = n.slots;
+    c.cols = c.split2 = n.part_stride;
     return ssd::launch_column_sums(c, s);
 }
 
@@ -493,10 +501,9 @@ int ssd_gated_norm_backward(const ssd_norm_problem_t* p, const void* x, const vo
     n.dout = dout;
     n.dx = dx;
     n.dz = dz;
-    n.part = static_cast<float*>(workspace);
-    n.slots = slots_of(p);
+    place_sums(p, &n, dweight, nullptr, workspace);
     hipError_t r = run_gated(p, true, n, s);
-    if (r == hipSuccess) r = finish(p, dweight, nullptr, workspace, s);
+    if (r == hipSuccess) r = finish(p, n, dweight, nullptr, s);
     return done("gated norm backward", p, r);
 }
 
@@ -571,10 +578,9 @@ int ssd_residual_norm_backward(const ssd_norm_problem_t* p, const void* x, const
     n.dstream = dresidual_out;
     n.dx = dx;
     n.dz = dresidual;
-    n.part = static_cast<float*>(workspace);
-    n.slots = slots_of(p);
+    place_sums(p, &n, dweight, scale ? dscale : nullptr, workspace);
     hipError_t r = run_residual(p, true, n, s);
-    if (r == hipSuccess) r = finish(p, dweight, scale ? dscale : nullptr, workspace, s);
+    if (r == hipSuccess) r = finish(p, n, dweight, scale ? dscale : nullptr, s);
     return done("residual norm backward", p, r);
 }
 

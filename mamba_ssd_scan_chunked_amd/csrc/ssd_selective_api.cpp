@@ -142,9 +142,10 @@ BackwardSpace backward_space(const ssd_selective_problem_t* p) {
     w.grad = w.step + align256(n * 4);
     w.ckpt = w.grad + align256(n * p->dstate * 4);
     w.ckpt_step = w.ckpt + align256(tiles * p->dstate * 4);
+    // a single channel block per group writes dB and dC themselves
     w.part_b = w.ckpt_step + align256(tiles * 4);
-    w.part_c = w.part_b + bc;
-    w.sums = w.part_c + bc;
+    w.part_c = w.part_b + (blocks_of(p) > 1 ? bc : 0);
+    w.sums = w.part_c + (blocks_of(p) > 1 ? bc : 0);
     w.total = w.sums + align256(p->batch * sg.n * p->channels * (p->dstate + 2) * 4);
     return w;
 }
@@ -353,8 +354,8 @@ int ssd_selective_backward(const ssd_selective_problem_t* p, const void* x, cons
     k.seg_grad = at<float>(workspace, ws.grad);
     k.ckpt = at<float>(workspace, ws.ckpt);
     k.ckpt_step = at<float>(workspace, ws.ckpt_step);
-    k.part_b = at<float>(workspace, ws.part_b);
-    k.part_c = at<float>(workspace, ws.part_c);
+    k.part_b = k.blocks > 1 ? at<float>(workspace, ws.part_b) : dB;
+    k.part_c = k.blocks > 1 ? at<float>(workspace, ws.part_c) : dC;
     k.part_sums = at<float>(workspace, ws.sums);
     // ids that do not occur keep a zero gradient
     if (seq_idx && dinit) r = ssd::launch_fill(dinit, s.state / 4, st);
@@ -365,7 +366,7 @@ int ssd_selective_backward(const ssd_selective_problem_t* p, const void* x, cons
         if (r == hipSuccess) r = ssd::launch_sel_combine(k, p->dstate, true, st);
     }
     if (r == hipSuccess) r = ssd::launch_sel_reverse(k, p->dtype, p->dstate, st);
-    if (r == hipSuccess) r = ssd::launch_sel_group_sums(k, p->dstate, dB, dC, st);
+    if (r == hipSuccess && k.blocks > 1) r = ssd::launch_sel_group_sums(k, p->dstate, dB, dC, st);
     if (r == hipSuccess) {
         ssd::ColumnSums c{};
         c.part = k.part_sums;

@@ -62,6 +62,7 @@ def test_conv_backward_pointers():
     p = conv(nseqs=3)
     n = ssd.conv_backward_workspace_size(p)
     assert n > 0 and n % 256 == 0 and ssd.conv_backward_workspace_size(conv(seqlen=0)) == 0
+    assert ssd.conv_backward_workspace_size(conv(batch=1, seqlen=4)) == 0           # one run
     ws = (A + 40 * STEP, n)
     for k in ("x", "weight", "dy", "dx", "dweight"):
         assert call("ssd_conv_backward", p, BWD, ws, **{k: None}) == 1
@@ -117,6 +118,8 @@ def test_gated_norm_pointers():
     assert call("ssd_gated_norm_forward", p, GF, x=A + 2) == 4 and call("ssd_gated_norm_forward", p, GF, z=A + 1) == 4
     for k in ("x", "z", "weight"):
         assert call("ssd_gated_norm_forward", p, GF, out=A, **{k: A}) == 6
+    assert ssd.gated_norm_backward_workspace_size(p) == 0                          # few rows: one team per group
+    p = norm(rows=40)
     n = ssd.gated_norm_backward_workspace_size(p)
     ws = (A + 40 * STEP, n)
     assert n > 0 and call("ssd_gated_norm_backward", p, GB, (None, 0)) == 5
@@ -137,6 +140,8 @@ def test_residual_norm_pointers():
     assert call("ssd_residual_norm_forward", p, RF, res_out=A, res=A + 4) == 6     # shifted
     assert call("ssd_residual_norm_forward", stream(ldz=80), RF, res_out=A, res=A) == 6
     assert call("ssd_residual_norm_forward", p, RF, out=A, x=A) == 6
+    assert ssd.residual_norm_backward_workspace_size(p, True) == 0
+    p = stream(rows=40)
     n = ssd.residual_norm_backward_workspace_size(p, True)
     assert n == 2 * ssd.residual_norm_backward_workspace_size(p, False) > 0
     ws = (A + 40 * STEP, n)
@@ -186,8 +191,8 @@ def test_selective_problems(kw, code):
 def test_selective_workspaces():
     assert ssd.selective_workspace_size(sel(seqlen=16)) == 0                       # one tile: not cut
     assert ssd.selective_workspace_size(sel(batch=8, channels=8192)) == 0          # the channels fill the chip
-    p = sel(seqlen=100, segments=3)                                                # 7 tiles of 16: segments of 3
-    assert ssd.selective_workspace_size(p) == 2 * 2 * 64 * 16 * 4 + 2 * 2 * 64 * 4
+    p = sel(seqlen=100, segments=3)                                                # 4 tiles of 32: two segments
+    assert ssd.selective_workspace_size(p) == 2 * 64 * 16 * 4 + 2 * 64 * 4
     assert ssd.selective_backward_workspace_size(sel(seqlen=0)) == 0
     n = ssd.selective_workspace_size(p)
     p.nseqs = 3
