@@ -31,6 +31,7 @@ struct ConvParams {
     int64_t T, D, nseqs, ldx;
     unsigned nvec, nblk, nrun, L;    // vectors, workgroups over them, runs per row, tokens per run
     int silu;
+    int stream;                      // y or dx stored past the caches
 };
 
 // A workgroup is one wave on 64 vectors of V channels and one run of tokens, so that every
@@ -114,7 +115,7 @@ template <int V, int K> __device__ inline void push(float (&win)[K - 1][V], cons
 
 constexpr int kAhead = 4;      // tokens whose loads are issued together
 
-template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(64, 4) void conv_forward_kernel(ConvParams p) {
+template <typename T, int V, int K, bool SEQ, bool STREAM> __device__ inline void conv_forward(const ConvParams& p) {
     const Place q = place_of<V>(p);
     if (!q.active) return;
     const int32_t* ids = SEQ ? p.seq_idx + q.b * p.T : nullptr;
@@ -160,7 +161,7 @@ template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(64, 4
 #pragma unroll
                 for (int v = 0; v < V; ++v) out[v] = silu_for<T>(out[v]);
             }
-            store_f32<V>(y + tt * p.D, out);
+            store_f32<V, STREAM>(y + tt * p.D, out);
             push<V, K>(win, in);
             if (p.fin && (tt == p.T - 1 || (SEQ && ids[tt + 1] != ids[tt]))) {
                 const int64_t seq = SEQ ? clamp_id(ids[tt], p.nseqs) : q.b;
@@ -171,6 +172,11 @@ template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(64, 4
     }
 }
 
+template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(64, 4) void conv_forward_kernel(ConvParams p) {
+    if (p.stream) conv_forward<T, V, K, SEQ, true>(p);
+    else conv_forward<T, V, K, SEQ, false>(p);
+}
+
 // Gradients.  With g[t] = dy[t] silu'(pre[t]), input row r receives
 // sum_j w[K-1-j] g[r+j] over the tokens r+j of its own sequence, and, being one of the
 // sequence's last K-1 inputs, its row of dfinal.  A thread walks its run once, keeping
@@ -179,7 +185,7 @@ template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(64, 4
 // the rows before its run to the run before.  Rows before a sequence's first token are
 // those of its initial state and go to dinit.  dw and dbias are summed per run into
 // `part` (K+1 arrays of runs x D), then over runs in a fixed order.
-template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(64, 3) void conv_backward_kernel(ConvParams p) {
+template <typename T, int V, int K, bool SEQ, bool STREAM> __device__ inline void conv_backward(const ConvParams& p) {
     const Place q = place_of<V>(p);
     if (!q.active) return;
     const int32_t* ids = SEQ ? p.seq_idx + q.b * p.T : nullptr;
@@ -208,7 +214,7 @@ template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(64, 3
     auto emit = [&](int64_t tt, int j, const float (&val)[V]) {
         const int64_t row = tt - j;
         if (place >= j) {
-            if (row >= q.t0 && row < q.t1) store_f32<V>(dx + row * p.D, val);
+            if (row >= q.t0 && row < q.t1) store_f32<V, STREAM>(dx + row * p.D, val);
         } else if (p.dinit && tt - place >= q.t0 && tt - place < q.t1) {
             store_f32<V>(p.dinit + (seq * (K - 1) + K - 1 + place - j) * p.D + q.c0, val);
         }
@@ -302,6 +308,11 @@ template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(64, 3
 #pragma unroll
         for (int k = 0; k < K; ++k) p.part[row + (q.c0 + v) * K + k] = dw[k][v];
     if (p.part_bias) store_f32<V>(p.part_bias + row + q.c0, db);
+}
+
+template <typename T, int V, int K, bool SEQ> __global__ __launch_bounds__(64, 3) void conv_backward_kernel(ConvParams p) {
+    if (p.stream) conv_backward<T, V, K, SEQ, true>(p);
+    else conv_backward<T, V, K, SEQ, false>(p);
 }
 
 // One token: a thread per (row, channel); state_out may be state (each element is read
@@ -512,6 +523,7 @@ int ssd_conv_forward(const ssd_conv_problem_t* p, const void* x, const float* we
     c.seq_idx = seq_idx;
     c.y = y;
     c.fin = final_state;
+    c.stream = z.y > ssd::kStreamBytes;
     hipError_t r;
     if (p->dtype == SSD_DTYPE_BF16)
         r = s.V == 8 ? ssd::launch_conv_k<__bf16, 8, false>(p->width, c, p->batch, st)
@@ -567,6 +579,7 @@ int ssd_conv_backward(const ssd_conv_problem_t* p, const void* x, const float* w
     c.dfin = dfinal;
     c.dx = dx;
     c.dinit = dinit;
+    c.stream = z.f > ssd::kStreamBytes;
     const bool direct = wsb == 0;
     c.part = direct ? dweight : static_cast<float*>(workspace);
     c.part_bias = direct ? dbias : c.part + p->channels * p->width;

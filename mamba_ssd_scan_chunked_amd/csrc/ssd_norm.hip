@@ -28,7 +28,7 @@ struct NormParams {
     const void *x, *z;               // z: the gate, or the residual stream (fp32)
     const float *w, *scale;
     void* out;
-    float* stream;
+    float* res;                      // the residual stream after the addition
     const float *dout, *dstream;
     float *dx, *dz;                  // dz: of the gate, or of the residual
     float *part, *part_scale;        // teams' sums of dw and dscale, rows of part_stride
@@ -37,6 +37,7 @@ struct NormParams {
     int size, groups;                // channels per group, groups per row
     int64_t slots;                   // teams per group (backward)
     float eps;
+    int stream;                      // outputs stored past the caches
 };
 
 constexpr int kV = 4;                // channels per pack
@@ -73,9 +74,9 @@ template <typename T> __device__ inline void load_part(const T* p, int n, float 
         for (int i = 0; i < kV; ++i) v[i] = i < n ? (float)p[i] : 0.f;
     }
 }
-template <typename T> __device__ inline void store_part(T* p, int n, const float (&v)[kV]) {
+template <bool STREAM = false, typename T> __device__ inline void store_part(T* p, int n, const float (&v)[kV]) {
     if (n >= kV) {
-        store_f32<kV>(p, v);
+        store_f32<kV, STREAM>(p, v);
     } else {
 #pragma unroll
         for (int i = 0; i < kV; ++i)
@@ -85,8 +86,8 @@ template <typename T> __device__ inline void store_part(T* p, int n, const float
 
 enum { kGateFirst = 0, kGateAfter = 1, kResidual = 2 };
 // One row (of a group) per team: rows in flight hide each other's latency.
-template <typename TX, typename TO, int MODE, int TEAM, int CH>
-__global__ __launch_bounds__(TEAM ? 256 : 1024) void norm_forward_kernel(NormParams p) {
+template <typename TX, typename TO, int MODE, int TEAM, int CH, bool STREAM>
+__device__ inline void norm_forward(const NormParams& p) {
     __shared__ float red[16];
     const int lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
     const unsigned unit = team_index<TEAM>();
@@ -120,7 +121,7 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void norm_forward_kernel(NormPar
 #pragma unroll
                 for (int v = 0; v < kV; ++v) u[c][v] += gate[c][v];
             }
-            store_part(p.stream + row * p.D + i, n, u[c]);
+            store_part<STREAM>(p.res + row * p.D + i, n, u[c]);
         } else {
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
@@ -142,16 +143,22 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void norm_forward_kernel(NormPar
         load_part(p.w + c0 + i, n, w);
 #pragma unroll
         for (int v = 0; v < kV; ++v) o[v] = u[c][v] * r * w[v] * (MODE == kGateAfter ? gate[c][v] : 1.f);
-        store_part(out + i, n, o);
+        store_part<STREAM>(out + i, n, o);
     }
+}
+
+template <typename TX, typename TO, int MODE, int TEAM, int CH>
+__global__ __launch_bounds__(TEAM ? 256 : 1024) void norm_forward_kernel(NormParams p) {
+    if (p.stream) norm_forward<TX, TO, MODE, TEAM, CH, true>(p);
+    else norm_forward<TX, TO, MODE, TEAM, CH, false>(p);
 }
 
 // Waves per SIMD that the backward is built for (about 45 registers a pack); teams are
 // launched to fill them, and walk the rows.
 constexpr int backward_waves(int team, int ch) { return ch <= 1 ? 5 : (ch <= 2 || team == 0 ? 4 : (ch <= 3 ? 3 : 2)); }
 
-template <typename TX, typename TO, int MODE, int TEAM, int CH>
-__global__ __launch_bounds__(TEAM ? 256 : 1024, backward_waves(TEAM, CH)) void norm_backward_kernel(NormParams p) {
+template <typename TX, typename TO, int MODE, int TEAM, int CH, bool STREAM>
+__device__ inline void norm_backward(const NormParams& p) {
     __shared__ float red[2][16];
     const int lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
     const unsigned team = team_index<TEAM>();
@@ -176,7 +183,7 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024, backward_waves(TEAM, CH)) void n
             if (n <= 0) continue;
             load_part(p.dout + row * p.D + c0 + i, n, ne[c]);
             if constexpr (MODE == kResidual) {
-                load_part(p.stream + row * p.D + i, n, nu[c]);
+                load_part(p.res + row * p.D + i, n, nu[c]);
                 if (p.dstream) load_part(p.dstream + row * p.D + i, n, nz[c]);
                 if (p.scale) load_part((const TX*)p.x + row * p.ldx + i, n, nx[c]);
             } else {
@@ -245,14 +252,14 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024, backward_waves(TEAM, CH)) void n
 #pragma unroll
                     for (int v = 0; v < kV; ++v) du[v] += z[c][v];
                 }
-                store_part(p.dz + row * p.D + i, n, du);
+                store_part<STREAM>(p.dz + row * p.D + i, n, du);
                 if (p.scale) {
 #pragma unroll
                     for (int v = 0; v < kV; ++v) {
                         ds[c][v] = fmaf(du[v], x[c][v], ds[c][v]);
                         du[v] *= g[c][v];
                     }
-                    store_part(p.dx + row * p.D + i, n, du);
+                    store_part<STREAM>(p.dx + row * p.D + i, n, du);
                 }
             } else {
                 if constexpr (MODE == kGateFirst) {
@@ -263,11 +270,11 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024, backward_waves(TEAM, CH)) void n
                         dz[v] = du[v] * x[c][v] * silu_slope(z[c][v], s);
                         du[v] *= z[c][v] * s;
                     }
-                    store_part(p.dz + row * p.D + c0 + i, n, dz);
+                    store_part<STREAM>(p.dz + row * p.D + c0 + i, n, dz);
                 } else {
-                    store_part(p.dz + row * p.D + c0 + i, n, z[c]);
+                    store_part<STREAM>(p.dz + row * p.D + c0 + i, n, z[c]);
                 }
-                store_part(p.dx + row * p.D + c0 + i, n, du);
+                store_part<STREAM>(p.dx + row * p.D + c0 + i, n, du);
             }
         }
     }
@@ -278,6 +285,12 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024, backward_waves(TEAM, CH)) void n
         store_part(p.part + slot * p.part_stride + c0 + i, n, dw[c]);
         if (MODE == kResidual && p.scale) store_part(p.part_scale + slot * p.part_stride + c0 + i, n, ds[c]);
     }
+}
+
+template <typename TX, typename TO, int MODE, int TEAM, int CH>
+__global__ __launch_bounds__(TEAM ? 256 : 1024, backward_waves(TEAM, CH)) void norm_backward_kernel(NormParams p) {
+    if (p.stream) norm_backward<TX, TO, MODE, TEAM, CH, true>(p);
+    else norm_backward<TX, TO, MODE, TEAM, CH, false>(p);
 }
 
 // Lanes per team and packs per lane for a group of `size` channels: a wave or less up to
@@ -294,7 +307,7 @@ static Team team_of(int64_t size, bool backward) {
     for (int lanes = 8; lanes <= 32; lanes *= 2)
         if (size <= 4 * lanes) return {lanes, lanes, 1};
     if (size <= 1024) return {64, 64, (int)((size + 255) / 256)};
-    if (size > 8192) return {0, 1024, (int)((size + 4095) / 4096)};
+    if (size > 8192) return {0, 1024, size <= 16384 ? 4 : 8};
     if (!backward) return {256, 256, (int)((size + 1023) / 1024)};
     const int ch = size <= 4096 ? 1 : 2;
     return {0, (int)((size + 256 * ch - 1) / (256 * ch)) * 64, ch};
@@ -326,8 +339,7 @@ template <typename TX, typename TO, int MODE> static hipError_t launch_norm(bool
     SSD_NORM_CASE(64, 1) SSD_NORM_CASE(64, 2) SSD_NORM_CASE(64, 3) SSD_NORM_CASE(64, 4)
     SSD_NORM_CASE(256, 2) SSD_NORM_CASE(256, 3) SSD_NORM_CASE(256, 4) SSD_NORM_CASE(256, 5) SSD_NORM_CASE(256, 6)
     SSD_NORM_CASE(256, 7) SSD_NORM_CASE(256, 8)
-    SSD_NORM_CASE(0, 1) SSD_NORM_CASE(0, 2) SSD_NORM_CASE(0, 3) SSD_NORM_CASE(0, 4) SSD_NORM_CASE(0, 5) SSD_NORM_CASE(0, 6)
-    SSD_NORM_CASE(0, 7) SSD_NORM_CASE(0, 8)
+    SSD_NORM_CASE(0, 1) SSD_NORM_CASE(0, 2) SSD_NORM_CASE(0, 4) SSD_NORM_CASE(0, 8)
 #undef SSD_NORM_CASE
     return hipGetLastError();
 }
@@ -383,6 +395,7 @@ ssd::NormParams params_of(const ssd_norm_problem_t* p) {
     n.size = (int)p->group_size;
     n.groups = (int)(p->channels / p->group_size);
     n.eps = p->eps;
+    n.stream = p->rows * p->channels * elem_size(p->dtype) > ssd::kStreamBytes;
     return n;
 }
 
@@ -532,7 +545,7 @@ int ssd_residual_norm_forward(const ssd_norm_problem_t* p, const void* x, const 
     n.w = weight;
     n.scale = scale;
     n.out = out;
-    n.stream = residual_out;
+    n.res = residual_out;
     return done("residual norm", p, run_residual(p, false, n, static_cast<hipStream_t>(stream)));
 }
 
@@ -573,7 +586,7 @@ int ssd_residual_norm_backward(const ssd_norm_problem_t* p, const void* x, const
     n.x = x;
     n.w = weight;
     n.scale = scale;
-    n.stream = const_cast<float*>(residual_out);
+    n.res = const_cast<float*>(residual_out);
     n.dout = dout;
     n.dstream = dresidual_out;
     n.dx = dx;
