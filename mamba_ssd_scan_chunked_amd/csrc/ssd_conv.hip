@@ -115,6 +115,12 @@ template <int V, int K> __device__ inline void push(float (&win)[K - 1][V], cons
 
 constexpr int kAhead = 4;      // tokens whose loads are issued together
 
+// Sequence ids of tokens t .. t + kAhead (the row's last one past its end).
+__device__ inline void fetch_ids(const ConvParams& p, const int32_t* ids, int64_t t, int32_t (&id)[kAhead + 1]) {
+#pragma unroll
+    for (int u = 0; u <= kAhead; ++u) id[u] = ids[t + u < p.T ? t + u : p.T - 1];
+}
+
 template <typename T, int V, int K, bool SEQ, bool STREAM> __device__ inline void conv_forward(const ConvParams& p) {
     const Place q = place_of<V>(p);
     if (!q.active) return;
@@ -130,24 +136,29 @@ template <typename T, int V, int K, bool SEQ, bool STREAM> __device__ inline voi
     open_window<T, V, K, SEQ>(p, q, ids, win);
     const T* x = (const T*)p.x + q.b * p.T * p.ldx + q.c0;
     T* y = (T*)p.y + q.b * p.T * p.D + q.c0;
+    // the next tokens' loads are in flight while these are worked on
     Pack<T, V> next[kAhead];
+    int32_t next_id[kAhead + 1], before = SEQ ? ids[q.t0] : 0;
     auto fetch = [&](int64_t t) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
             if (t + u < q.t1) next[u] = load_pack<V>(x + (t + u) * p.ldx);
+        if (SEQ) fetch_ids(p, ids, t, next_id);
     };
     fetch(q.t0);
     for (int64_t t = q.t0; t < q.t1; t += kAhead) {
-        // the next tokens' loads are in flight while these are worked on
         Pack<T, V> raw[kAhead];
+        int32_t id[kAhead + 1];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) raw[u] = next[u];
+#pragma unroll
+        for (int u = 0; u <= kAhead; ++u) id[u] = SEQ ? next_id[u] : 0;
         fetch(t + kAhead);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (t + u >= q.t1) break;
             const int64_t tt = t + u;
-            if (SEQ && tt > q.t0 && ids[tt] != ids[tt - 1]) load_init<V, K>(p, clamp_id(ids[tt], p.nseqs), q.c0, win);
+            if (SEQ && id[u] != (u ? id[u - 1] : before)) load_init<V, K>(p, clamp_id(id[u], p.nseqs), q.c0, win);
             float in[V], out[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -163,12 +174,13 @@ template <typename T, int V, int K, bool SEQ, bool STREAM> __device__ inline voi
             }
             store_f32<V, STREAM>(y + tt * p.D, out);
             push<V, K>(win, in);
-            if (p.fin && (tt == p.T - 1 || (SEQ && ids[tt + 1] != ids[tt]))) {
-                const int64_t seq = SEQ ? clamp_id(ids[tt], p.nseqs) : q.b;
+            if (p.fin && (tt == p.T - 1 || (SEQ && id[u + 1] != id[u]))) {
+                const int64_t seq = SEQ ? clamp_id(id[u], p.nseqs) : q.b;
 #pragma unroll
                 for (int i = 0; i < K - 1; ++i) store_f32<V>(p.fin + (seq * (K - 1) + i) * p.D + q.c0, win[i]);
             }
         }
+        before = id[kAhead - 1];
     }
 }
 
@@ -223,6 +235,7 @@ template <typename T, int V, int K, bool SEQ, bool STREAM> __device__ inline voi
     // the next tokens' loads are in flight while these are worked on
     Pack<T, V> next[kAhead];
     Pack<float, V> next_dy[kAhead];
+    int32_t next_id[kAhead + 1], before = SEQ ? ids[q.t0] : 0;
     auto fetch = [&](int64_t t) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
@@ -230,6 +243,7 @@ template <typename T, int V, int K, bool SEQ, bool STREAM> __device__ inline voi
                 next[u] = load_pack<V>(x + (t + u) * p.ldx);
                 next_dy[u] = load_pack<V>(dy + (t + u) * p.D);
             }
+        if (SEQ) fetch_ids(p, ids, t, next_id);
     };
     fetch(q.t0);
     bool open = true;                     // the run's last sequence goes on past the run
@@ -241,13 +255,16 @@ template <typename T, int V, int K, bool SEQ, bool STREAM> __device__ inline voi
             raw[u] = next[u];
             dyr[u] = next_dy[u];
         }
+        int32_t id[kAhead + 1];
+#pragma unroll
+        for (int u = 0; u <= kAhead; ++u) id[u] = SEQ ? next_id[u] : 0;
         fetch(t + kAhead);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int64_t tt = t + u;
             if (tt >= end || !open) break;
-            if (SEQ && tt > q.t0 && ids[tt] != ids[tt - 1]) {
-                seq = clamp_id(ids[tt], p.nseqs);
+            if (SEQ && id[u] != (u ? id[u - 1] : before)) {
+                seq = clamp_id(id[u], p.nseqs);
                 place = 0;
                 load_init<V, K>(p, seq, q.c0, win);
             }
@@ -274,7 +291,7 @@ template <typename T, int V, int K, bool SEQ, bool STREAM> __device__ inline voi
                 }
             }
             emit(tt, K - 1, acc[K - 1]);
-            const bool last = tt == p.T - 1 || (SEQ && ids[tt + 1] != ids[tt]);
+            const bool last = tt == p.T - 1 || (SEQ && id[u + 1] != id[u]);
             if (last) {
 #pragma unroll
                 for (int j = K - 2; j >= 0; --j) {
@@ -301,6 +318,7 @@ template <typename T, int V, int K, bool SEQ, bool STREAM> __device__ inline voi
             push<V, K>(win, in);
             if (place < K - 1) ++place;
         }
+        before = id[kAhead - 1];
     }
     const int64_t row = (int64_t)q.run * p.D * (K + 1);
 #pragma unroll
