@@ -342,8 +342,8 @@ typedef struct {
     int64_t dstate;     /* N: 8, 16, 32 or 64                                       */
     int64_t ngroups;    /* G: B/C groups; channel d reads group d / (D / G)         */
     int64_t nseqs;      /* number of sequences: == batch without seq_idx            */
-    int64_t ldx, lddt, ldz;   /* elements from one token to the next, >= channels   */
-    int64_t ldb, ldc;         /* the same of B and C, >= ngroups * dstate           */
+    int64_t ldx, lddt, ldz;   /* elements from one token to the next, >= channels, < 2^25 */
+    int64_t ldb, ldc;         /* the same of B and C, >= ngroups * dstate, < 2^25         */
     int32_t dtype;      /* ssd_dtype_t of x, dt, B, C, z and y                      */
     uint32_t flags;     /* SSD_FLAG_DT_SOFTPLUS or 0                                */
     int32_t segments;   /* segments per row, as in ssd_problem_t: 0 lets the library choose */

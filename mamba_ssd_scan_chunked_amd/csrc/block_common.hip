@@ -10,33 +10,35 @@ namespace ssd {
 __global__ __launch_bounds__(1024) void column_sums_kernel(ColumnSums c) {
     __shared__ float acc[16][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t col = (int64_t)blockIdx.x * 64 + lane;
-    const float* src = c.part;
-    float sum = 0.f;
-    if (col < c.cols) {
-        int64_t r = w;
-        for (; r + 7 * 16 < c.rows; r += 8 * 16) {
-            float v[8];
+    for (int64_t first = (int64_t)blockIdx.x * 64; first < c.cols; first += (int64_t)gridDim.x * 64) {
+        const int64_t col = first + lane;
+        float sum = 0.f;
+        if (col < c.cols) {
+            int64_t r = w;
+            for (; r + 7 * 16 < c.rows; r += 8 * 16) {
+                float v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = src[(r + 16 * k) * c.cols + col];
+                for (int k = 0; k < 8; ++k) v[k] = c.part[(r + 16 * k) * c.cols + col];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum += v[k];
+                for (int k = 0; k < 8; ++k) sum += v[k];
+            }
+            for (; r < c.rows; r += 16) sum += c.part[r * c.cols + col];
         }
-        for (; r < c.rows; r += 16) sum += src[r * c.cols + col];
-    }
-    acc[w][lane] = sum;
-    __syncthreads();
-    if (w == 0 && col < c.cols) {
-        float total = 0.f;
+        acc[w][lane] = sum;
+        __syncthreads();
+        if (w == 0 && col < c.cols) {
+            float total = 0.f;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) total += acc[k][lane];
-        if (col < c.split) {
-            if (c.out) c.out[col] = total;
-        } else if (col < c.split2) {
-            if (c.out2) c.out2[col - c.split] = total;
-        } else if (c.out3) {
-            c.out3[col - c.split2] = total;
+            for (int k = 0; k < 16; ++k) total += acc[k][lane];
+            if (col < c.split) {
+                if (c.out) c.out[col] = total;
+            } else if (col < c.split2) {
+                if (c.out2) c.out2[col - c.split] = total;
+            } else if (c.out3) {
+                c.out3[col - c.split2] = total;
+            }
         }
+        __syncthreads();
     }
 }
 
@@ -49,7 +51,8 @@ __global__ __launch_bounds__(256) void copy_kernel(float* dst, const float* src,
 
 hipError_t launch_column_sums(const ColumnSums& c, hipStream_t s) {
     if (c.cols <= 0) return hipSuccess;
-    hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)((c.cols + 63) / 64)), dim3(1024), 0, s, c);
+    const int64_t blocks = (c.cols + 63) / 64;
+    hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(1024), 0, s, c);
     return hipGetLastError();
 }
 static unsigned grid_of(int64_t n) {

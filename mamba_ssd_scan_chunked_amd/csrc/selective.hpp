@@ -6,10 +6,10 @@
 //   step      = dt + dt_bias, or softplus of it;  A = -exp(A_log)
 //
 // The decay differs per channel and state, so there is no C B^T product to put on the
-// matrix units: the work is one exp2 and four multiply-adds per (token, channel, state),
-// and the exp2 takes as many issue cycles as the rest.  A lane therefore owns a channel
-// with S of its N states in registers and walks the tokens; nothing is recomputed per
-// state that is per channel (the step size, its product with x) or per token (B, C).
+// matrix units: the work is one exp2 and four other vector instructions per (token, channel,
+// state).  A lane therefore owns a channel with S of its N states in registers and walks the
+// tokens; nothing is recomputed per state that is per channel (the step size, its product
+// with x) or per token (B, C).
 #pragma once
 #include "block_common.hpp"
 #include "ssd.h"

@@ -7,8 +7,13 @@
 // token, the row of its initial state (K-1 rows, oldest first), or zero.
 //
 // Memory-bound: each thread owns V neighbouring channels and walks a run of tokens with
-// the last K-1 inputs in registers, so x is read once (plus K-1 rows per run, which the
-// neighbouring run has just brought into L2) and y written once.
+// the last K-1 inputs in registers, so x is read once (plus K-1 rows per run) and y written
+// once; the next four tokens' loads are in flight while four are worked on.  Measured on an
+// MI355X, 4 x 4096 tokens of 5376 channels, bf16, K = 4 (a device copy moves 5.0 TB/s): forward
+// 64-74 us for 353 MB, 4.8-5.5 TB/s; backward, packed, with states, 213 us for 887 MB, 4.2
+// TB/s: its 43 vector instructions per element take about half of that time, and 170
+// registers leave three waves per SIMD.  A step of 4 rows takes 2.7 us on the GPU, 10 us with
+// the launch and the binding.
 #include "ssd.h"
 
 #include <algorithm>
@@ -408,7 +413,8 @@ Shape shape_of(const ssd_conv_problem_t* p, bool backward) {
     const int64_t longest = backward ? 128 : 32, resident = (backward ? 3 : 4) * 1024;
     const int64_t columns = std::max<int64_t>(1, p->batch * s.nblk);
     const int64_t least = (p->seqlen + longest - 1) / longest;                      // runs per row
-    const int64_t rounds = (int64_t)(double(least) * double(columns) / resident) + 1;
+    const double all = double(least) * double(columns) / resident;                  // (validate refuses the largest)
+    const int64_t rounds = all < 1e9 ? (int64_t)all + 1 : (int64_t)1e9;
     const int64_t runs = std::max(std::max<int64_t>(1, least), rounds * resident / columns);
     s.L = std::max<int64_t>(4, (p->seqlen + runs - 1) / runs);
     s.nrun = std::max<int64_t>(1, (p->seqlen + s.L - 1) / s.L);

@@ -10,6 +10,17 @@ namespace ssd {
 //     step x once (LDS), and stage B and C as fp32; the next tile's loads are issued then;
 //   - every wave walks the tile with its states and leaves its part of y in LDS;
 //   - the threads share out the pairs again, sum the parts, add D x, gate and store.
+//
+// Bound by vector instructions: per (token, channel) 16 states x 5 (a multiply and an exp2 for
+// the decay, a multiply by the row broadcast of B, two fused multiply-adds) and some 50 for
+// the step size, the gate and the sums.  An instruction issues in about 4.3 cycles and exp2 in
+// 8.6, which makes 0.24 ms for the states alone at 4 x 4096 tokens, 5120 channels, 16 states
+// and 0.37 with the rest; measured 0.46 (bf16, gated, softplus; 674 MB, 1.5 TB/s), as 640
+// workgroups of 32 channels are 2.5 for each of 256 compute units.  Rows whole in 64-channel
+// workgroups of four states a lane take 0.65, in 16-channel waves 0.66, with B and C from LDS
+// per state instead of by row broadcasts 0.79; two buffers and one barrier a tile 0.59.
+// Rows in segments take 64-channel workgroups of four states a lane (16384 tokens of 1536
+// channels: 0.19 ms for the local pass, the combine and the scan; 32-channel ones 0.22).
 template <typename T, int N, int CH, int S, bool SEQ>
 __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_forward_kernel(SelParams p) {
     using Sh = SelShape<N, CH, S>;

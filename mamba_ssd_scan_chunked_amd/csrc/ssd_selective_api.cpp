@@ -69,14 +69,16 @@ int validate(const ssd_selective_problem_t* p) {
         if (ld < p->channels || ld >= kMaxDim) return SSD_ERR_BAD_SHAPE;
     for (int64_t ld : {p->ldb, p->ldc})
         if (ld < gn || ld >= kMaxDim) return SSD_ERR_BAD_SHAPE;
-    // element counts stay far from int64 overflow, and every launch below 2^32 threads
-    const double tokens = double(p->batch) * double(p->seqlen);
-    if (tokens * double(kMaxDim) > 4e18 && tokens * double(std::max(p->ldx, std::max(p->lddt, p->ldz))) > 4e17)
+    // a tile is addressed with 32-bit byte offsets
+    if (std::max({p->ldx, p->lddt, p->ldz, p->ldb, p->ldc, p->channels}) >= int64_t(1) << 25) return SSD_ERR_UNSUPPORTED;
+    // sizes stay far from int64 overflow, and every launch below 2^32 threads
+    const double tokens = double(p->batch) * double(p->seqlen), states = double(p->channels) * p->dstate;
+    if (tokens * states > 1e17 || tokens * (int64_t(1) << 25) > 4e17 || double(p->nseqs) * states > 1e17 ||
+        tokens * gn * double(blocks_of(p)) > 1e17)
         return SSD_ERR_BAD_SHAPE;
-    if (double(p->nseqs) * double(p->channels) * 64 > 4e17) return SSD_ERR_BAD_SHAPE;
     const double items = double(p->batch) * double(p->ngroups) * double(blocks_of(p));
     const double most = std::max(segments_of(p, false).n, segments_of(p, true).n);
-    if (items * most * 256 >= 4e9 || double(p->batch) * p->channels * p->dstate >= 4e9 || tokens * gn / 4 >= 4e9)
+    if (items * most * 512 >= 4e9 || double(p->batch) * states >= 4e9 || tokens * gn / 4 >= 4e9)
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }

@@ -181,6 +181,10 @@ def sel(**kw):
     (dict(ngroups=3), 2), (dict(segments=-1), 2), (dict(nseqs=-1), 2), (dict(seqlen=1 << 31), 2),
     (dict(ldx=63), 2), (dict(lddt=63), 2), (dict(ldz=63), 2), (dict(ldb=15), 2), (dict(ldc=15), 2), (dict(ldx=1 << 31), 2),
     (dict(dtype=3), 3), (dict(dstate=12), 3), (dict(dstate=128), 3),
+    # a tile is addressed with 32-bit byte offsets
+    (dict(ldx=1 << 25), 3), (dict(lddt=1 << 25), 3), (dict(ldz=1 << 25), 3), (dict(ldb=1 << 25), 3), (dict(ldc=1 << 25), 3),
+    (dict(channels=1 << 25), 3),
+    (dict(batch=1 << 30, nseqs=1 << 30, seqlen=1 << 30), 2), (dict(nseqs=1 << 30, channels=1 << 24, dstate=64), 2),
     (dict(batch=1 << 20, nseqs=1 << 20, channels=1 << 14), 3),
 ])
 def test_selective_problems(kw, code):

@@ -251,3 +251,47 @@ def test_another_stream():
         y, f = ssd.causal_conv(d["x"], d["w"], d["bias"], d["init"], stream=handle)
         s.synchronize()
         assert torch.equal(y, y0) and torch.equal(f, f0)
+
+
+def test_offsets_past_32_bits():
+    """A row of more than 2^31 elements: its last tokens equal a run of their own."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("conv long row")
+    T, D, tail = 420000, 5376, 40
+    x = torch.randn(1, 4096, D, device="cuda").to(torch.bfloat16).repeat(1, 103, 1)[:, :T]
+    w, b = torch.randn(D, 4, device="cuda"), torch.randn(D, device="cuda")
+    y, f = ssd.causal_conv(x, w, b)
+    y1, f1 = ssd.causal_conv(x[:, -tail:], w, b, x[:, -tail - 3:-tail].float().contiguous())
+    assert torch.equal(y[:, -tail:], y1) and torch.equal(f, f1)
+    del y
+    dy = torch.zeros(1, T, D, device="cuda")
+    dy[:, -tail:] = torch.randn(1, tail, D, device="cuda")
+    g = ssd.causal_conv_backward(x, w, dy, b)
+    g1 = ssd.causal_conv_backward(x[:, -tail:], w, dy[:, -tail:], b, x[:, -tail - 3:-tail].float().contiguous())
+    assert torch.equal(g["dx"][:, -tail:], g1["dx"]) and torch.equal(g["dx"][:, -tail - 3:-tail], g1["dinit"])
+
+
+def test_arguments_are_checked():
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("conv arguments")
+    x, w = torch.zeros(2, 5, 8, device="cuda"), torch.zeros(8, 4, device="cuda")
+    ok = dict(init_state=torch.zeros(2, 3, 8, device="cuda"))
+    for kind, f in (
+            (TypeError, lambda: ssd.causal_conv(x.half(), w)), (TypeError, lambda: ssd.causal_conv(x, w.bfloat16())),
+            (ValueError, lambda: ssd.causal_conv(x, w[:7])), (ValueError, lambda: ssd.causal_conv(x, w, w[:, 0][:7])),
+            (ValueError, lambda: ssd.causal_conv(x, w.cpu())), (ValueError, lambda: ssd.causal_conv(x[0], w)),
+            (ValueError, lambda: ssd.causal_conv(x, w, init_state=ok["init_state"][:1])),
+            (ValueError, lambda: ssd.causal_conv(x, w, nseqs=3)),
+            (ValueError, lambda: ssd.causal_conv(x, w, seq_idx=torch.zeros(2, 5, dtype=torch.int32, device="cuda"))),
+            (TypeError, lambda: ssd.causal_conv(x, w, seq_idx=torch.zeros(2, 5, device="cuda"), nseqs=2)),
+            (ValueError, lambda: ssd.causal_conv(x, w, y=torch.zeros(2, 8, 5, device="cuda").transpose(1, 2))),
+            (TypeError, lambda: ssd.causal_conv(x, w, y=x.bfloat16())),
+            (ValueError, lambda: ssd.causal_conv(x, w, final_state=torch.zeros(2, 4, 8, device="cuda"))),
+            (ValueError, lambda: ssd.causal_conv_step(x[:, 0], w, None, torch.zeros(2, 8, 3, device="cuda").transpose(1, 2))),
+            (ValueError, lambda: ssd.causal_conv_backward(x, w, x[:1])), (TypeError, lambda: ssd.causal_conv_backward(x, w, x.half())),
+            (ssd.SSDError, lambda: ssd.causal_conv(x, w[:, :1])), (ssd.SSDError, lambda: ssd.causal_conv(x, w, y=x)),
+            (ssd.SSDError, lambda: ssd.causal_conv(x, w, final_state=ok["init_state"], **ok)),
+            (ValueError, lambda: ssd.causal_conv_backward(torch.zeros(8, 300, 8, device="cuda"), w, torch.zeros(8, 300, 8, device="cuda"),
+                                                          workspace=torch.zeros(16, dtype=torch.uint8, device="cuda")))):
+        with pytest.raises(kind):
+            f()

@@ -194,3 +194,40 @@ def test_graph_replays_equal_eager():
         run()
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(outs, eager))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows equal a call of their own."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("norm many rows")
+    M, D, tail = 420000, 5376, 5
+    x = torch.randn(4000, D, device="cuda").repeat(105, 1)
+    z, w = x.to(torch.bfloat16), torch.randn(D, device="cuda")
+    assert torch.equal(ssd.gated_norm(x, z, w)[-tail:], ssd.gated_norm(x[-tail:], z[-tail:], w))
+    out, res = ssd.residual_norm(z, x, w)
+    out1, res1 = ssd.residual_norm(z[-tail:], x[-tail:], w)
+    assert torch.equal(out[-tail:], out1) and torch.equal(res[-tail:], res1)
+    del out
+    g = ssd.residual_norm_backward(z, res, w, x)
+    assert torch.equal(g["dx"][-tail:], ssd.residual_norm_backward(z[-tail:], res1, w, x[-tail:])["dx"])
+
+
+def test_arguments_are_checked():
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("norm arguments")
+    x, w = torch.zeros(6, 8, device="cuda"), torch.ones(8, device="cuda")
+    h = x.bfloat16()
+    for kind, f in (
+            (TypeError, lambda: ssd.gated_norm(x.half(), x, w)), (TypeError, lambda: ssd.gated_norm(x, x.half(), w)),
+            (TypeError, lambda: ssd.gated_norm(x, x, w.bfloat16())), (ValueError, lambda: ssd.gated_norm(x, x[:5], w)),
+            (ValueError, lambda: ssd.gated_norm(x, x, w[:7])), (ValueError, lambda: ssd.gated_norm(x, x.cpu(), w)),
+            (ssd.SSDError, lambda: ssd.gated_norm(x, x, w, group_size=3)), (ssd.SSDError, lambda: ssd.gated_norm(x, x, w, group_size=0)),
+            (ssd.SSDError, lambda: ssd.gated_norm(h, x, w)), (ssd.SSDError, lambda: ssd.gated_norm(x, x, w, eps=-1.0)),
+            (ssd.SSDError, lambda: ssd.gated_norm(x, x.clone(), w, out=x)), (TypeError, lambda: ssd.gated_norm(x, h, w, out=x.clone())),
+            (ValueError, lambda: ssd.gated_norm_backward(x, x, w, x[:5])), (TypeError, lambda: ssd.residual_norm(x, h, w)),
+            (ValueError, lambda: ssd.residual_norm(x, x[:5], w)), (ValueError, lambda: ssd.residual_norm(x, x, w, scale=w[:7])),
+            (ValueError, lambda: ssd.residual_norm(x, x, w, residual_out=x[:5])),
+            (ValueError, lambda: ssd.residual_norm_backward(x, x[:5], w, x)),
+            (TypeError, lambda: ssd.residual_norm_backward(x, x, w, x, dresidual_out=h))):
+        with pytest.raises(kind):
+            f()

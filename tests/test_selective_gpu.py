@@ -341,3 +341,82 @@ def test_long_row_is_split_and_agrees():
     g, g1 = backward(q), backward(q, segments=1)
     for k in g:
         ref.check(g[k], g1[k].cpu(), g1[k].abs().max().item() * 4, 2 * 8 * 64, k)
+
+
+def test_masked_tokens_leave_the_state_alone():
+    """A step that softplus maps to zero (dt of -inf, or the type's lowest value) masks its token."""
+    announce("selective masked tokens")
+    for dt in ("f32", "bf16"):
+        for low in (float("-inf"), torch.finfo(TYPES[dt]).min):
+            q = make(dt, 2, 40, 33, 16, 1, seed=14)
+            q["dt"][0, 3:30], q["dt"][1] = low, low
+            y, f = forward(q)
+            g = backward(q)
+            assert bool(torch.isfinite(y).all()) and torch.equal(f[1].cpu(), q["init"][1])
+            assert all(bool(torch.isfinite(v).all()) for v in g.values())
+            assert not bool(g["ddt"][0, 3:30].any()) and torch.equal(g["dinit"][1].cpu(), check_dinit(q, 1))
+            short = {**q, **{k: torch.cat([q[k][:1, :3], q[k][:1, 30:]], 1) for k in ("x", "dt", "B", "C", "z", "dy")},
+                     "init": q["init"][:1], "dfinal": q["dfinal"][:1], "n": 1}
+            _, f1 = forward(short)
+            ref.check(f[:1], f1.double().cpu(), f1.abs().double().cpu() + 4, 8 * 13, "final")
+
+
+def check_dinit(q, row):
+    """dL/dinit of a row whose steps are all zero: its state is its initial state throughout."""
+    g = (q["dy"][row] * ref.silu(q["z"][row].float())).double()                  # (T, D)
+    want = torch.einsum("td,tn->dn", g, q["C"][row, :, 0].double()) + q["dfinal"][row].double()
+    got = backward(q)["dinit"][row].cpu()
+    size = torch.einsum("td,tn->dn", g.abs(), q["C"][row, :, 0].double().abs()) + q["dfinal"][row].double().abs()
+    ref.check(got, want, size, 40 + 12, "dinit of a masked row")
+    return got
+
+
+def test_offsets_past_32_bits():
+    """A row of more than 2^31 elements: its last tokens equal a run of their own from the state
+    that the steps' decay leaves (steps of 30 forget everything before)."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("selective long row")
+    T, D, N, tail = 264000, 8192, 8, 50
+    x = torch.randn(1, 4000, D, device="cuda").to(torch.bfloat16).repeat(1, 66, 1)
+    dt = torch.full((1, T, D), -3.0, dtype=torch.bfloat16, device="cuda")
+    dt[:, -tail] = 200.0
+    B = torch.randn(1, T, 1, N, device="cuda").to(torch.bfloat16)
+    A_log = torch.zeros(D, N, device="cuda")
+    y, f = ssd.selective_scan(x, dt, A_log, B, B, dt_softplus=True)
+    y1, f1 = ssd.selective_scan(x[:, -tail:], dt[:, -tail:], A_log, B[:, -tail:], B[:, -tail:], dt_softplus=True)
+    # the same products in kernels of other shapes: sums of eight terms in another order.  Both
+    # sides are rounded to bf16: |a - b| <= |a - v| + |v - w| + |w - b| with a half step each
+    # for the first and the last, so the bound has two half steps where check() counts one
+    one, whole = y1.cpu().double(), y[:, -tail:].cpu().double()
+    bound = 2 * ref.U16 * one.abs() + 16 * ref.U32 * (one.abs() + 8 * 200.0)
+    assert bool(((whole - one).abs() <= bound).all())
+    ref.check(f, f1.cpu().double(), f1.cpu().double().abs(), 8, "final")
+
+
+def test_arguments_are_checked():
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("selective arguments")
+    q = make("f32", 2, 6, 8, 8, 1, seed=15)
+    d = {k: gpu(v) for k, v in q.items()}
+
+    def call(x=d["x"], dt=d["dt"], A=d["A_log"], B=d["B"], C=d["C"], **kw):
+        return ssd.selective_scan(x, dt, A, B, C, **kw)
+
+    for kind, f in (
+            (TypeError, lambda: call(x=d["x"].half())), (TypeError, lambda: call(dt=d["dt"].bfloat16())),
+            (TypeError, lambda: call(B=d["B"].bfloat16())), (TypeError, lambda: call(z=d["z"].bfloat16())),
+            (TypeError, lambda: call(A=d["A_log"].bfloat16())), (ValueError, lambda: call(dt=d["dt"][:, :5])),
+            (ValueError, lambda: call(A=d["A_log"][:7])), (ValueError, lambda: call(B=d["B"][:, :5], C=d["C"][:, :5])),
+            (ValueError, lambda: call(C=d["C"][:, :5])), (ValueError, lambda: call(z=d["z"].cpu())),
+            (ValueError, lambda: call(init_state=d["init"][:1])), (ValueError, lambda: call(nseqs=5)),
+            (ValueError, lambda: call(D=d["D"][:7])), (ValueError, lambda: call(y=torch.zeros(2, 6, 9, device="cuda"))),
+            (ValueError, lambda: call(final_state=d["init"][:1])),
+            (ssd.SSDError, lambda: call(segments=-1)), (ssd.SSDError, lambda: call(y=d["x"])),
+            (ssd.SSDError, lambda: call(init_state=d["init"], final_state=d["init"])),
+            (ssd.SSDError, lambda: call(A=d["A_log"][:, :5].contiguous(), B=d["B"][..., :5], C=d["C"][..., :5])),
+            (ValueError, lambda: ssd.selective_scan_backward(d["x"], d["dt"], d["A_log"], d["B"], d["C"], d["dy"][:1])),
+            (ValueError, lambda: ssd.selective_scan_backward(d["x"], d["dt"], d["A_log"], d["B"], d["C"], d["dy"],
+                                                             workspace=torch.zeros(8, dtype=torch.uint8, device="cuda"))),
+            (ValueError, lambda: ssd.selective_step(d["x"][:, 0], d["dt"][:, 0], d["A_log"], d["B"][:, 0], d["C"][:, 0], None, d["init"][:1]))):
+        with pytest.raises(kind):
+            f()
