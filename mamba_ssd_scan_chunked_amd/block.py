@@ -25,6 +25,7 @@ import sys
 from typing import Optional
 
 _pkg = sys.modules[__package__]       # its loader, error and buffer checks
+torch = None                          # imported by the first call, as in the rest of the binding
 
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
@@ -95,7 +96,6 @@ _HERE = contextlib.nullcontext()
 
 def _on(dev, stream):
     """The device and stream a call works on, as a context."""
-    import torch
     if stream is None:
         return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
     if not hasattr(stream, "cuda_stream"):
@@ -108,22 +108,24 @@ def _on(dev, stream):
 def _current(dev):
     """The current stream's handle: straight from torch's binding where it has one, since
     the stream object that the public call builds takes as long as the launch."""
-    import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return raw(dev.index) if raw else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _gpu(x):
-    if x.device.type != "cuda":
+    global torch
+    if torch is None:
+        import torch
+    dev = x.device
+    if dev.type != "cuda":
         raise ValueError("tensors must be on a GPU device")
-    return x.device
+    return dev
 
 
 def _dtype(name, t):
-    import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return DTYPE_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return DTYPE_F32
     raise TypeError("%s must be bfloat16 or float32" % name)
 
@@ -134,17 +136,16 @@ def _given(name, t, shape, dtype, dev):
         return None
     if t.device != dev:
         raise ValueError("%s is on %s, x on %s" % (name, t.device, dev))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _output(name, t, shape, dtype, dev):
     """A caller's output buffer, or a new one."""
     if t is None:
-        import torch
         return torch.empty(shape, dtype=dtype, device=dev)
     _pkg._check_buffer(name, t, shape, dtype, dev)
     return t
@@ -173,7 +174,6 @@ def _rows(t):
 
 
 def _workspace(ws, nbytes, dev):
-    import torch
     if ws is None and nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _pkg._check_workspace(ws, nbytes, dev)
@@ -182,7 +182,6 @@ def _workspace(ws, nbytes, dev):
 
 def _sequences(x, seq_idx, nseqs):
     """(seq_idx, nseqs) of rows x (b,T,...); without ids each row is one sequence."""
-    import torch
     b, T = x.shape[:2]
     if seq_idx is None:
         if nseqs is not None and int(nseqs) != b:
@@ -204,7 +203,6 @@ def conv_backward_workspace_size(p: ConvProblem) -> int:
 
 
 def _conv_arguments(x, weight, bias, init_state, seq_idx, nseqs, silu):
-    import torch
     if x.dim() != 3 or weight.dim() != 2:
         raise ValueError("x must be (b,T,D) and weight (D,K)")
     dev, f32 = x.device, torch.float32
@@ -226,7 +224,6 @@ def causal_conv(x, weight, bias=None, init_state=None, seq_idx=None, nseqs: Opti
     ``seq_idx`` (b,T) with ``nseqs`` packs sequences into rows as in :func:`forward`.
     ``init_state`` and the final state are (nseqs,K-1,D): the K-1 inputs before and at
     the end of each sequence.  Returns (y like x, final_state or None)."""
-    import torch
     dev = _gpu(x)
     with _on(dev, stream):
         p, x, weight, bias, init_state, seq_idx = _conv_arguments(x, weight, bias, init_state, seq_idx, nseqs, silu)
@@ -244,7 +241,6 @@ def causal_conv_backward(x, weight, dy, bias=None, init_state=None, dfinal=None,
     :func:`causal_conv` with the same arguments; dy (b,T,D) and dfinal fp32.  Returns a
     dict of fp32 tensors dx, dweight, dbias, dinit (dbias and dinit at zero when the
     input was not given)."""
-    import torch
     dev = _gpu(x)
     with _on(dev, stream):
         p, x, weight, bias, init_state, seq_idx = _conv_arguments(x, weight, bias, init_state, seq_idx, nseqs, silu)
@@ -267,7 +263,6 @@ def causal_conv_step(x, weight, bias, state, y=None, silu: bool = True, state_ou
     """One token per row through ``ssd_conv_step``: x (b,D), ``state`` (b,K-1,D) fp32,
     updated in place or, with ``state_out``, left as it was and the new state written
     there.  Returns y (b,D)."""
-    import torch
     dev = _gpu(x)
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x must be (b,D) and weight (D,K)")
@@ -287,7 +282,6 @@ def causal_conv_step(x, weight, bias, state, y=None, silu: bool = True, state_ou
 
 def _states(state, state_out, shape, dev):
     """The state a step reads and the one it writes (the same without ``state_out``)."""
-    import torch
     if state_out is None:
         _pkg._check_buffer("state", state, shape, torch.float32, dev)
         return state, state
@@ -331,7 +325,6 @@ def _activation(name, t, shape, like):
 
 def _selective_arguments(x, dt, A_log, B, C, D, z, init_state, seq_idx, nseqs, dt_bias, dt_softplus, segments):
     """(problem, pointers' tensors in the order of the C call up to seq_idx)."""
-    import torch
     if x.dim() != 3 or B.dim() != 4 or A_log.dim() != 2:
         raise ValueError("x must be (b,T,D), B and C (b,T,G,N) and A_log (D,N)")
     dev, f32 = x.device, torch.float32
@@ -365,7 +358,6 @@ def selective_scan(x, dt, A_log, B, C, D=None, z=None, init_state=None, seq_idx=
     A_log (D,N), D, dt_bias (D) fp32; the state (nseqs,D,N) fp32, N one of 8, 16, 32, 64.
     The step size is dt + dt_bias, through softplus with ``dt_softplus``; packed sequences
     and ``segments`` as in :func:`forward`.  Returns (y like x, final_state or None)."""
-    import torch
     dev = _gpu(x)
     with _on(dev, stream):
         p, args = _selective_arguments(x, dt, A_log, B, C, D, z, init_state, seq_idx, nseqs, dt_bias, dt_softplus,
@@ -386,7 +378,6 @@ def selective_scan_backward(x, dt, A_log, B, C, dy, D=None, z=None, init_state=N
     :func:`selective_scan` with the same arguments; dy (b,T,D) and dfinal fp32.  Returns a
     dict of fp32 tensors dx, ddt, dA_log, dB, dC, dD, dinit, ddt_bias and, with z, dz (dD,
     dinit and ddt_bias at zero when the input was not given)."""
-    import torch
     dev, f32 = _gpu(x), torch.float32
     with _on(dev, stream):
         p, args = _selective_arguments(x, dt, A_log, B, C, D, z, init_state, seq_idx, nseqs, dt_bias, dt_softplus,
@@ -413,7 +404,6 @@ def selective_step(x, dt, A_log, B, C, D, state, z=None, y=None, dt_bias=None, d
     """One token per row through ``ssd_selective_step``: x, dt, z (b,D), B, C (b,G,N),
     ``state`` (b,D,N) fp32, updated in place or, with ``state_out``, left as it was and the
     new state written there.  Returns y (b,D)."""
-    import torch
     dev, f32 = _gpu(x), torch.float32
     if x.dim() != 2 or B.dim() != 3 or A_log.dim() != 2:
         raise ValueError("x must be (b,D), B and C (b,G,N) and A_log (D,N)")
@@ -456,7 +446,6 @@ def residual_norm_backward_workspace_size(p: NormProblem, scaled: bool) -> int:
 
 
 def _gated_arguments(x, z, weight, group_size, eps, gate_first):
-    import torch
     dev = x.device
     if x.dim() < 1 or z.shape != x.shape:
         raise ValueError("x and z must have one shape (..., D)")
@@ -490,7 +479,6 @@ def gated_norm_backward(x, z, weight, dout, group_size: Optional[int] = None, ep
                         gate_first: bool = True, workspace=None, stream=None):
     """Gradients of <dout, out> for :func:`gated_norm` through ``ssd_gated_norm_backward``;
     dout fp32.  Returns a dict of fp32 tensors dx, dz, dweight."""
-    import torch
     dev = _gpu(x)
     with _on(dev, stream):
         p, x, z, weight = _gated_arguments(x, z, weight, group_size, eps, gate_first)
@@ -511,7 +499,6 @@ def residual_norm(x, residual, weight, scale=None, eps: float = 1e-5, out=None, 
     root-mean-square norm times weight.  x (..., D); residual (..., D) fp32 or None;
     weight, scale (D) fp32 (scale None: 1).  ``residual_out`` may be ``residual`` (in
     place).  Returns (out in x's type, residual_out fp32)."""
-    import torch
     dev, f32 = _gpu(x), torch.float32
     with _on(dev, stream):
         D = x.shape[-1]
@@ -540,7 +527,6 @@ def residual_norm_backward(x, residual_out, weight, dout, dresidual_out=None, sc
     through ``ssd_residual_norm_backward``, from the residual_out it returned; dout and
     dresidual_out fp32.  Returns a dict of fp32 tensors dx, dresidual, dweight and, with
     a scale, dscale.  Without a scale dx and dresidual are the same values and one tensor."""
-    import torch
     dev, f32 = _gpu(x), torch.float32
     with _on(dev, stream):
         D = x.shape[-1]
