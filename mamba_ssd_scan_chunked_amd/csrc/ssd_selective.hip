@@ -361,8 +361,13 @@ template <typename T, int N, int CH, int S> static void forward_shape(const SelP
     if (p.seq_idx) hipLaunchKernelGGL((sel_forward_kernel<T, N, CH, S, true>), sel_grid(p), block, 0, s, p);
     else hipLaunchKernelGGL((sel_forward_kernel<T, N, CH, S, false>), sel_grid(p), block, 0, s, p);
 }
+// 64-channel workgroups, N/4 states a lane, spend fewer instructions per state; 32-channel ones,
+// N/8 states a lane, give twice the waves where there are fewer than three of the larger for
+// each of 256 compute units.  1024 tokens of 5120 channels, bf16, us with 32 and 64 channels:
+// N = 16: 4 rows (320 workgroups of 64) 132 and 161, 8 rows 223 and 213, 12 rows 310 and 282,
+// 32 rows 748 and 642; N = 64: 4 rows 358 and 419, 8 rows 573 and 623, 12 rows 883 and 806.
 template <typename T, int N> static void forward_n(const SelParams& p, hipStream_t s) {
-    if (p.nseg > 1) forward_shape<T, N, 64, N / 4>(p, s);
+    if (p.nseg > 1 || p.batch * p.G * ((p.per_group + 63) / 64) >= 768) forward_shape<T, N, 64, N / 4>(p, s);
     else forward_shape<T, N, 32, N / 8>(p, s);
 }
 template <typename T, int N, bool CKPT> static void local_n(const SelParams& p0, hipStream_t s) {

@@ -162,6 +162,17 @@ def test_segments_with_larger_states():
             ref.check(got[k], grads[k], sizes[k], 16 * 50 + 200, k)
 
 
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+def test_many_rows(N):
+    """More than three 64-channel workgroups for every compute unit: the wider shape."""
+    announce("selective many rows N=%d" % N)
+    q = make("f32", 800, 3, 20, N, 1, seed=16)
+    (yr, fr), (ys, fs) = reference(q)
+    y, f = forward(q)
+    ref.check(y, yr, ys, 8 * 3 + N + 12, "y")
+    ref.check(f, fr, fs, 8 * 3 + 8, "final")
+
+
 def test_gradients_against_differences():
     announce("selective differences")
     q = make("f32", 1, 24, 12, 8, 2, [[5, 1, 18]], seed=4)
