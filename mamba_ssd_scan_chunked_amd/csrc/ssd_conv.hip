@@ -637,6 +637,7 @@ int ssd_conv_step(const ssd_conv_problem_t* p, const void* x, const float* weigh
     if (p->seqlen != 1 || p->nseqs != p->batch) return SSD_ERR_BAD_SHAPE;
     const int v = validate(p);
     if (v != SSD_OK) return v;
+    if (double(p->batch) * p->channels >= 4e9) return SSD_ERR_UNSUPPORTED;       // a thread per (row, channel)
     if (!weight || (p->batch > 0 && (!x || !state || !state_out || !y))) return SSD_ERR_NULL_POINTER;
     const uintptr_t e = (uintptr_t)elem_size(p->dtype);
     if (misaligned(x, e) || misaligned(y, e) || misaligned(weight, 4) || misaligned(bias, 4) || misaligned(state, 4) ||

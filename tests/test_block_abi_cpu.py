@@ -80,6 +80,7 @@ def test_conv_step_pointers():
     p = conv(seqlen=1)
     assert call("ssd_conv_step", conv(seqlen=2), STP) == 2
     assert call("ssd_conv_step", conv(seqlen=1, nseqs=3), STP) == 2
+    assert call("ssd_conv_step", conv(seqlen=1, batch=1 << 20, channels=1 << 12), STP) == 3      # 2^32 threads
     for k in ("x", "weight", "state", "state_out", "y"):
         assert call("ssd_conv_step", p, STP, **{k: None}) == 1
     assert call("ssd_conv_step", p, STP, state_out=A + 4 * STEP + 4) == 6   # state shifted by a channel
