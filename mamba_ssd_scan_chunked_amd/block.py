@@ -500,6 +500,8 @@ def residual_norm(x, residual, weight, scale=None, eps: float = 1e-5, out=None, 
     weight, scale (D) fp32 (scale None: 1).  ``residual_out`` may be ``residual`` (in
     place).  Returns (out in x's type, residual_out fp32)."""
     dev, f32 = _gpu(x), torch.float32
+    if x.dim() < 1:
+        raise ValueError("x must be (..., D)")
     with _on(dev, stream):
         D = x.shape[-1]
         weight = _given("weight", weight, (D,), f32, dev)
@@ -528,6 +530,8 @@ def residual_norm_backward(x, residual_out, weight, dout, dresidual_out=None, sc
     dresidual_out fp32.  Returns a dict of fp32 tensors dx, dresidual, dweight and, with
     a scale, dscale.  Without a scale dx and dresidual are the same values and one tensor."""
     dev, f32 = _gpu(x), torch.float32
+    if x.dim() < 1:
+        raise ValueError("x must be (..., D)")
     with _on(dev, stream):
         D = x.shape[-1]
         code = _dtype("x", x)

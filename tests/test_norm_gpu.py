@@ -227,6 +227,8 @@ def test_arguments_are_checked():
             (ValueError, lambda: ssd.gated_norm_backward(x, x, w, x[:5])), (TypeError, lambda: ssd.residual_norm(x, h, w)),
             (ValueError, lambda: ssd.residual_norm(x, x[:5], w)), (ValueError, lambda: ssd.residual_norm(x, x, w, scale=w[:7])),
             (ValueError, lambda: ssd.residual_norm(x, x, w, residual_out=x[:5])),
+            (ValueError, lambda: ssd.residual_norm(x[0, 0], None, w)),
+            (ValueError, lambda: ssd.residual_norm_backward(x[0, 0], x[0, 0], w, x[0, 0])),
             (ValueError, lambda: ssd.residual_norm_backward(x, x[:5], w, x)),
             (TypeError, lambda: ssd.residual_norm_backward(x, x, w, x, dresidual_out=h))):
         with pytest.raises(kind):
