@@ -151,11 +151,11 @@ template <int J> __device__ inline void map_steps(float (&v)[J], int soft) {
 }
 
 int64_t sel_ckpt_tile();             // tokens per checkpoint of the backward pass
-hipError_t launch_sel_local(const SelParams& p, int dtype, int64_t N, bool checkpoints, hipStream_t s);
-hipError_t launch_sel_combine(const SelParams& p, int64_t N, bool reverse, hipStream_t s);
+hipError_t launch_sel_local(const SelParams& p, int dtype, int64_t N, hipStream_t s);
+hipError_t launch_sel_combine(const SelParams& p, int64_t N, bool both, hipStream_t s);      // both: backwards too
 hipError_t launch_sel_forward(const SelParams& p, int dtype, int64_t N, hipStream_t s);
 hipError_t launch_sel_step(const SelParams& p, int dtype, int64_t N, hipStream_t s);
-hipError_t launch_sel_reverse_local(const SelParams& p, int dtype, int64_t N, hipStream_t s);
+hipError_t launch_sel_locals(const SelParams& p, int dtype, int64_t N, hipStream_t s);
 hipError_t launch_sel_reverse(const SelParams& p, int dtype, int64_t N, hipStream_t s);
 hipError_t launch_sel_group_sums(const SelParams& p, int64_t N, float* dB, float* dC, hipStream_t s);
 

@@ -156,18 +156,17 @@ __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_forward_ker
 // The scan of one segment without its read-out, from a zero state (the first segment:
 // from the row's initial state): the segment's end state and the sum of its steps, whose
 // decay exp(A sum) is what an incoming state would still weigh; infinite when a sequence
-// starts inside, so that nothing comes through.  For the backward pass (CKPT) the same
-// two are also kept before every tile.  A wave on its own, up to 16 states a lane.
-template <typename T, int N, int CH, int S, bool SEQ, bool CKPT, int TQ>
+// starts inside, so that nothing comes through.  A wave on its own, up to 16 states a lane.
+template <typename T, int N, int CH, int S, bool SEQ>
 __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_local_kernel(SelParams p) {
     using Sh = SelShape<N, CH, S>;
-    constexpr int TH = Sh::THREADS, J = TQ * CH / TH, E = (TQ * N + TH - 1) / TH;
+    constexpr int TQ = 16, TH = Sh::THREADS, J = TQ * CH / TH, E = (TQ * N + TH - 1) / TH;
     static_assert(J * TH == TQ * CH, "tile shape");
     __shared__ float2 su[TQ][CH];
     __shared__ float4 Bs[TQ / 4][N];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const SelPlace q = sel_place<CH>(p);
-    if (!CKPT && q.seg == p.nseg - 1) return;
+    if (q.seg == p.nseg - 1) return;
     const int ch = lane % CH, n0 = (w * Sh::M + lane / CH) * S;
     const bool mine = ch < q.chans;
     const int64_t d = q.d0 + (mine ? ch : q.chans - 1);
@@ -200,14 +199,8 @@ __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_local_kerne
         B += TQ * p.ldb;
     };
     load(q.t1 - q.t0);
-    const int64_t tiles = (p.T + TQ - 1) / TQ;
     for (int64_t t = q.t0; t < q.t1; t += TQ) {
         const int tokens = q.t1 - t < TQ ? (int)(q.t1 - t) : TQ;
-        if (CKPT && mine) {
-            const int64_t at = (q.b * tiles + t / TQ) * p.D + d;
-            store_f32<S>(p.ckpt + at * N + n0, h);
-            if (n0 == 0) p.ckpt_step[at] = sum;
-        }
         __syncthreads();
         float step[J], xk[J];
 #pragma unroll
@@ -253,7 +246,7 @@ __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_local_kerne
             }
         }
     }
-    if (q.seg < p.nseg - 1 && mine) {
+    if (mine) {
         const int64_t at = (q.b * (p.nseg - 1) + q.seg) * p.D + d;
         store_f32<S>(p.seg_state + at * N + n0, h);
         if (n0 == 0) p.seg_step[at] = sum;
@@ -267,7 +260,7 @@ __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_local_kerne
 // 24576 states take 15 us with eight in flight and 13.6 with 32).
 constexpr int kCombineAhead = 32;
 constexpr int kCombineBlock = 64;      // small workgroups: few threads, spread over all units
-template <bool REVERSE> __global__ __launch_bounds__(kCombineBlock) void sel_combine_kernel(SelParams p, int N) {
+template <bool REVERSE> __device__ inline void sel_combine(const SelParams& p, int N) {
     const int64_t DN = p.D * N, i = (int64_t)blockIdx.x * kCombineBlock + threadIdx.x;
     if (i >= p.batch * DN) return;
     const int64_t b = i / DN, e = i % DN;
@@ -296,6 +289,10 @@ template <bool REVERSE> __global__ __launch_bounds__(kCombineBlock) void sel_com
             st[segment(k0 + k) * DN] = carry;
         }
     }
+}
+__global__ __launch_bounds__(kCombineBlock) void sel_combine_kernel(SelParams p, int N) {
+    if (blockIdx.y) sel_combine<true>(p, N);
+    else sel_combine<false>(p, N);
 }
 
 // ---------------------------------------------------------------- step
@@ -370,15 +367,13 @@ template <typename T, int N> static void forward_n(const SelParams& p, hipStream
     if (p.nseg > 1 || p.batch * p.G * ((p.per_group + 63) / 64) >= 768) forward_shape<T, N, 64, N / 4>(p, s);
     else forward_shape<T, N, 32, N / 8>(p, s);
 }
-template <typename T, int N, bool CKPT> static void local_n(const SelParams& p0, hipStream_t s) {
-    constexpr int CH = 64, S = N <= 16 ? N : 16, TQ = CKPT ? 8 : 16;
+template <typename T, int N> static void local_n(const SelParams& p0, hipStream_t s) {
+    constexpr int CH = 64, S = N <= 16 ? N : 16;
     const SelParams p = blocked(p0, CH);
     const dim3 block(SelShape<N, CH, S>::THREADS);
-    if (p.seq_idx) hipLaunchKernelGGL((sel_local_kernel<T, N, CH, S, true, CKPT, TQ>), sel_grid(p), block, 0, s, p);
-    else hipLaunchKernelGGL((sel_local_kernel<T, N, CH, S, false, CKPT, TQ>), sel_grid(p), block, 0, s, p);
+    if (p.seq_idx) hipLaunchKernelGGL((sel_local_kernel<T, N, CH, S, true>), sel_grid(p), block, 0, s, p);
+    else hipLaunchKernelGGL((sel_local_kernel<T, N, CH, S, false>), sel_grid(p), block, 0, s, p);
 }
-
-int64_t sel_ckpt_tile() { return 8; }
 
 hipError_t launch_sel_forward(const SelParams& p, int dtype, int64_t N, hipStream_t s) {
 #define CALL(n) dtype == SSD_DTYPE_BF16 ? forward_n<__bf16, n>(p, s) : forward_n<float, n>(p, s)
@@ -386,18 +381,15 @@ hipError_t launch_sel_forward(const SelParams& p, int dtype, int64_t N, hipStrea
 #undef CALL
     return hipGetLastError();
 }
-hipError_t launch_sel_local(const SelParams& p, int dtype, int64_t N, bool checkpoints, hipStream_t s) {
-#define CALL(n)                                                                                              \
-    checkpoints ? (dtype == SSD_DTYPE_BF16 ? local_n<__bf16, n, true>(p, s) : local_n<float, n, true>(p, s)) \
-                : (dtype == SSD_DTYPE_BF16 ? local_n<__bf16, n, false>(p, s) : local_n<float, n, false>(p, s))
+hipError_t launch_sel_local(const SelParams& p, int dtype, int64_t N, hipStream_t s) {
+#define CALL(n) dtype == SSD_DTYPE_BF16 ? local_n<__bf16, n>(p, s) : local_n<float, n>(p, s)
     SSD_SEL_BY_STATE(N, CALL)
 #undef CALL
     return hipGetLastError();
 }
-hipError_t launch_sel_combine(const SelParams& p, int64_t N, bool reverse, hipStream_t s) {
-    const dim3 grid((unsigned)((p.batch * p.D * N + kCombineBlock - 1) / kCombineBlock)), block(kCombineBlock);
-    if (reverse) hipLaunchKernelGGL(sel_combine_kernel<true>, grid, block, 0, s, p, (int)N);
-    else hipLaunchKernelGGL(sel_combine_kernel<false>, grid, block, 0, s, p, (int)N);
+hipError_t launch_sel_combine(const SelParams& p, int64_t N, bool both, hipStream_t s) {
+    const dim3 grid((unsigned)((p.batch * p.D * N + kCombineBlock - 1) / kCombineBlock), both ? 2 : 1);
+    hipLaunchKernelGGL(sel_combine_kernel, grid, dim3(kCombineBlock), 0, s, p, (int)N);
     return hipGetLastError();
 }
 template <typename T, int N, int R> static void step_rows(SelParams p, hipStream_t s) {

@@ -249,7 +249,7 @@ int ssd_selective_forward(const ssd_selective_problem_t* p, const void* x, const
     if (k.nseg > 1) {
         k.seg_state = at<float>(workspace, 0);
         k.seg_step = at<float>(workspace, ws.step);
-        r = ssd::launch_sel_local(k, p->dtype, p->dstate, false, st);
+        r = ssd::launch_sel_local(k, p->dtype, p->dstate, st);
         if (r == hipSuccess) r = ssd::launch_sel_combine(k, p->dstate, false, st);
     }
     if (r == hipSuccess) r = ssd::launch_sel_forward(k, p->dtype, p->dstate, st);
@@ -361,12 +361,8 @@ int ssd_selective_backward(const ssd_selective_problem_t* p, const void* x, cons
     k.part_sums = at<float>(workspace, ws.sums);
     // ids that do not occur keep a zero gradient
     if (seq_idx && dinit) r = ssd::launch_fill(dinit, s.state / 4, st);
-    if (r == hipSuccess) r = ssd::launch_sel_local(k, p->dtype, p->dstate, true, st);
-    if (k.nseg > 1) {
-        if (r == hipSuccess) r = ssd::launch_sel_combine(k, p->dstate, false, st);
-        if (r == hipSuccess) r = ssd::launch_sel_reverse_local(k, p->dtype, p->dstate, st);
-        if (r == hipSuccess) r = ssd::launch_sel_combine(k, p->dstate, true, st);
-    }
+    if (r == hipSuccess) r = ssd::launch_sel_locals(k, p->dtype, p->dstate, st);
+    if (r == hipSuccess && k.nseg > 1) r = ssd::launch_sel_combine(k, p->dstate, true, st);
     if (r == hipSuccess) r = ssd::launch_sel_reverse(k, p->dtype, p->dstate, st);
     if (r == hipSuccess && k.blocks > 1) r = ssd::launch_sel_group_sums(k, p->dstate, dB, dC, st);
     if (r == hipSuccess) {
