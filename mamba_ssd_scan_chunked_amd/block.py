@@ -323,6 +323,13 @@ def _activation(name, t, shape, like):
     return _rows(t)
 
 
+def _grouped(name, t, shape, like):
+    """The same of B or C, shape (..., G, N): rows of G N channels."""
+    if t.is_contiguous() and t.shape == shape and t.dtype is like.dtype and t.device == like.device:
+        return t, shape[-2] * shape[-1]           # without a view, which takes as long as all checks
+    return _activation(name, t.flatten(-2), (*shape[:-2], shape[-2] * shape[-1]), like)
+
+
 def _selective_arguments(x, dt, A_log, B, C, D, z, init_state, seq_idx, nseqs, dt_bias, dt_softplus, segments):
     """(problem, pointers' tensors in the order of the C call up to seq_idx)."""
     if x.dim() != 3 or B.dim() != 4 or A_log.dim() != 2:
@@ -342,8 +349,8 @@ def _selective_arguments(x, dt, A_log, B, C, D, z, init_state, seq_idx, nseqs, d
     ldz = Dc
     if z is not None:
         z, ldz = _activation("z", z, x.shape, x)
-    B, ldb = _activation("B", B.flatten(-2), (b, T, G * N), x)
-    C, ldc = _activation("C", C.flatten(-2), (b, T, G * N), x)
+    B, ldb = _grouped("B", B, (b, T, G, N), x)
+    C, ldc = _grouped("C", C, (b, T, G, N), x)
     x, ldx = _rows(x)
     p = selective_problem(b, T, Dc, N, G, ns, code, dt_softplus, segments, ldx, lddt, ldz, ldb, ldc)
     return p, (x, dt, dt_bias, A_log, B, C, D, z, init_state, seq_idx)
@@ -418,8 +425,8 @@ def selective_step(x, dt, A_log, B, C, D, state, z=None, y=None, dt_bias=None, d
         ldz = Dc
         if z is not None:
             z, ldz = _activation("z", z, x.shape, x)
-        B, ldb = _activation("B", B.flatten(-2), (b, G * N), x)
-        C, ldc = _activation("C", C.flatten(-2), (b, G * N), x)
+        B, ldb = _grouped("B", B, (b, G, N), x)
+        C, ldc = _grouped("C", C, (b, G, N), x)
         y = _output("y", y, (b, Dc), x.dtype, dev)
         x, ldx = _rows(x)
         p = selective_problem(b, 1, Dc, N, G, b, _dtype("x", x), dt_softplus, 0, ldx, lddt, ldz, ldb, ldc)
