@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 
@@ -27,9 +28,12 @@ int64_t blocks_of(const ssd_selective_problem_t* p) { return (p->channels / p->n
 // an MI355X (2048 tokens, 16 states, bf16) 10 items take 160 us whole and 38 us in segments
 // of 64 tokens, 80 items 158 and 93, 160 items 190 and 158, 240 items 188 and 221; 80 items
 // of 512 tokens 44 and 40, 16 items of 300 tokens 30 and 32.  Backward, the local pass is
-// needed for its checkpoints anyway and the segments only add the reverse one: 10 items 1552
-// us whole and 92 us in segments of 32 tokens, 320 items 1945 and (16 segments) 1101, 640
-// items 2582 and (8 segments) 2122.
+// needed for its checkpoints anyway and the segments only add to it: 10 items 1356 us whole
+// and 69 us in segments of 32 tokens, 80 items 1416 and 279, 320 items 1748 and (12 segments)
+// 947, 640 items 2232 and (six) 1780.  Rows stay whole where they alone fill four fifths of
+// their rounds of resident workgroups (1024 tokens, whole and in segments: 16 states, of 768
+// resident, 1280 items 1684 and 1776 us, 960 items 1493 and 1346; 64 states, of 256, 240
+// items 1221 and 1306, 480 items 2228 and 2511, 320 items 2177 and 1628).
 struct Segments {
     int64_t n, len;
 };
@@ -43,8 +47,11 @@ Segments segments_of(const ssd_selective_problem_t* p, bool backward) {
     } else if (backward) {
         // whole rounds of the reverse pass's workgroups, as many as stay on the chip together
         const int64_t resident = p->dstate == 8 ? 1536 : (p->dstate == 16 ? 768 : (p->dstate == 32 ? 512 : 256));
-        const int64_t rounds = std::max<int64_t>(1, std::min<int64_t>(5, p->seqlen / 32 * items / resident));
-        n = std::min(rounds * resident / items, p->seqlen / 32);
+        const double whole = double(items) / double(resident);
+        if (whole < 0.8 * std::ceil(whole)) {
+            const int64_t rounds = std::max<int64_t>(1, std::min<int64_t>(5, p->seqlen / 32 * items / resident));
+            n = std::min(rounds * resident / items, p->seqlen / 32);
+        }
     } else if (items <= 192 && p->seqlen >= 512) {
         n = std::min(4096 / items, p->seqlen / 64);
     }

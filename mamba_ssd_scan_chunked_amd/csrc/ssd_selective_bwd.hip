@@ -10,10 +10,10 @@
 //
 // Bound by vector instructions (78 % of the reverse pass's cycles issue one): per (token,
 // channel, state) 7 on the way out, 8 on the way back and 4 for the sums over channels.
-// Measured on an MI355X, 8 x 2048 tokens of 1536 channels with 16 states, bf16, gated: 0.62 ms
-// in all, of which the reverse pass 0.43, the local passes 0.10 each and the four small
-// launches 0.03.  Eight states a lane need 128 registers for p alone and spill or run two
-// waves per SIMD (0.8 ms and more); the decays computed again on the way back, 0.69.
+// Measured on an MI355X, 8 x 2048 tokens of 1536 channels with 16 states, bf16, gated: 0.58 ms
+// in all, of which the reverse pass 0.40, the local pass 0.14 and the three small launches
+// 0.03.  Eight states a lane need 128 registers for p alone and spill or run two waves per
+// SIMD (0.8 ms and more); the decays computed again on the way back, 0.69.
 #include "selective.hpp"
 
 namespace ssd {
