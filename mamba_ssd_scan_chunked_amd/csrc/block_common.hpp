@@ -59,15 +59,18 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // e^v for |v| <= 100 from the hardware exp2.  The product v log2(e) is taken as its rounded
-// value and its remainder, so the error does not grow with |v| (about 1e-7 relative).
+// value and its remainder, so the error does not grow with |v| (about 1e-7 relative).  Above
+// 88.72 e^v leaves fp32 and the result is +Inf, without the remainder: Inf times it has
+// either sign, or is NaN.
 __device__ inline float exp_small(float v) {
     const float hi = v * kLog2e;
     const float lo = fmaf(v, 1.925963033500012e-08f, fmaf(v, kLog2e, -hi));
     const float e = __builtin_amdgcn_exp2f(hi);
-    return fmaf(e * lo, kLn2, e);
+    return e < __builtin_inff() ? fmaf(e * lo, kLn2, e) : e;
 }
 
-// 1 / (1 + e^-v); v beyond +-100 counts as +-100 (1 and 4e-44).
+// 1 / (1 + e^-v); v beyond +-100 counts as +-100 (1 and, e^100 being Inf, 0: so the gate of the
+// type's lowest value is 0 and not a rest of it).
 __device__ inline float sigmoid(float v) {
     return __builtin_amdgcn_rcpf(1.f + exp_small(__builtin_amdgcn_fmed3f(-v, -100.f, 100.f)));
 }
