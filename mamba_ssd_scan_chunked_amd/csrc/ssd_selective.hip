@@ -156,7 +156,8 @@ __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_forward_ker
 // The scan of one segment without its read-out, from a zero state (the first segment:
 // from the row's initial state): the segment's end state and the sum of its steps, whose
 // decay exp(A sum) is what an incoming state would still weigh; infinite when a sequence
-// starts inside, so that nothing comes through.  A wave on its own, up to 16 states a lane.
+// starts inside (whatever its own steps are), so that nothing comes through.  A wave on its
+// own, up to 16 states a lane.
 template <typename T, int N, int CH, int S, bool SEQ>
 __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_local_kernel(SelParams p) {
     using Sh = SelShape<N, CH, S>;
@@ -178,6 +179,7 @@ __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_local_kerne
     const int pc = threadIdx.x % CH;
     const float bias = p.dt_bias ? p.dt_bias[q.d0 + (pc < q.chans ? pc : q.chans - 1)] : 0.f;
     float A2[S], h[S], sum = 0.f;
+    bool cut = false;                     // a sequence has started inside
     load_decay<S>(p, d, N, n0, A2);
     const int64_t state = d * N + n0, DN = p.D * N;
     load_state<S>(q.seg == 0 && p.init && !SEQ ? p.init + q.b * DN + state : nullptr, h);
@@ -235,10 +237,11 @@ __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_local_kerne
                 const int i = 4 * i4 + k;
                 if (SEQ && (bits.starts >> i & 1)) {
                     load_state<S>(p.init ? p.init + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, h);
+                    cut = true;
                     sum = __builtin_inff();
                 }
                 const float2 s = su[i][ch];
-                sum += s.x;
+                sum += SEQ && cut ? 0.f : s.x;
                 static_for<S>([&](auto I) {
                     constexpr int n = decltype(I)::value;
                     h[n] = fmaf(decay(s.x, A2[n]), h[n], row_lane<n>(Bv[k]) * s.y);

@@ -98,7 +98,7 @@ __device__ inline int64_t last_tile(const SelPlace& q) { return q.t0 + (q.t1 - q
 // One segment from a zero state (the row's first: from its initial state), eight states a
 // lane.  Kept before every tile, and at the segment's end: the state and the sum of the steps
 // so far, whose decay exp(A sum) is what an incoming state would still weigh; infinite when a
-// sequence starts inside, so that nothing comes through.
+// sequence starts inside (whatever its own steps are), so that nothing comes through.
 // With REV (rows in segments) also what the segment's own tokens send back to its incoming
 // state: the sum over its tokens t of P_t C_t g_t, P_t = exp(step_first A) .. exp(step_t A), plus
 // P dfinal where its sequence ends; it stops before the first sequence that starts inside.
@@ -129,7 +129,8 @@ __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS), 4) void sel_locals_k
         P[n] = 1.f;
         back[n] = 0.f;
     }
-    bool open = REV && q.seg > 0;         // no sequence has started yet
+    bool cut = false;                     // a sequence has started inside
+    bool open = REV && q.seg > 0;         // none has, and there is a segment to send to
     float* sent = open ? p.seg_grad + (q.b * (p.nseg - 1) + q.seg - 1) * DN + state : nullptr;
 
     const int64_t tok = q.b * p.T + q.t0, tiles = (p.T + TQ - 1) / TQ;
@@ -212,13 +213,14 @@ __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS), 4) void sel_locals_k
                 const int i = 4 * i4 + k;
                 if (SEQ && (bits.starts >> i & 1)) {
                     load_state<S>(p.init ? p.init + clamp_id(ids[t + i], p.nseqs) * DN + state : nullptr, h);
+                    cut = true;
                     sum = __builtin_inff();
                     if (open && mine) store_f32<S>(sent, back);
                     open = false;
                 }
                 const float2 s = su[i][lane];
                 const float g = REV ? gs[i][lane] : 0.f;
-                sum += s.x;
+                sum += SEQ && cut ? 0.f : s.x;
                 static_for<S>([&](auto I) {
                     constexpr int n = decltype(I)::value;
                     const float a = decay(s.x, A2[n]);

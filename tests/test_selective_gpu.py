@@ -431,3 +431,22 @@ def test_arguments_are_checked():
             (ValueError, lambda: ssd.selective_step(d["x"][:, 0], d["dt"][:, 0], d["A_log"], d["B"][:, 0], d["C"][:, 0], None, d["init"][:1]))):
         with pytest.raises(kind):
             f()
+
+
+@pytest.mark.parametrize("soft", [True, False])
+def test_bad_steps_stay_in_their_sequence_across_segments(soft):
+    """Segments of 32 tokens; the bad sequence starts in the middle of the second, which the
+    sequence before reaches from the first."""
+    announce("selective no leak across segments softplus=%s" % soft)
+    q = make("f32", 1, 96, 66, 16, 1, [[40, 40, 16]], soft=soft, seed=17)
+    clean, cleang = forward(q, segments=3), backward(q, segments=3)
+    for bad in (float("nan"), float("-inf"), float("inf")):
+        r = {**q, "dt": q["dt"].clone()}
+        r["dt"][:, 50:55] = bad
+        y, f = forward(r, segments=3)
+        g = backward(r, segments=3)
+        for lo, hi in ((0, 40), (80, 96)):
+            assert torch.equal(y[:, lo:hi], clean[0][:, lo:hi]), bad
+            for name in ("dx", "ddt", "dB", "dC", "dz"):
+                assert torch.equal(g[name][:, lo:hi], cleang[name][:, lo:hi]), (bad, name)
+        assert torch.equal(f[[0, 2]], clean[1][[0, 2]]) and torch.equal(g["dinit"][[0, 2]], cleang["dinit"][[0, 2]])
