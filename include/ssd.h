@@ -289,7 +289,7 @@ typedef struct {
     int64_t seqlen;     /* tokens per row (may be 0)                                */
     int64_t channels;   /* D                                                        */
     int64_t nseqs;      /* number of sequences: == batch without seq_idx            */
-    int64_t ldx;        /* elements from one token of x to the next (>= channels)   */
+    int64_t ldx;        /* elements from one token of x to the next, >= channels, < 2^31 */
     int32_t width;      /* K: taps, 2 to 4                                          */
     int32_t dtype;      /* ssd_dtype_t of x and y                                   */
     uint32_t flags;     /* SSD_CONV_*                                               */
@@ -338,12 +338,13 @@ int ssd_conv_step(const ssd_conv_problem_t* p, const void* x, const float* weigh
 typedef struct {
     int64_t batch;      /* rows                                                     */
     int64_t seqlen;     /* tokens per row (may be 0)                                */
-    int64_t channels;   /* D                                                        */
+    int64_t channels;   /* D, < 2^25                                                */
     int64_t dstate;     /* N: 8, 16, 32 or 64                                       */
     int64_t ngroups;    /* G: B/C groups; channel d reads group d / (D / G)         */
     int64_t nseqs;      /* number of sequences: == batch without seq_idx            */
-    int64_t ldx, lddt, ldz;   /* elements from one token to the next, >= channels, < 2^25 */
-    int64_t ldb, ldc;         /* the same of B and C, >= ngroups * dstate, < 2^25         */
+    int64_t ldx, lddt, ldz;   /* elements from one token to the next, >= channels, < 2^25
+                                 (ssd_selective_step: < 2^31)                       */
+    int64_t ldb, ldc;   /* the same of B and C, >= ngroups * dstate                 */
     int32_t dtype;      /* ssd_dtype_t of x, dt, B, C, z and y                      */
     uint32_t flags;     /* SSD_FLAG_DT_SOFTPLUS or 0                                */
     int32_t segments;   /* segments per row, as in ssd_problem_t: 0 lets the library choose */
@@ -406,7 +407,7 @@ typedef struct {
     int64_t rows;
     int64_t channels;     /* D                                                              */
     int64_t group_size;   /* consecutive channels normed together; divides channels; <= 32768 */
-    int64_t ldx;          /* elements from one row of x to the next (>= channels)           */
+    int64_t ldx;          /* elements from one row of x to the next, >= channels, < 2^31    */
     int64_t ldz;          /* the same of z, or of residual                                  */
     float eps;            /* >= 0                                                           */
     int32_t x_dtype;      /* ssd_dtype_t of x                                               */

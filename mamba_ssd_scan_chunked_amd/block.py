@@ -12,8 +12,9 @@ the C ABI in ``include/ssd.h``.
 
 Activations (x, dt, B, C, z, y, out) are bf16 or fp32; parameters, states and gradients are
 fp32.  Activations may be slices of a projection's output (channels contiguous, one
-distance between all tokens): they are read in place.  Anything else that is not
-contiguous is copied first.  A call runs on ``stream`` (a torch stream or a raw
+distance between all tokens, below 2^31 elements, or 2^25 for the selective scan of a
+prompt): they are read in place.  Anything else that is not contiguous is copied first.
+A call runs on ``stream`` (a torch stream or a raw
 handle; None: the current stream of the tensors' device), and so do the copies and
 allocations it makes.
 """
@@ -151,8 +152,12 @@ def _output(name, t, shape, dtype, dev):
     return t
 
 
-def _rows(t):
-    """(t, ld): t (..., channels) as rows ld elements apart, copied if it is not that."""
+FAR = 1 << 31                         # the library takes distances below this,
+FAR_IN_TILE = 1 << 25                 # and below this where a tile has 32-bit offsets
+
+
+def _rows(t, far=FAR):
+    """(t, ld): t (..., channels) as rows ld < ``far`` elements apart, copied if it is not that."""
     D = t.shape[-1]
     if t.is_contiguous():
         return t, D
@@ -168,7 +173,7 @@ def _rows(t):
             if not ld:                          # a broadcast dimension
                 break
         else:
-            if ld >= D:
+            if D <= ld < far:
                 return t, ld
     return t.contiguous(), D
 
@@ -312,7 +317,7 @@ def selective_backward_workspace_size(p: SelectiveProblem) -> int:
     return int(_lib().ssd_selective_backward_workspace_size(ctypes.byref(p)))
 
 
-def _activation(name, t, shape, like):
+def _activation(name, t, shape, like, far):
     """An activation of x's type and device as rows: (t, ld)."""
     if t.device != like.device:
         raise ValueError("%s is on %s, x on %s" % (name, t.device, like.device))
@@ -320,14 +325,14 @@ def _activation(name, t, shape, like):
         raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    return _rows(t)
+    return _rows(t, far)
 
 
-def _grouped(name, t, shape, like):
+def _grouped(name, t, shape, like, far):
     """The same of B or C, shape (..., G, N): rows of G N channels."""
     if t.is_contiguous() and t.shape == shape and t.dtype is like.dtype and t.device == like.device:
         return t, shape[-2] * shape[-1]           # without a view, which takes as long as all checks
-    return _activation(name, t.flatten(-2), (*shape[:-2], shape[-2] * shape[-1]), like)
+    return _activation(name, t.flatten(-2), (*shape[:-2], shape[-2] * shape[-1]), like, far)
 
 
 def _selective_arguments(x, dt, A_log, B, C, D, z, init_state, seq_idx, nseqs, dt_bias, dt_softplus, segments):
@@ -345,13 +350,13 @@ def _selective_arguments(x, dt, A_log, B, C, D, z, init_state, seq_idx, nseqs, d
     init_state = _given("init_state", init_state, (ns, Dc, N), f32, dev)
     if C.shape != B.shape:
         raise ValueError("B and C must have one shape")
-    dt, lddt = _activation("dt", dt, x.shape, x)
+    dt, lddt = _activation("dt", dt, x.shape, x, FAR_IN_TILE)
     ldz = Dc
     if z is not None:
-        z, ldz = _activation("z", z, x.shape, x)
-    B, ldb = _grouped("B", B, (b, T, G, N), x)
-    C, ldc = _grouped("C", C, (b, T, G, N), x)
-    x, ldx = _rows(x)
+        z, ldz = _activation("z", z, x.shape, x, FAR_IN_TILE)
+    B, ldb = _grouped("B", B, (b, T, G, N), x, FAR_IN_TILE)
+    C, ldc = _grouped("C", C, (b, T, G, N), x, FAR_IN_TILE)
+    x, ldx = _rows(x, FAR_IN_TILE)
     p = selective_problem(b, T, Dc, N, G, ns, code, dt_softplus, segments, ldx, lddt, ldz, ldb, ldc)
     return p, (x, dt, dt_bias, A_log, B, C, D, z, init_state, seq_idx)
 
@@ -421,12 +426,12 @@ def selective_step(x, dt, A_log, B, C, D, state, z=None, y=None, dt_bias=None, d
         D = _given("D", D, (Dc,), f32, dev)
         dt_bias = _given("dt_bias", dt_bias, (Dc,), f32, dev)
         state, state_out = _states(state, state_out, (b, Dc, N), dev)
-        dt, lddt = _activation("dt", dt, x.shape, x)
+        dt, lddt = _activation("dt", dt, x.shape, x, FAR)
         ldz = Dc
         if z is not None:
-            z, ldz = _activation("z", z, x.shape, x)
-        B, ldb = _grouped("B", B, (b, G, N), x)
-        C, ldc = _grouped("C", C, (b, G, N), x)
+            z, ldz = _activation("z", z, x.shape, x, FAR)
+        B, ldb = _grouped("B", B, (b, G, N), x, FAR)
+        C, ldc = _grouped("C", C, (b, G, N), x, FAR)
         y = _output("y", y, (b, Dc), x.dtype, dev)
         x, ldx = _rows(x)
         p = selective_problem(b, 1, Dc, N, G, b, _dtype("x", x), dt_softplus, 0, ldx, lddt, ldz, ldb, ldc)

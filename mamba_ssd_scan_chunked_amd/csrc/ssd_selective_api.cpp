@@ -60,7 +60,8 @@ Segments segments_of(const ssd_selective_problem_t* p, bool backward) {
     return {(tiles + per - 1) / per, per * tile};
 }
 
-int validate(const ssd_selective_problem_t* p) {
+// `step`: for the single token, whose kernel takes each element's offset in 64 bits.
+int validate(const ssd_selective_problem_t* p, bool step = false) {
     if (!p) return SSD_ERR_NULL_POINTER;
     if (p->batch < 0 || p->seqlen < 0 || p->channels <= 0 || p->dstate <= 0 || p->ngroups <= 0 || p->nseqs < 0 ||
         p->segments < 0)
@@ -77,10 +78,11 @@ int validate(const ssd_selective_problem_t* p) {
     for (int64_t ld : {p->ldb, p->ldc})
         if (ld < gn || ld >= kMaxDim) return SSD_ERR_BAD_SHAPE;
     // a tile is addressed with 32-bit byte offsets
-    if (std::max({p->ldx, p->lddt, p->ldz, p->ldb, p->ldc, p->channels}) >= int64_t(1) << 25) return SSD_ERR_UNSUPPORTED;
+    const int64_t widest = std::max({p->ldx, p->lddt, p->ldz, p->ldb, p->ldc, p->channels});
+    if ((step ? p->channels : widest) >= int64_t(1) << 25) return SSD_ERR_UNSUPPORTED;
     // sizes stay far from int64 overflow, and every launch below 2^32 threads
     const double tokens = double(p->batch) * double(p->seqlen), states = double(p->channels) * p->dstate;
-    if (tokens * states > 1e17 || tokens * (int64_t(1) << 25) > 4e17 || double(p->nseqs) * states > 1e17 ||
+    if (tokens * states > 1e17 || tokens * double(widest) > 4e17 || double(p->nseqs) * states > 1e17 ||
         tokens * gn * double(blocks_of(p)) > 1e17)
         return SSD_ERR_BAD_SHAPE;
     const double items = double(p->batch) * double(p->ngroups) * double(blocks_of(p));
@@ -268,7 +270,7 @@ int ssd_selective_step(const ssd_selective_problem_t* p, const void* x, const vo
                        const float* state, float* state_out, void* y, void* stream) {
     if (!p) return SSD_ERR_NULL_POINTER;
     if (p->seqlen != 1 || p->nseqs != p->batch) return SSD_ERR_BAD_SHAPE;
-    const int v = validate(p);
+    const int v = validate(p, true);
     if (v != SSD_OK) return v;
     if (!A_log || (p->batch > 0 && (!x || !dt || !B || !C || !state || !state_out || !y))) return SSD_ERR_NULL_POINTER;
     const uintptr_t e = (uintptr_t)elem_size(p->dtype);

@@ -295,3 +295,23 @@ def test_arguments_are_checked():
                                                           workspace=torch.zeros(16, dtype=torch.uint8, device="cuda")))):
         with pytest.raises(kind):
             f()
+
+
+def test_far_apart_rows_are_copied():
+    """Rows 2^31 elements apart and more are copied first."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("conv, rows 2^31 elements apart")
+    D, ld = 40, 1 << 31
+    wide = torch.empty(ld + D, dtype=torch.bfloat16, device="cuda")
+    far = wide.as_strided((2, D), (ld, 1))
+    far.copy_(torch.randn(2, D))
+    x, w = far.contiguous(), torch.randn(D, 4, device="cuda")
+    state = torch.randn(2, 3, D, device="cuda")
+    other = state.clone()
+    assert torch.equal(ssd.causal_conv_step(far, w, None, state), ssd.causal_conv_step(x, w, None, other))
+    assert torch.equal(state, other)
+    assert torch.equal(ssd.causal_conv(far[:, None], w)[0], ssd.causal_conv(x[:, None], w)[0])
+    weight = torch.ones(D, device="cuda")
+    assert torch.equal(ssd.gated_norm(far, far, weight), ssd.gated_norm(x, x, weight))
+    a, c = ssd.residual_norm(far, None, weight), ssd.residual_norm(x, None, weight)
+    assert torch.equal(a[0], c[0]) and torch.equal(a[1], c[1])

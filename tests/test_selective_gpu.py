@@ -450,3 +450,38 @@ def test_bad_steps_stay_in_their_sequence_across_segments(soft):
             for name in ("dx", "ddt", "dB", "dC", "dz"):
                 assert torch.equal(g[name][:, lo:hi], cleang[name][:, lo:hi]), (bad, name)
         assert torch.equal(f[[0, 2]], clean[1][[0, 2]]) and torch.equal(g["dinit"][[0, 2]], cleang["dinit"][[0, 2]])
+
+
+def test_last_tokens_of_long_prompts():
+    """A step on ``hidden[:, -1]``: rows are a whole prompt apart, here 2^25 elements and more."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("selective step, rows 2^25 elements apart")
+    b, T, D, N = 2, 8192, 5120, 16
+    wide = torch.randn(b, T, D, device="cuda", dtype=torch.bfloat16)
+    x, dt, z = (wide[:, -k] for k in (1, 2, 3))
+    B, C = (wide[:, -k, :N].unflatten(-1, (1, N)) for k in (4, 5))
+    assert all(t.stride(0) >= 1 << 25 for t in (x, dt, z, B, C))
+    A, skip = torch.rand(D, N, device="cuda"), torch.randn(D, device="cuda")
+    state = torch.randn(b, D, N, device="cuda")
+    other = state.clone()
+    y = ssd.selective_step(x, dt, A, B, C, skip, state, z, dt_softplus=True)
+    want = ssd.selective_step(*[t.contiguous() for t in (x, dt, A, B, C)], skip, other, z.contiguous(), dt_softplus=True)
+    assert torch.equal(y, want) and torch.equal(state, other)
+
+
+def test_far_apart_tokens_are_copied():
+    """The prompt calls read tokens up to 2^25 elements apart in place; past that they are copied."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("selective prompt, tokens 2^25 elements apart")
+    T, D, N, ld = 9, 70, 8, 1 << 25
+    wide = torch.zeros((T - 1) * ld + D, dtype=torch.bfloat16, device="cuda")
+    far = wide.as_strided((1, T, D), (T * ld, ld, 1))
+    far.copy_(torch.randn(1, T, D))
+    B = far[..., :N].unflatten(-1, (1, N))
+    A, dy = torch.rand(D, N, device="cuda"), torch.randn(1, T, D, device="cuda")
+    y, f = ssd.selective_scan(far, far, A, B, B, z=far, dt_softplus=True)
+    g = ssd.selective_scan_backward(far, far, A, B, B, dy, z=far, dt_softplus=True)
+    x, B = far.contiguous(), B.contiguous()
+    y1, f1 = ssd.selective_scan(x, x, A, B, B, z=x, dt_softplus=True)
+    g1 = ssd.selective_scan_backward(x, x, A, B, B, dy, z=x, dt_softplus=True)
+    assert torch.equal(y, y1) and torch.equal(f, f1) and all(torch.equal(g[k], g1[k]) for k in g)
