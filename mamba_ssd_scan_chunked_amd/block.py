@@ -422,6 +422,8 @@ def selective_step(x, dt, A_log, B, C, D, state, z=None, y=None, dt_bias=None, d
     with _on(dev, stream):
         b, Dc = x.shape
         G, N = B.shape[1:]
+        if C.shape != B.shape:
+            raise ValueError("B and C must have one shape")
         A_log = _given("A_log", A_log, (Dc, N), f32, dev)
         D = _given("D", D, (Dc,), f32, dev)
         dt_bias = _given("dt_bias", dt_bias, (Dc,), f32, dev)

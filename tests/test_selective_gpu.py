@@ -485,3 +485,14 @@ def test_far_apart_tokens_are_copied():
     y1, f1 = ssd.selective_scan(x, x, A, B, B, z=x, dt_softplus=True)
     g1 = ssd.selective_scan_backward(x, x, A, B, B, dy, z=x, dt_softplus=True)
     assert torch.equal(y, y1) and torch.equal(f, f1) and all(torch.equal(g[k], g1[k]) for k in g)
+
+
+def test_shapes_of_a_step():
+    """B and C of a step are (b,G,N) both, not merely of as many values."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("selective step shapes")
+    q = make("f32", 2, 1, 16, 8, 2, seed=18)
+    d = {k: gpu(v[:, 0] if k in ("x", "dt", "B", "C") else v) for k, v in q.items() if k in ("x", "dt", "A_log", "B", "C", "init")}
+    for C in (d["C"].transpose(1, 2), d["C"].reshape(2, 1, 16), d["C"].reshape(2, 16), d["C"][0, 0], d["C"][:1]):
+        with pytest.raises(ValueError):
+            ssd.selective_step(d["x"], d["dt"], d["A_log"], d["B"], C, None, d["init"].clone())
