@@ -44,6 +44,7 @@
 extern "C" {
 #endif
 
+/* Raised when a call or a struct that was there changes; calls are added without. */
 #define SSD_ABI_VERSION 5
 
 /* Element type of x, B and C.  dt, A_log, D, init_state, y and final_state are

@@ -82,6 +82,19 @@ def load_library():
     if not os.path.exists(path):
         raise ImportError("%s is not built; run `python -m mamba_ssd_scan_chunked_amd.build`" % path)
     lib = ctypes.CDLL(path)
+    lib.ssd_version.restype = ctypes.c_int
+    if lib.ssd_version() != ABI_VERSION:
+        raise ImportError("%s has ABI %d, this binding needs %d: rebuild it" % (path, lib.ssd_version(), ABI_VERSION))
+    try:
+        _declare(lib)
+    except AttributeError as e:           # entry points were added without a change to those before
+        raise ImportError("%s is older than this binding (%s): rebuild it" % (path, e)) from None
+    _lib = lib
+    return lib
+
+
+def _declare(lib):
+    """Argument types of the library's entry points."""
     P = ctypes.POINTER(Problem)
     vp, sz = ctypes.c_void_p, ctypes.c_size_t
     lib.ssd_validate.argtypes = [P]
@@ -103,11 +116,6 @@ def load_library():
     _block._declare(lib)
     lib.ssd_strerror.argtypes = [ctypes.c_int]
     lib.ssd_strerror.restype = ctypes.c_char_p
-    lib.ssd_version.restype = ctypes.c_int
-    if lib.ssd_version() != ABI_VERSION:
-        raise ImportError("%s has ABI %d, this binding needs %d: rebuild it" % (path, lib.ssd_version(), ABI_VERSION))
-    _lib = lib
-    return lib
 
 
 def version() -> int:

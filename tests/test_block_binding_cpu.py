@@ -7,6 +7,35 @@ import mamba_ssd_scan_chunked_amd as ssd
 from mamba_ssd_scan_chunked_amd import block
 
 
+class Older:
+    """The library as it was before the operators around the scan, or of another version."""
+
+    def __init__(self, version):
+        self._lib, self._version = ctypes.CDLL(ssd.library_path()), version
+
+    def __getattr__(self, name):
+        if name == "ssd_version":
+            class Version:
+                restype = None
+
+                def __call__(this):
+                    return self._version
+            return Version()
+        if name.startswith(("ssd_conv", "ssd_selective", "ssd_gated", "ssd_residual")):
+            raise AttributeError("undefined symbol: " + name)
+        return getattr(self._lib, name)
+
+
+@pytest.mark.parametrize("version", [5, 4])
+def test_an_older_library_asks_for_a_rebuild(monkeypatch, version):
+    older = Older(version)
+    monkeypatch.setattr(ssd, "_lib", None)
+    monkeypatch.setattr(ssd.ctypes, "CDLL", lambda path: older)
+    with pytest.raises(ImportError, match="rebuild it"):
+        ssd.load_library()
+    assert ssd._lib is None
+
+
 def test_a_step_takes_rows_any_distance_apart():
     """The step has no tile, so the prompt calls' bound on its offsets is not its own.  A batch
     of no rows gets past every check (and, without a device, no further)."""
