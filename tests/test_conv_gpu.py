@@ -297,6 +297,55 @@ def test_arguments_are_checked():
             f()
 
 
+LONG = [
+    # dtype, rows, tokens, channels, K.  Forward runs of 10 and 20 tokens (4096 waves over 64 and
+    # 72 of the channels' and rows' workgroups), backward of 25 and 27 (3072 over 128 and 72).
+    ("bf16", 16, 600, 2048, 4), ("f32", 8, 1111, 2052, 3),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "%s-b%d-T%d-D%d-K%d" % c)
+def test_packed_rows_in_long_runs(case):
+    """Runs of several groups of four tokens: sequences that start and end in any token of a
+    group and of a run, several of them in a run, and some over several runs."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    dt, b, T, D, K = case
+    announce("conv long runs %s" % (case,))
+    g = torch.Generator().manual_seed(T)
+    lens = []
+    for _ in range(b):
+        row, left = [], T
+        while left:
+            longest = (3, 12, 200)[int(torch.randint(3, (1,), generator=g))]
+            row.append(min(left, 1 + int(torch.randint(longest, (1,), generator=g))))
+            left -= row[-1]
+        lens.append(row)
+    q = make(dt, b, T, D, K, lens, True, True, seed=T)
+    d = {k: gpu(v) for k, v in q.items()}
+    runs = ssd.conv_backward_workspace_size(ssd.conv_problem(b, T, D, K, q["n"], ssd.DTYPE_BF16 if dt == "bf16" else ssd.DTYPE_F32)) \
+        // (D * (K + 1) * 4)
+    assert T * b >= 24 * runs, "backward runs are shorter than this test is about"
+    y, f = ssd.causal_conv(d["x"], d["w"], d["bias"], d["init"], d["ids"], q["n"])
+    args = [d[k].double() for k in ("x", "w", "bias", "init")]
+    yr, fr = ref.conv(*args, lens, True)
+    size, _ = ref.conv(*[t.abs() for t in args], lens, False)
+    # as in test_forward
+    ref.check(y, yr.cpu(), size.cpu(), 1.1 * K + 8, "y")
+    assert torch.equal(f.double(), fr)
+
+    got = ssd.causal_conv_backward(d["x"], d["w"], d["dy"], d["bias"], d["init"], d["dfinal"], d["ids"], q["n"])
+    lv = [t.detach().requires_grad_() for t in args]
+    y, f = ref.conv(*lv, lens, True)
+    grads = torch.autograd.grad((y * d["dy"].double()).sum() + (f * d["dfinal"].double()).sum(), lv)
+    av = [t.detach().abs().requires_grad_() for t in args]
+    ya, fa = ref.conv(*av, lens, False)
+    scales = torch.autograd.grad((1.1 * ya * d["dy"].double().abs()).sum() + (fa * d["dfinal"].double().abs()).sum(), av)
+    # as in test_backward, with K U32 size(pre) / 2 from the slope's argument for the largest size here
+    n = K * float(ya.detach().max()) / 2 + K + 8
+    for name, r, s, extra in zip(("dx", "dweight", "dbias", "dinit"), grads, scales, (0, 96 + runs / 16, 96 + runs / 16, 0)):
+        ref.check(got[name], r.cpu(), s.cpu(), n + extra, name)
+
+
 def test_far_apart_rows_are_copied():
     """Rows 2^31 elements apart and more are copied first."""
     import mamba_ssd_scan_chunked_amd as ssd
