@@ -48,11 +48,12 @@ template <int V, bool STREAM = false, typename T> __device__ inline void store_f
     else store_pack<V>(p, r);
 }
 
-// Outputs above the eight L2 caches' 32 MB are stored non-temporally: the next kernel would
-// not find them there anyway, and they no longer push out what this one still reads (4 x
-// 4096 tokens of 5376 channels convolved: 66 us against 78; gated norm of 16384 rows of
-// 5120: 134 against 154, its gradients for 8192 rows: 147 against 172).  Smaller ones stay
-// in L2 for the kernel that reads them.
+// A call whose largest output is above the eight L2 caches' 32 MB stores non-temporally: the
+// next kernel would not find it there anyway, and it no longer pushes out what this one still
+// reads (4 x 4096 tokens of 5376 channels convolved: 66 us against 78; gated norm of 16384 rows
+// of 5120: 134 against 154, its gradients for 8192 rows: 147 against 172; just above the border,
+// 40 MB of stream of 4096 rows of 2560: 20 against 24, and 44 against 49 with the norm after it
+// that reads the stream).  Smaller ones stay in L2 for the kernel that reads them.
 constexpr int64_t kStreamBytes = int64_t(32) << 20;
 
 constexpr float kLog2e = 1.4426950408889634f;

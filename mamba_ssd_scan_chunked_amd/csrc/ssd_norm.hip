@@ -391,7 +391,8 @@ int64_t backward_bytes(const ssd_norm_problem_t* p, bool scaled) {
 
 int64_t span(int64_t rows, int64_t ld, int64_t cols, int64_t e) { return rows > 0 ? ((rows - 1) * ld + cols) * e : 0; }
 
-ssd::NormParams params_of(const ssd_norm_problem_t* p) {
+// out_size: bytes of an element of the largest output.
+ssd::NormParams params_of(const ssd_norm_problem_t* p, int64_t out_size) {
     ssd::NormParams n{};
     n.rows = p->rows;
     n.D = p->channels;
@@ -400,7 +401,7 @@ ssd::NormParams params_of(const ssd_norm_problem_t* p) {
     n.size = (int)p->group_size;
     n.groups = (int)(p->channels / p->group_size);
     n.eps = p->eps;
-    n.stream = p->rows * p->channels * elem_size(p->dtype) > ssd::kStreamBytes;
+    n.stream = p->rows * p->channels * out_size > ssd::kStreamBytes;
     return n;
 }
 
@@ -479,7 +480,7 @@ int ssd_gated_norm_forward(const ssd_norm_problem_t* p, const void* x, const voi
     const int d = check_device();
     if (d != SSD_OK) return d;
     if (p->rows == 0) return SSD_OK;
-    ssd::NormParams n = params_of(p);
+    ssd::NormParams n = params_of(p, e);
     n.x = x;
     n.z = z;
     n.w = weight;
@@ -512,7 +513,7 @@ int ssd_gated_norm_backward(const ssd_norm_problem_t* p, const void* x, const vo
     if (d != SSD_OK) return d;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (p->rows == 0) return done("gated norm backward", p, ssd::launch_fill(dweight, p->channels, s));
-    ssd::NormParams n = params_of(p);
+    ssd::NormParams n = params_of(p, 4);
     n.x = x;
     n.z = z;
     n.w = weight;
@@ -544,7 +545,7 @@ int ssd_residual_norm_forward(const ssd_norm_problem_t* p, const void* x, const 
     const int d = check_device();
     if (d != SSD_OK) return d;
     if (p->rows == 0) return SSD_OK;
-    ssd::NormParams n = params_of(p);
+    ssd::NormParams n = params_of(p, 4);
     n.x = x;
     n.z = residual;
     n.w = weight;
@@ -587,7 +588,7 @@ int ssd_residual_norm_backward(const ssd_norm_problem_t* p, const void* x, const
         if (r == hipSuccess && scale) r = ssd::launch_fill(dscale, p->channels, s);
         return done("residual norm backward", p, r);
     }
-    ssd::NormParams n = params_of(p);
+    ssd::NormParams n = params_of(p, 4);
     n.x = x;
     n.w = weight;
     n.scale = scale;

@@ -233,3 +233,24 @@ def test_arguments_are_checked():
             (TypeError, lambda: ssd.residual_norm_backward(x, x, w, x, dresidual_out=h))):
         with pytest.raises(kind):
             f()
+
+
+def test_outputs_larger_than_the_caches():
+    """Rows are independent, so those of a call whose fp32 outputs pass 32 MB (bf16 ones do not)
+    equal those of a call below it, however either stores them."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("norms, outputs above and below 32 MB")
+    D, M, few = 1030, 8400, 700
+    assert M * D * 2 < 32 << 20 < M * D * 4
+    g = torch.Generator(device="cuda").manual_seed(11)
+    x, z, res, dout = (torch.randn(M, D, device="cuda", generator=g) for _ in range(4))
+    w, scale = (torch.randn(D, device="cuda", generator=g) for _ in range(2))
+    z = z.bfloat16()
+    for first in (True, False):
+        kw = dict(group_size=D // 2, gate_first=first)
+        a, c = ssd.gated_norm_backward(x, z, w, dout, **kw), ssd.gated_norm_backward(x[:few], z[:few], w, dout[:few], **kw)
+        assert torch.equal(a["dx"][:few], c["dx"]) and torch.equal(a["dz"][:few], c["dz"])
+    a, c = ssd.residual_norm(z, res, w, scale), ssd.residual_norm(z[:few], res[:few], w, scale)
+    assert torch.equal(a[0][:few], c[0]) and torch.equal(a[1][:few], c[1])
+    ga, gc = (ssd.residual_norm_backward(z[:m], s, w, dout[:m], scale=scale) for m, s in ((M, a[1]), (few, c[1])))
+    assert torch.equal(ga["dx"][:few], gc["dx"]) and torch.equal(ga["dresidual"][:few], gc["dresidual"])
