@@ -457,27 +457,6 @@ ConvSizes conv_sizes(const ssd_conv_problem_t* p) {
     return s;
 }
 
-struct Buf {
-    const void* ptr;
-    int64_t bytes;
-};
-// every output against every input and the outputs after it
-int check_alias(const Buf* in, int nin, const Buf* out, int nout) {
-    for (int i = 0; i < nout; ++i) {
-        for (int j = 0; j < nin; ++j)
-            if (overlap(out[i].ptr, out[i].bytes, in[j].ptr, in[j].bytes)) return SSD_ERR_ALIAS;
-        for (int j = i + 1; j < nout; ++j)
-            if (overlap(out[i].ptr, out[i].bytes, out[j].ptr, out[j].bytes)) return SSD_ERR_ALIAS;
-    }
-    return SSD_OK;
-}
-
-int check_sequences(const ssd_conv_problem_t* p, const int32_t* seq_idx) {
-    if (!seq_idx && p->nseqs != p->batch) return SSD_ERR_BAD_SHAPE;
-    if (seq_idx && p->batch * p->seqlen > 0 && p->nseqs < 1) return SSD_ERR_BAD_SHAPE;
-    return SSD_OK;
-}
-
 ssd::ConvParams params_of(const ssd_conv_problem_t* p, const Shape& s) {
     ssd::ConvParams c{};
     c.T = p->seqlen;

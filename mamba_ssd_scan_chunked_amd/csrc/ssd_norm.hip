@@ -405,20 +405,6 @@ ssd::NormParams params_of(const ssd_norm_problem_t* p, int64_t out_size) {
     return n;
 }
 
-struct Buf {
-    const void* ptr;
-    int64_t bytes;
-};
-int check_alias(const Buf* in, int nin, const Buf* out, int nout) {
-    for (int i = 0; i < nout; ++i) {
-        for (int j = 0; j < nin; ++j)
-            if (overlap(out[i].ptr, out[i].bytes, in[j].ptr, in[j].bytes)) return SSD_ERR_ALIAS;
-        for (int j = i + 1; j < nout; ++j)
-            if (overlap(out[i].ptr, out[i].bytes, out[j].ptr, out[j].bytes)) return SSD_ERR_ALIAS;
-    }
-    return SSD_OK;
-}
-
 hipError_t run_gated(const ssd_norm_problem_t* p, bool backward, const ssd::NormParams& n, hipStream_t s) {
     const bool first = (p->flags & SSD_NORM_GATE_FIRST) != 0;
     if (p->dtype == SSD_DTYPE_F32)

@@ -92,20 +92,6 @@ int validate(const ssd_selective_problem_t* p, bool step = false) {
     return SSD_OK;
 }
 
-struct Buf {
-    const void* ptr;
-    int64_t bytes;
-};
-int check_alias(const Buf* in, int nin, const Buf* out, int nout) {
-    for (int i = 0; i < nout; ++i) {
-        for (int j = 0; j < nin; ++j)
-            if (overlap(out[i].ptr, out[i].bytes, in[j].ptr, in[j].bytes)) return SSD_ERR_ALIAS;
-        for (int j = i + 1; j < nout; ++j)
-            if (overlap(out[i].ptr, out[i].bytes, out[j].ptr, out[j].bytes)) return SSD_ERR_ALIAS;
-    }
-    return SSD_OK;
-}
-
 struct SelSizes {
     int64_t x, dt, z, b, c, y, f, a, d, state, seq, bc;
 };
@@ -183,12 +169,6 @@ ssd::SelParams params_of(const ssd_selective_problem_t* p, bool backward) {
 }
 
 template <typename T> T* at(void* base, int64_t off) { return reinterpret_cast<T*>(static_cast<char*>(base) + off); }
-
-int check_sequences(const ssd_selective_problem_t* p, const int32_t* seq_idx) {
-    if (!seq_idx && p->nseqs != p->batch) return SSD_ERR_BAD_SHAPE;
-    if (seq_idx && p->batch * p->seqlen > 0 && p->nseqs < 1) return SSD_ERR_BAD_SHAPE;
-    return SSD_OK;
-}
 
 int done(const char* what, const ssd_selective_problem_t* p, int64_t segs, hipError_t e) {
     if (log_enabled())
