@@ -251,31 +251,32 @@ def fused_step_size_leg(w, prob, d, steps: int, warmup: int):
                          "alg_bytes_per_launch": balg}}
 
 
+# The operators around the scan: the scan and its backward neither include nor call them.
+LAYER_SOURCES = ("block_", "selective", "ssd_conv", "ssd_norm", "ssd_selective")
+
+
+def source_hash(leave_out) -> str:
+    h = hashlib.sha256()
+    csrc = os.path.join(ROOT, "mamba_ssd_scan_chunked_amd", "csrc")
+    for name in sorted(os.listdir(csrc)):
+        if name.startswith(LAYER_SOURCES + leave_out):
+            continue
+        with open(os.path.join(csrc, name), "rb") as f:
+            h.update(name.encode() + b"\0" + f.read())
+    return h.hexdigest()[:16]
+
+
 def kernel_source_hash() -> str:
     """Hash of the sources of the forward path (kernels, instantiations, host
     launch code); the backward's files, the instance generator and the header
     that only declares the launchers are left out."""
-    h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "mamba_ssd_scan_chunked_amd", "csrc")
-    for name in sorted(os.listdir(csrc)):
-        if name.startswith("ssd_bwd") or name in ("gen_instances.py", "ssd_launch.hpp"):
-            continue
-        with open(os.path.join(csrc, name), "rb") as f:
-            h.update(name.encode() + b"\0" + f.read())
-    return h.hexdigest()[:16]
+    return source_hash(("ssd_bwd", "gen_instances.py", "ssd_launch.hpp"))
 
 
 def all_source_hash() -> str:
-    """Hash of every kernel and launch source (the backward runs the forward's local
-    pass and combine too)."""
-    h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "mamba_ssd_scan_chunked_amd", "csrc")
-    for name in sorted(os.listdir(csrc)):
-        if name == "gen_instances.py":
-            continue
-        with open(os.path.join(csrc, name), "rb") as f:
-            h.update(name.encode() + b"\0" + f.read())
-    return h.hexdigest()[:16]
+    """Hash of every kernel and launch source of the scan and its backward (which
+    runs the forward's local pass and combine too)."""
+    return source_hash(("gen_instances.py",))
 
 
 def committed_backward_traffic(workload: str):

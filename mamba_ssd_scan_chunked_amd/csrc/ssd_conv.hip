@@ -20,7 +20,7 @@
 #include <cstdio>
 
 #include "block_common.hpp"
-#include "ssd_host.hpp"
+#include "block_host.hpp"
 
 namespace ssd {
 

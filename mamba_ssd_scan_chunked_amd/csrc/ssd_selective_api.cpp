@@ -10,8 +10,8 @@
 #include <cstdint>
 #include <cstdio>
 
+#include "block_host.hpp"
 #include "selective.hpp"
-#include "ssd_host.hpp"
 
 namespace {
 

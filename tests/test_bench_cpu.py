@@ -2,6 +2,7 @@
 fractions divide by, spelled out tensor by tensor for the 2.7B-layer workload,
 and the single-GPU contract of its command line."""
 import os
+import shutil
 import subprocess
 import sys
 
@@ -52,3 +53,27 @@ def test_metric_names_its_workload():
         "SSD fwd tokens/sec (2.7B-layer shape, T=4096) and % of MFMA/HBM roofline"
     m = bench.metric_name(si.WORKLOADS["long_n256"])
     assert m.startswith("SSD fwd tokens/sec (long_n256: b=1, T=16384, H=32, P=64, N=256, bf16)")
+
+
+def test_counters_stay_valid_when_only_a_layer_operator_changes(monkeypatch, tmp_path):
+    """The committed counters are of the scan's sources: a change to one of them makes them
+    stale, one to the operators around the scan does not."""
+    csrc = os.path.join("mamba_ssd_scan_chunked_amd", "csrc")
+    shutil.copytree(os.path.join(ROOT, csrc), tmp_path / csrc)
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+
+    def hashes():
+        return bench.kernel_source_hash(), bench.all_source_hash()
+
+    before = hashes()
+    for name in ("block_common.hip", "block_common.hpp", "selective.hpp", "ssd_conv.hip", "ssd_norm.hip",
+                 "ssd_selective.hip", "ssd_selective_bwd.hip", "ssd_selective_api.cpp"):
+        with open(tmp_path / csrc / name, "a") as f:
+            f.write("//")
+        assert hashes() == before, name
+    for name, which in (("ssd_bwd.hpp", (False, True)), ("ssd_kernels.hpp", (True, True)), ("ssd_host.hpp", (True, True)),
+                        ("ssd_bf16_s0_e0_l0.hip", (True, True))):
+        old = hashes()
+        with open(tmp_path / csrc / name, "a") as f:
+            f.write("//")
+        assert tuple(a != b for a, b in zip(hashes(), old)) == which, name
