@@ -370,7 +370,9 @@ typedef struct {
  *                                                  not occur are not written
  *   workspace   >= ssd_selective_workspace_size(p) bytes, 256-byte aligned (NULL / 0 when 0)
  * The recurrence runs in fp32.  Rows are cut into segments (one launch becomes three) when
- * there are too few channels and rows to fill the chip.  Outputs must not overlap inputs,
+ * there are too few channels and rows to fill the chip.  Step sizes are meant to be >= 0, so
+ * that states decay; with negative ones they grow, and in a cut row the growth exp(A sum of
+ * steps) of a whole segment has to be finite in fp32, also where the state is zero.  Outputs must not overlap inputs,
  * the workspace or each other (SSD_ERR_ALIAS); the state is not carried in place. */
 size_t ssd_selective_workspace_size(const ssd_selective_problem_t* p);
 int ssd_selective_forward(const ssd_selective_problem_t* p, const void* x, const void* dt, const float* dt_bias,
@@ -391,7 +393,8 @@ int ssd_selective_step(const ssd_selective_problem_t* p, const void* x, const vo
  * wanted, dD, dinit (at a zero state when init_state is NULL; zero for ids that do not
  * occur) and ddt_bias.  workspace: >= ssd_selective_backward_workspace_size(p) bytes,
  * 256-byte aligned: a state every eight tokens, and the channel blocks' parts of dB and dC.
- * Sums are taken in a fixed order: results are deterministic. */
+ * Sums are taken in a fixed order: results are deterministic.  Negative step sizes: as in
+ * ssd_selective_forward. */
 size_t ssd_selective_backward_workspace_size(const ssd_selective_problem_t* p);
 int ssd_selective_backward(const ssd_selective_problem_t* p, const void* x, const void* dt, const float* dt_bias,
                            const float* A_log, const void* B, const void* C, const float* D, const void* z,

@@ -9,11 +9,12 @@
 // Memory-bound: each thread owns V neighbouring channels and walks a run of tokens with
 // the last K-1 inputs in registers, so x is read once (plus K-1 rows per run) and y written
 // once; the next four tokens' loads are in flight while four are worked on.  Measured on an
-// MI355X, 4 x 4096 tokens of 5376 channels, bf16, K = 4 (a device copy moves 5.0 TB/s): forward
-// 64-74 us for 353 MB, 4.8-5.5 TB/s; backward, packed, with states, 213 us for 887 MB, 4.2
-// TB/s: its 43 vector instructions per element take about half of that time, and 170
-// registers leave three waves per SIMD.  A step of 4 rows takes 2.7 us on the GPU, 10 us with
-// the launch and the binding.
+// MI355X, 4 x 4096 tokens of 5376 channels, K = 4 (a device copy moves 5.0 TB/s): forward bf16
+// 71 us for 353 MB (63 when the call before has left part of x in the memory-side cache), fp32
+// 135 us for 705 MB, 5.0-5.2 TB/s; backward, packed, with states, bf16 209 us for 887 MB, fp32
+// 235 us for 1063 MB, 4.2-4.5 TB/s: its 43 vector instructions per element keep the vector
+// units at work for 49 % of that time, and 148 registers leave three waves per SIMD.  A step of
+// 4 rows takes 2.8 us on the GPU, 10 us with the launch and the binding.
 #include "ssd.h"
 
 #include <algorithm>
@@ -408,8 +409,9 @@ Shape shape_of(const ssd_conv_problem_t* p, bool backward) {
     // Runs: as many waves as the chip holds at once (three per SIMD backward, four forward),
     // or a whole number of times that when runs would get longer than `longest`: a run
     // re-reads K-1 rows, but a last round of few waves costs a whole one (4 x 4096 tokens of
-    // 5376 channels backward: runs of 64 tokens, 1.75 rounds, 266 us; of 96, 1.2 rounds, 311;
-    // of 128, 0.9 rounds, 254).
+    // 5376 channels backward, packed and not: runs of 64 tokens, 1.75 rounds, 217 and 192 us; of
+    // 96, 1.2 rounds, 253 and 206; of 114, this rule's 0.98 rounds, 209 and 192; of 128, 0.9
+    // rounds, 212 and 193).
     const int64_t longest = backward ? 128 : 32, resident = (backward ? 3 : 4) * 1024;
     const int64_t columns = std::max<int64_t>(1, p->batch * s.nblk);
     const int64_t least = (p->seqlen + longest - 1) / longest;                      // runs per row

@@ -6,19 +6,25 @@
 // Residual norm, before a block (whole rows):
 //   u = residual + scale x,  out = u r w,  u kept in fp32 as the stream
 //
-// Memory-bound.  A row (of a group) is held in registers by a team of TEAM lanes, CH
-// packs of four channels each, so every input is read once; sums of squares are fp32
-// butterflies within a wave and meet in LDS above it.
+// Memory-bound.  A row (of a group) is held by a team of TEAM lanes, CH packs of four
+// channels each, so every input is read once; sums of squares are fp32 butterflies within a
+// wave and meet in LDS above it.  It stays in registers forward and, up to 8192 channels, in the
+// gradients (but for 68 bytes a lane of the residual norm's at 513 to 768 channels and 44 at
+// 4097 to 8192); gradients of wider groups keep 380 to 2270 bytes a lane in scratch memory.
 //
 // Gradients, with e = dL/d(u r w) and hat = u r:
 //   du = r (e w - hat mean(e w hat)),   dw = sum over rows of e hat.
 // A team walks several rows of one group (as it does forward), with dw (and the residual's dscale) in
 // registers; the teams' sums go to the workspace and are added in a fixed order.
 //
-// Measured on an MI355X (a device copy moves 5.0 TB/s), bf16: gated norm of 16384 rows of 5120
-// (fp32 x) 132 us, 5.1 TB/s; its gradients for 8192 rows in eight groups 145 us, 5.2 TB/s;
-// residual norm's gradients for 16384 rows of 2560 with a scale 163 us, 5.6 TB/s; four decoded
-// rows of 2560 4.3 us on the GPU, 12 us with the launch and the binding.
+// Measured on an MI355X (a device copy moves 5.0 TB/s, calls that read more than they write up
+// to 5.7), bf16: gated norm of 16384 rows of 5120 (fp32 x) 131 us, 5.1 TB/s; its gradients for
+// 8192 rows in eight groups 146 us, 5.2 TB/s; residual norm's gradients for 16384 rows of 2560
+// with a scale 163 us, 5.6 TB/s; four decoded rows of 2560 4.3 us on the GPU, 12 us with the
+// launch and the binding.  Gradients by width, 42 million channels in all, gated and residual
+// with a scale, TB/s: 768 channels 5.0 and 4.3, 1024 5.0 and 5.1, 2560 5.3 and 5.6, 4096 4.8 and
+// 5.0, 5120 4.5 and 4.2, 8192 4.7 and 4.6; of scratch, 12288 1.1 and 1.5, 16384 1.3 and 1.5,
+// 32768 0.5 and 0.5.
 #include "ssd.h"
 
 #include <algorithm>
@@ -158,8 +164,9 @@ __global__ __launch_bounds__(TEAM ? 256 : 1024) void norm_forward_kernel(NormPar
     else norm_forward<TX, TO, MODE, TEAM, CH, false>(p);
 }
 
-// Waves per SIMD that the backward is built for (about 45 registers a pack); teams are
-// launched to fill them, and walk the rows.
+// Waves per SIMD that the backward is built for; teams are launched to fill them, and walk
+// the rows.  A pack takes about 45 registers, so four waves (128 registers) hold two of them;
+// the teams of more packs, 16 waves of one workgroup, can have no more registers than that.
 constexpr int backward_waves(int team, int ch) { return ch <= 1 ? 5 : (ch <= 2 || team == 0 ? 4 : (ch <= 3 ? 3 : 2)); }
 
 template <typename TX, typename TO, int MODE, int TEAM, int CH, bool STREAM>
@@ -318,7 +325,8 @@ static Team team_of(int64_t size, bool backward) {
     return {0, (int)((size + 256 * ch - 1) / (256 * ch)) * 64, ch};
 }
 // Teams per group in the backward: as many as stay on the chip together, but at least 8
-// rows each, so that the partial sums stay small beside the rows.
+// rows each, so that the partial sums stay small beside the rows.  (What adding them takes is
+// not counted: see column_sums_kernel for narrow rows.)
 static int64_t slots_of(int64_t size, int64_t groups, int64_t rows) {
     const Team t = team_of(size, true);
     const int64_t waves = backward_waves(t.team, t.ch);

@@ -13,14 +13,17 @@ namespace ssd {
 //
 // Bound by vector instructions: per (token, channel) 16 states x 5 (a multiply and an exp2 for
 // the decay, a multiply by the row broadcast of B, two fused multiply-adds) and some 50 for
-// the step size, the gate and the sums.  An instruction issues in about 4.3 cycles and exp2 in
-// 8.6, which makes 0.24 ms for the states alone at 4 x 4096 tokens, 5120 channels, 16 states
-// and 0.37 with the rest; measured 0.46 (bf16, gated, softplus; 674 MB, 1.5 TB/s), as 640
-// workgroups of 32 channels are 2.5 for each of 256 compute units.  Rows whole in 64-channel
+// the step size, the gate and the sums.  A wave's instruction takes a SIMD about 1.84 ns and
+// exp2 3.95, which makes 0.23 ms for the states alone at 4 x 4096 tokens, 5120 channels, 16
+// states and 0.33 with the rest; measured 0.46 (bf16, gated, softplus; fp32 0.47), with the vector
+// units at work for 65 % of the time, as 640 workgroups of 32 channels are 2.5 for each of 256
+// compute units.  (The 64 bytes that 32 bf16 channels take of a token are half a cache line, and
+// most lines are fetched twice: 1066 MB for 507 of inputs, which costs no time.)  Rows whole in 64-channel
 // workgroups of four states a lane take 0.65, in 16-channel waves 0.66, with B and C from LDS
 // per state instead of by row broadcasts 0.79; two buffers and one barrier a tile 0.59.
 // Rows in segments take 64-channel workgroups of four states a lane (16384 tokens of 1536
-// channels: 0.19 ms for the local pass, the combine and the scan; 32-channel ones 0.22).
+// channels: 0.18 ms for the local pass, the combine and the scan, at work for 81 and 87 % of the
+// two passes; 32-channel ones 0.22).
 template <typename T, int N, int CH, int S, bool SEQ>
 __global__ __launch_bounds__((SelShape<N, CH, S>::THREADS)) void sel_forward_kernel(SelParams p) {
     using Sh = SelShape<N, CH, S>;
@@ -365,7 +368,8 @@ template <typename T, int N, int CH, int S> static void forward_shape(const SelP
 // N/8 states a lane, give twice the waves where there are fewer than three of the larger for
 // each of 256 compute units.  1024 tokens of 5120 channels, bf16, us with 32 and 64 channels:
 // N = 16: 4 rows (320 workgroups of 64) 132 and 161, 8 rows 223 and 213, 12 rows 310 and 282,
-// 32 rows 748 and 642; N = 64: 4 rows 358 and 419, 8 rows 573 and 623, 12 rows 883 and 806.
+// 32 rows 748 and 642; N = 64: 4 rows 358 and 419, 8 rows 573 and 623, 12 rows 883 and 806.  One
+// border for all N: at 8 rows it gives away 10 us with 16 states and wins 50 with 64.
 template <typename T, int N> static void forward_n(const SelParams& p, hipStream_t s) {
     if (p.nseg > 1 || p.batch * p.G * ((p.per_group + 63) / 64) >= 768) forward_shape<T, N, 64, N / 4>(p, s);
     else forward_shape<T, N, 32, N / 8>(p, s);

@@ -27,7 +27,10 @@ int64_t blocks_of(const ssd_selective_problem_t* p) { return (p->channels / p->n
 // is cut to fill the chip.  Forward, a cut adds the local pass (nearly the scan again): on
 // an MI355X (2048 tokens, 16 states, bf16) 10 items take 160 us whole and 38 us in segments
 // of 64 tokens, 80 items 158 and 93, 160 items 190 and 158, 240 items 188 and 221; 80 items
-// of 512 tokens 44 and 40, 16 items of 300 tokens 30 and 32.  Backward, the local pass is
+// of 512 tokens 44 and 40, 16 items of 300 tokens 30 and 32.  The borders are those of 16
+// states; whole and as the rule has it, 2048 tokens: 8 states 80 items 124 and 65, 160 items 145
+// and 112, 192 items 146 and 122; 32 states 207 and 157, 277 and 290, 277 and 321; 64 states 321
+// and 253, 462 and 496, 462 and 559 (from 160 items on these lose by the cut).  Backward, the local pass is
 // needed for its checkpoints anyway and the segments only add to it: 10 items 1356 us whole
 // and 69 us in segments of 32 tokens, 80 items 1416 and 279, 320 items 1748 and (12 segments)
 // 947, 640 items 2232 and (six) 1780.  Rows stay whole where they alone fill four fifths of

@@ -8,12 +8,13 @@
 // tile of eight tokens, and the reverse pass runs a tile forwards (keeping p and the decays
 // in registers) and then backwards.
 //
-// Bound by vector instructions (78 % of the reverse pass's cycles issue one): per (token,
-// channel, state) 7 on the way out, 8 on the way back and 4 for the sums over channels.
-// Measured on an MI355X, 8 x 2048 tokens of 1536 channels with 16 states, bf16, gated: 0.58 ms
-// in all, of which the reverse pass 0.40, the local pass 0.14 and the three small launches
-// 0.03.  Eight states a lane need 128 registers for p alone and spill or run two waves per
-// SIMD (0.8 ms and more); the decays computed again on the way back, 0.69.
+// Bound by vector instructions (the vector units are at work for 83 % of the reverse pass and
+// 79 % of the local pass): per (token, channel, state) 7 on the way out, 7 on the way back and
+// 3 for the sums over channels.  Measured on an MI355X, 8 x 2048 tokens of 1536 channels with
+// 16 states, gated: bf16 0.58 ms, fp32 0.55, of which the reverse pass 0.40, the local pass 0.14
+// and the three small launches 0.03.  Eight states a lane need 128 registers for p and the decays
+// alone and spill or run two waves per SIMD (0.8 ms and more); the decays computed again on
+// the way back, 0.69.
 #include "selective.hpp"
 
 namespace ssd {
@@ -258,9 +259,12 @@ __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS), 4) void sel_locals_k
 }
 
 // ---------------------------------------------------------------- reverse pass
-// One workgroup per 64 channels and segment, N/S waves with S states each (four: the
-// tile's p and decays then take 64 registers, and three waves fit a SIMD).  The sums over states of a
-// token (for y, d(step x) and dstep) meet in LDS, the sums over channels (for dB and dC)
+// One workgroup per 64 channels and segment, N/S waves with S states each (four, or eight for
+// N = 64).  With four the tile's p and decays take 64 registers, and N = 16 fits three waves per
+// SIMD without scratch (packed bf16: 12 bytes a lane); N = 8 at three waves keeps 72 to 116 bytes a
+// lane in scratch memory, N = 32 at four 52 to 104.  (2 x 777 packed tokens of 650 channels with 32
+// states, fp32, take 60 us here, the vector units at work for 34 % of it.)  The sums over states of
+// a token (for y, d(step x) and dstep) meet in LDS, the sums over channels (for dB and dC)
 // within the wave and then, over channel blocks, in part_b and part_c.
 template <typename T, int N, int S, bool SEQ>
 __global__ __launch_bounds__((SelShape<N, 64, S>::THREADS), (N == 32 ? 4 : (N < 32 ? 3 : 2))) void sel_reverse_kernel(SelParams p) {
