@@ -18,7 +18,7 @@ namespace ssd {
 // states and 0.33 with the rest; measured 0.46 (bf16, gated, softplus; fp32 0.47), with the vector
 // units at work for 65 % of the time, as 640 workgroups of 32 channels are 2.5 for each of 256
 // compute units.  (The 64 bytes that 32 bf16 channels take of a token are half a cache line, and
-// most lines are fetched twice: 1066 MB for 507 of inputs, which costs no time.)  Rows whole in 64-channel
+// most lines are fetched twice: 1066 MB for 507 of inputs, 2.7 TB/s in all.)  Rows whole in 64-channel
 // workgroups of four states a lane take 0.65, in 16-channel waves 0.66, with B and C from LDS
 // per state instead of by row broadcasts 0.79; two buffers and one barrier a tile 0.59.
 // Rows in segments take 64-channel workgroups of four states a lane (16384 tokens of 1536
