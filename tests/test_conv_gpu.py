@@ -298,8 +298,9 @@ def test_arguments_are_checked():
 
 
 LONG = [
-    # dtype, rows, tokens, channels, K.  Forward runs of 10 and 20 tokens (4096 waves over 64 and
-    # 72 of the channels' and rows' workgroups), backward of 25 and 27 (3072 over 128 and 72).
+    # dtype, rows, tokens, channels, K.  Forward runs of 10 and 20 tokens (a round of four waves a
+    # SIMD over the 64 and 72 workgroups of channels and rows), backward of 25 and 27 (three
+    # waves a SIMD over 128 and 72).
     ("bf16", 16, 600, 2048, 4), ("f32", 8, 1111, 2052, 3),
 ]
 
