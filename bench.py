@@ -252,7 +252,7 @@ def fused_step_size_leg(w, prob, d, steps: int, warmup: int):
 
 
 # The operators around the scan: the scan and its backward neither include nor call them.
-LAYER_SOURCES = ("block_", "selective", "ssd_conv", "ssd_norm", "ssd_selective")
+LAYER_SOURCES = ("block_", "selective", "ssd_conv", "ssd_norm", "ssd_selective", "ssd_recurrence", "ssd_rotary")
 
 
 def source_hash(leave_out) -> str:

@@ -465,6 +465,100 @@ int ssd_residual_norm_backward(const ssd_norm_problem_t* p, const void* x, const
                                float* dx, float* dresidual, float* dweight, float* dscale, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+typedef struct {
+    int64_t batch;      /* rows                                                     */
+    int64_t seqlen;     /* tokens per row (may be 0)                                */
+    int64_t channels;   /* D                                                        */
+    int64_t nseqs;      /* number of sequences: == batch without seq_idx            */
+    int64_t ldx, ldr, ldi, ldz;   /* elements from one token to the next, >= channels, < 2^31 */
+    int32_t dtype;      /* ssd_dtype_t of x, r, i, z and y                          */
+    uint32_t flags;     /* must be 0                                                */
+} ssd_recurrence_problem_t;
+
+/* The gated linear recurrence: one state per channel, its decay and the scale of its input
+ * from gates of the same token (sigma(v) = 1 / (1 + e^-v)):
+ *     a_t = exp(A[d] sigma(r_t)),    A = -exp(A_log),
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigma(i_t) x_t,
+ *     y_t = h_t,   times silu(z_t) with z.
+ *   x, r, i     (batch, seqlen, channels)   dtype; tokens ldx, ldr, ldi apart
+ *   A_log       (channels)                  fp32
+ *   z           (batch, seqlen, channels)   dtype, tokens ldz apart, or NULL for no gate
+ *   init_state  (nseqs, channels)           fp32, or NULL for zeros
+ *   seq_idx     (batch, seqlen)             int32 or NULL, as in ssd_forward
+ *   y           (batch, seqlen, channels)   dtype, output
+ *   final_state (nseqs, channels)           fp32 output, or NULL; rows of ids that do not occur
+ *                                           are not written
+ *   workspace   >= ssd_recurrence_workspace_size(p) bytes, 256-byte aligned (NULL / 0 when 0)
+ * The recurrence runs in fp32; 1 - a and 1 - a^2 are formed without cancellation.  Outputs must
+ * not overlap inputs, the workspace or each other (SSD_ERR_ALIAS); the state is not carried in
+ * place. */
+size_t ssd_recurrence_workspace_size(const ssd_recurrence_problem_t* p);
+int ssd_recurrence_forward(const ssd_recurrence_problem_t* p, const void* x, const void* r, const void* i,
+                           const float* A_log, const void* z, const float* init_state, const int32_t* seq_idx, void* y,
+                           float* final_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token (decoding): ssd_recurrence_forward with seqlen 1 and nseqs == batch, from `state`
+ * to `state_out`, which may be the same buffer (in place) or one that does not overlap it. */
+int ssd_recurrence_step(const ssd_recurrence_problem_t* p, const void* x, const void* r, const void* i,
+                        const float* A_log, const void* z, const float* state, float* state_out, void* y, void* stream);
+
+/* Gradients of L for dL/dy = dy (fp32) and dL/dfinal_state = dfinal (fp32, or NULL), all fp32
+ * and dense, shaped like their inputs: dx, dr, di, dA_log, dz (required with z) and dinit (NULL
+ * if not wanted; at a zero state when init_state is NULL, zero for ids that do not occur).
+ * workspace: >= ssd_recurrence_backward_workspace_size(p) bytes, 256-byte aligned.  Sums are
+ * taken in a fixed order: results are deterministic. */
+size_t ssd_recurrence_backward_workspace_size(const ssd_recurrence_problem_t* p);
+int ssd_recurrence_backward(const ssd_recurrence_problem_t* p, const void* x, const void* r, const void* i,
+                            const float* A_log, const void* z, const float* init_state, const int32_t* seq_idx,
+                            const float* dy, const float* dfinal, float* dx, float* dr, float* di, float* dA_log,
+                            float* dz, float* dinit, void* workspace, size_t workspace_bytes, void* stream);
+
+/* rotary flags */
+enum {
+    SSD_ROTARY_INTERLEAVED = 1u << 0    /* pairs are channels 2j, 2j + 1 (else j, j + rotary_dim / 2) */
+};
+
+typedef struct {
+    int64_t tokens;       /* over the whole batch                                            */
+    int64_t seqlen;       /* without positions, token t has position t % seqlen; >= 1, <= 2^31 */
+    int64_t b_heads;      /* heads (groups) of B: keys                                       */
+    int64_t c_heads;      /* heads (groups) of C: queries                                    */
+    int64_t headdim;      /* N: channels of a head, <= 1024                                  */
+    int64_t rotary_dim;   /* channels rotated, from the first on: even, 0 to headdim         */
+    int64_t ldb, ldc;     /* elements from one token to the next, >= heads * headdim, < 2^31 */
+    float eps;            /* >= 0                                                            */
+    int32_t dtype;        /* ssd_dtype_t of B, C and the outputs                             */
+    uint32_t flags;       /* SSD_ROTARY_*                                                    */
+    int32_t reserved;     /* must be 0                                                       */
+} ssd_rotary_problem_t;
+
+/* The root-mean-square norm of B and C per head with the rotation by position, in one pass
+ * (C plays the query, B the key of the dual form, so rotating both by their tokens' positions
+ * makes the scan see C_t R(t - s) B_s, a decay with a complex factor):
+ *     v = u / sqrt(mean(u^2) + eps) weight        per token and head,
+ *     (out_p, out_q) = (v_p cos w - v_q sin w, v_p sin w + v_q cos w),   w = position freqs[j],
+ * for the pairs (p, q) of the first rotary_dim channels, pair j; the rest of v passes as it is.
+ * The angle is taken in fp64, so positions may be any int32.
+ *   B, C       (tokens, heads, headdim)   dtype; tokens ldb, ldc apart, heads dense
+ *   b_weight, c_weight  (headdim)         fp32, shared by the heads
+ *   freqs      (rotary_dim / 2)           fp32: angle per position (NULL when rotary_dim is 0)
+ *   positions  (tokens)                   int32, or NULL: t % seqlen
+ *   B_out, C_out  (tokens, heads, headdim)  dtype, dense outputs, as ssd_forward takes them
+ * Outputs must not overlap inputs or each other (SSD_ERR_ALIAS).  One kernel launch. */
+int ssd_rotary_norm_forward(const ssd_rotary_problem_t* p, const void* B, const void* C, const float* b_weight,
+                            const float* c_weight, const float* freqs, const int32_t* positions, void* B_out,
+                            void* C_out, void* stream);
+
+/* Gradients for dL/dB_out = dB_out and dL/dC_out = dC_out (fp32, dense): dB, dC (tokens, heads,
+ * headdim), db_weight and dc_weight (headdim), fp32 and dense; freqs are constants.
+ * workspace: 256-byte aligned, of the size given (0 for an invalid problem).  Sums are taken in
+ * a fixed order: results are deterministic. */
+size_t ssd_rotary_norm_backward_workspace_size(const ssd_rotary_problem_t* p);
+int ssd_rotary_norm_backward(const ssd_rotary_problem_t* p, const void* B, const void* C, const float* b_weight,
+                             const float* c_weight, const float* freqs, const int32_t* positions, const float* dB_out,
+                             const float* dC_out, float* dB, float* dC, float* db_weight, float* dc_weight,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of an error code. */
 const char* ssd_strerror(int status);
 

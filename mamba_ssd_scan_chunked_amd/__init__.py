@@ -27,7 +27,10 @@ from .block import (CONV_SILU, NORM_GATE_FIRST, ConvProblem, NormProblem, causal
                     gated_norm_backward_workspace_size, norm_problem, residual_norm, residual_norm_backward,
                     residual_norm_backward_workspace_size, SelectiveProblem, selective_backward_workspace_size,
                     selective_problem, selective_scan, selective_scan_backward, selective_step,
-                    selective_workspace_size)
+                    selective_workspace_size, RecurrenceProblem, RotaryProblem, ROTARY_INTERLEAVED, gated_recurrence,
+                    gated_recurrence_backward, gated_recurrence_step, recurrence_backward_workspace_size,
+                    recurrence_problem, recurrence_workspace_size, rotary_norm, rotary_norm_backward,
+                    rotary_norm_backward_workspace_size, rotary_problem)
 
 __all__ = ["forward", "forward_into", "forward_into_noalloc", "noalloc_scratch_bytes", "step", "backward", "backward_into", "backward_workspace_size", "workspace_size", "validate", "problem", "SSDError",
            "version", "library_path", "load_library", "DTYPE_F32", "DTYPE_BF16", "FLAG_DT_SCALES_X",
@@ -36,7 +39,10 @@ __all__ = ["forward", "forward_into", "forward_into_noalloc", "noalloc_scratch_b
            "residual_norm_backward", "norm_problem", "gated_norm_backward_workspace_size",
            "residual_norm_backward_workspace_size", "ConvProblem", "NormProblem", "CONV_SILU", "NORM_GATE_FIRST",
            "selective_scan", "selective_scan_backward", "selective_step", "selective_problem",
-           "selective_workspace_size", "selective_backward_workspace_size", "SelectiveProblem"]
+           "selective_workspace_size", "selective_backward_workspace_size", "SelectiveProblem", "gated_recurrence",
+           "gated_recurrence_backward", "gated_recurrence_step", "recurrence_problem", "recurrence_workspace_size",
+           "recurrence_backward_workspace_size", "RecurrenceProblem", "rotary_norm", "rotary_norm_backward",
+           "rotary_problem", "rotary_norm_backward_workspace_size", "RotaryProblem", "ROTARY_INTERLEAVED"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libssd_mi355x.so"

@@ -1,16 +1,20 @@
 """The operators around the scan in a Mamba layer: the short causal convolution, the
-selective scan with a decay per channel and state, the gated norm after the scan and
-the residual norm before a block, with their gradients and single-token forms, through
-the C ABI in ``include/ssd.h``.
+selective scan with a decay per channel and state, the gated linear recurrence, the norm of
+B and C with the rotation by position, the gated norm after the scan and the residual norm
+before a block, with their gradients and single-token forms, through the C ABI in
+``include/ssd.h``.
 
     y, final   = causal_conv(x, weight, bias, init_state, seq_idx, nseqs)
     y          = causal_conv_step(x, weight, bias, state)
     y, final   = selective_scan(x, dt, A_log, B, C, D, z, init_state, seq_idx, nseqs)
     y          = selective_step(x, dt, A_log, B, C, D, state, z)
+    y, final   = gated_recurrence(x, r, i, A_log, z, init_state, seq_idx, nseqs)
+    y          = gated_recurrence_step(x, r, i, A_log, state, z)
+    B, C       = rotary_norm(B, C, b_weight, c_weight, freqs, positions)
     out        = gated_norm(x, z, weight)
     out, res   = residual_norm(x, residual, weight)
 
-Activations (x, dt, B, C, z, y, out) are bf16 or fp32; parameters, states and gradients are
+Activations (x, dt, r, i, B, C, z, y, out) are bf16 or fp32; parameters, states and gradients are
 fp32.  Activations may be slices of a projection's output (channels contiguous, one
 distance between all tokens, below 2^31 elements, or 2^25 for the selective scan of a
 prompt): they are read in place.  Anything else that is not contiguous is copied first.
@@ -32,6 +36,7 @@ DTYPE_F32 = 0
 DTYPE_BF16 = 1
 CONV_SILU = 1
 NORM_GATE_FIRST = 1
+ROTARY_INTERLEAVED = 1
 
 
 class ConvProblem(ctypes.Structure):
@@ -55,10 +60,24 @@ class NormProblem(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class RecurrenceProblem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("nseqs", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldi", ctypes.c_int64),
+                ("ldz", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class RotaryProblem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("b_heads", ctypes.c_int64),
+                ("c_heads", ctypes.c_int64), ("headdim", ctypes.c_int64), ("rotary_dim", ctypes.c_int64),
+                ("ldb", ctypes.c_int64), ("ldc", ctypes.c_int64), ("eps", ctypes.c_float), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32)]
+
+
 def _declare(lib):
     """Argument types of the library's entry points."""
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
-    conv, norm, sel = (ctypes.POINTER(s) for s in (ConvProblem, NormProblem, SelectiveProblem))
+    conv, norm, sel, rec, rot = (ctypes.POINTER(s) for s in (ConvProblem, NormProblem, SelectiveProblem,
+                                                             RecurrenceProblem, RotaryProblem))
     for name, args, res in (
             ("ssd_conv_forward", [conv] + [vp] * 8, i32),
             ("ssd_conv_backward_workspace_size", [conv], sz),
@@ -69,6 +88,14 @@ def _declare(lib):
             ("ssd_selective_step", [sel] + [vp] * 12, i32),
             ("ssd_selective_backward_workspace_size", [sel], sz),
             ("ssd_selective_backward", [sel] + [vp] * 22 + [sz, vp], i32),
+            ("ssd_recurrence_workspace_size", [rec], sz),
+            ("ssd_recurrence_forward", [rec] + [vp] * 10 + [sz, vp], i32),
+            ("ssd_recurrence_step", [rec] + [vp] * 9, i32),
+            ("ssd_recurrence_backward_workspace_size", [rec], sz),
+            ("ssd_recurrence_backward", [rec] + [vp] * 16 + [sz, vp], i32),
+            ("ssd_rotary_norm_forward", [rot] + [vp] * 9, i32),
+            ("ssd_rotary_norm_backward_workspace_size", [rot], sz),
+            ("ssd_rotary_norm_backward", [rot] + [vp] * 13 + [sz, vp], i32),
             ("ssd_gated_norm_forward", [norm] + [vp] * 5, i32),
             ("ssd_gated_norm_backward_workspace_size", [norm], sz),
             ("ssd_gated_norm_backward", [norm] + [vp] * 8 + [sz, vp], i32),
@@ -441,6 +468,183 @@ def selective_step(x, dt, A_log, B, C, D, state, z=None, y=None, dt_bias=None, d
                                          _ptr(C), _ptr(D), _ptr(z), _ptr(state), _ptr(state_out), _ptr(y),
                                          _current(dev)))
     return y
+
+
+# ------------------------------------------------------------------ gated linear recurrence
+def recurrence_problem(batch, seqlen, channels, nseqs=None, dtype=DTYPE_BF16, ldx=None, ldr=None, ldi=None,
+                       ldz=None) -> RecurrenceProblem:
+    lds = [channels if ld is None else ld for ld in (ldx, ldr, ldi, ldz)]
+    return RecurrenceProblem(batch, seqlen, channels, batch if nseqs is None else nseqs, *lds, dtype, 0)
+
+
+def recurrence_workspace_size(p: RecurrenceProblem) -> int:
+    return int(_lib().ssd_recurrence_workspace_size(ctypes.byref(p)))
+
+
+def recurrence_backward_workspace_size(p: RecurrenceProblem) -> int:
+    return int(_lib().ssd_recurrence_backward_workspace_size(ctypes.byref(p)))
+
+
+def _recurrence_activations(x, r, i, A_log, z):
+    """(tensors x, r, i, z as rows, their distances, A_log, the type's code)."""
+    code = _dtype("x", x)
+    A_log = _given("A_log", A_log, (x.shape[-1],), torch.float32, x.device)
+    r, ldr = _activation("r", r, x.shape, x, FAR)
+    i, ldi = _activation("i", i, x.shape, x, FAR)
+    ldz = x.shape[-1]
+    if z is not None:
+        z, ldz = _activation("z", z, x.shape, x, FAR)
+    x, ldx = _rows(x)
+    return (x, r, i, z), (ldx, ldr, ldi, ldz), A_log, code
+
+
+def _recurrence_arguments(x, r, i, A_log, z, init_state, seq_idx, nseqs):
+    """(problem, pointers' tensors in the order of the C call up to seq_idx)."""
+    if x.dim() != 3:
+        raise ValueError("x must be (b,T,D)")
+    (xr, r, i, z), lds, A_log, code = _recurrence_activations(x, r, i, A_log, z)
+    b, T, D = x.shape
+    seq_idx, ns = _sequences(x, seq_idx, nseqs)
+    init_state = _given("init_state", init_state, (ns, D), torch.float32, x.device)
+    return recurrence_problem(b, T, D, ns, code, *lds), (xr, r, i, A_log, z, init_state, seq_idx)
+
+
+def gated_recurrence(x, r, i, A_log, z=None, init_state=None, seq_idx=None, nseqs: Optional[int] = None, y=None,
+                     final_state=None, workspace=None, return_final: bool = True, stream=None):
+    """The gated linear recurrence of whole rows through ``ssd_recurrence_forward``:
+    a = exp(A sigmoid(r)) with A = -exp(A_log), h = a h + sqrt(1 - a^2) sigmoid(i) x, y = h,
+    or h silu(z) with z.
+
+    x, the gates r and i before their sigmoid, and z are (b,T,D) in one type; A_log (D) and
+    the state (nseqs,D) fp32; packed sequences as in :func:`forward`.  Returns (y like x,
+    final_state or None)."""
+    dev = _gpu(x)
+    with _on(dev, stream):
+        p, args = _recurrence_arguments(x, r, i, A_log, z, init_state, seq_idx, nseqs)
+        y = _output("y", y, x.shape, x.dtype, dev)
+        if final_state is not None or return_final:
+            final_state = _output("final_state", final_state, (p.nseqs, p.channels), torch.float32, dev)
+        ws, nbytes = _workspace(workspace, recurrence_workspace_size(p), dev)
+        _check(_lib().ssd_recurrence_forward(ctypes.byref(p), *map(_ptr, args), _ptr(y), _ptr(final_state), _ptr(ws),
+                                             nbytes, _current(dev)))
+    return y, final_state
+
+
+def gated_recurrence_backward(x, r, i, A_log, dy, z=None, init_state=None, dfinal=None, seq_idx=None,
+                              nseqs: Optional[int] = None, workspace=None, stream=None):
+    """Gradients through ``ssd_recurrence_backward`` of <dy, y> + <dfinal, final_state> for
+    :func:`gated_recurrence` with the same arguments; dy (b,T,D) and dfinal fp32.  Returns a
+    dict of fp32 tensors dx, dr, di, dA_log, dinit and, with z, dz (dinit at a zero state when
+    none was given)."""
+    dev, f32 = _gpu(x), torch.float32
+    with _on(dev, stream):
+        p, args = _recurrence_arguments(x, r, i, A_log, z, init_state, seq_idx, nseqs)
+        state = (p.nseqs, p.channels)
+        dy = _given("dy", dy, x.shape, f32, dev)
+        dfinal = _given("dfinal", dfinal, state, f32, dev)
+        shapes = {"dx": x.shape, "dr": x.shape, "di": x.shape, "dA_log": A_log.shape, "dz": x.shape, "dinit": state}
+        if z is None:
+            del shapes["dz"]
+        out = {k: torch.empty(s, dtype=f32, device=dev) for k, s in shapes.items()}
+        ws, nbytes = _workspace(workspace, recurrence_backward_workspace_size(p), dev)
+        _check(_lib().ssd_recurrence_backward(ctypes.byref(p), *map(_ptr, args), _ptr(dy), _ptr(dfinal),
+                                              _ptr(out["dx"]), _ptr(out["dr"]), _ptr(out["di"]), _ptr(out["dA_log"]),
+                                              _ptr(out.get("dz")), _ptr(out["dinit"]), _ptr(ws), nbytes, _current(dev)))
+    return out
+
+
+def gated_recurrence_step(x, r, i, A_log, state, z=None, y=None, state_out=None, stream=None):
+    """One token per row through ``ssd_recurrence_step``: x, r, i, z (b,D), ``state`` (b,D)
+    fp32, updated in place or, with ``state_out``, left as it was and the new state written
+    there.  Returns y (b,D)."""
+    dev = _gpu(x)
+    if x.dim() != 2:
+        raise ValueError("x must be (b,D)")
+    with _on(dev, stream):
+        b, D = x.shape
+        (xr, r, i, z), lds, A_log, code = _recurrence_activations(x, r, i, A_log, z)
+        state, state_out = _states(state, state_out, (b, D), dev)
+        y = _output("y", y, (b, D), x.dtype, dev)
+        p = recurrence_problem(b, 1, D, b, code, *lds)
+        _check(_lib().ssd_recurrence_step(ctypes.byref(p), _ptr(xr), _ptr(r), _ptr(i), _ptr(A_log), _ptr(z),
+                                          _ptr(state), _ptr(state_out), _ptr(y), _current(dev)))
+    return y
+
+
+# ------------------------------------------------------------------ norm with rotation
+def rotary_problem(tokens, b_heads, c_heads, headdim, rotary_dim, seqlen=1, eps=1e-5, dtype=DTYPE_BF16,
+                   interleaved=False, ldb=None, ldc=None) -> RotaryProblem:
+    return RotaryProblem(tokens, seqlen, b_heads, c_heads, headdim, rotary_dim,
+                         b_heads * headdim if ldb is None else ldb, c_heads * headdim if ldc is None else ldc, eps,
+                         dtype, ROTARY_INTERLEAVED if interleaved else 0, 0)
+
+
+def rotary_norm_backward_workspace_size(p: RotaryProblem) -> int:
+    return int(_lib().ssd_rotary_norm_backward_workspace_size(ctypes.byref(p)))
+
+
+def _rotary_arguments(B, C, b_weight, c_weight, freqs, positions, interleaved, eps):
+    """(problem, pointers' tensors in the order of the C call up to positions)."""
+    if B.dim() < 3 or C.dim() != B.dim() or C.shape[:-2] != B.shape[:-2] or C.shape[-1] != B.shape[-1]:
+        raise ValueError("B and C must be (..., G, N) with the same tokens and N")
+    if freqs.dim() != 1:
+        raise ValueError("freqs must have one dimension (rotary_dim / 2)")
+    dev, f32 = B.device, torch.float32
+    lead, (G, N), H = B.shape[:-2], B.shape[-2:], C.shape[-2]
+    code = _dtype("B", B)
+    b_weight = _given("b_weight", b_weight, (N,), f32, dev)
+    c_weight = _given("c_weight", c_weight, (N,), f32, dev)
+    freqs = _given("freqs", freqs, freqs.shape, f32, dev)
+    positions = _given("positions", positions, lead, torch.int32, dev)
+    B, ldb = _grouped("B", B, (*lead, G, N), B, FAR)
+    C, ldc = _grouped("C", C, (*lead, H, N), B, FAR)
+    tokens = 1
+    for n in lead:
+        tokens *= n
+    p = rotary_problem(tokens, G, H, N, 2 * freqs.shape[0], max(1, lead[-1]), eps, code, interleaved, ldb, ldc)
+    return p, (B, C, b_weight, c_weight, freqs, positions)
+
+
+def rotary_norm(B, C, b_weight, c_weight, freqs, positions=None, interleaved: bool = False, eps: float = 1e-5,
+                B_out=None, C_out=None, stream=None):
+    """The root-mean-square norm of B and C (the dual form's keys and queries) per head with
+    the rotation by position, through ``ssd_rotary_norm_forward``.
+
+    B (..., G, N) and C (..., H, N), as :func:`forward` and :func:`step` take them or with
+    heads of their own number; b_weight, c_weight (N) fp32, shared by the heads; ``freqs``
+    (R/2) fp32: the first R channels of each head are turned in pairs (j, j + R/2), with
+    ``interleaved`` (2j, 2j + 1), by the angle position * freqs[j].  ``positions`` (...) int32;
+    None: the token's index along the dimension before the heads.  Returns (B, C), dense, in
+    their type."""
+    dev = _gpu(B)
+    with _on(dev, stream):
+        shapes = B.shape, C.shape
+        p, args = _rotary_arguments(B, C, b_weight, c_weight, freqs, positions, interleaved, eps)
+        B_out = _output("B_out", B_out, shapes[0], B.dtype, dev)
+        C_out = _output("C_out", C_out, shapes[1], B.dtype, dev)
+        _check(_lib().ssd_rotary_norm_forward(ctypes.byref(p), *map(_ptr, args), _ptr(B_out), _ptr(C_out),
+                                              _current(dev)))
+    return B_out, C_out
+
+
+def rotary_norm_backward(B, C, b_weight, c_weight, freqs, dB_out, dC_out, positions=None, interleaved: bool = False,
+                         eps: float = 1e-5, workspace=None, stream=None):
+    """Gradients of <dB_out, B_out> + <dC_out, C_out> for :func:`rotary_norm` with the same
+    arguments, through ``ssd_rotary_norm_backward``; dB_out and dC_out fp32.  Returns a dict of
+    fp32 tensors dB, dC, db_weight, dc_weight (``freqs`` are constants)."""
+    dev, f32 = _gpu(B), torch.float32
+    with _on(dev, stream):
+        p, args = _rotary_arguments(B, C, b_weight, c_weight, freqs, positions, interleaved, eps)
+        dB_out = _given("dB_out", dB_out, B.shape, f32, dev)
+        dC_out = _given("dC_out", dC_out, C.shape, f32, dev)
+        out = {"dB": torch.empty(B.shape, dtype=f32, device=dev), "dC": torch.empty(C.shape, dtype=f32, device=dev),
+               "db_weight": torch.empty(p.headdim, dtype=f32, device=dev),
+               "dc_weight": torch.empty(p.headdim, dtype=f32, device=dev)}
+        ws, nbytes = _workspace(workspace, rotary_norm_backward_workspace_size(p), dev)
+        _check(_lib().ssd_rotary_norm_backward(ctypes.byref(p), *map(_ptr, args), _ptr(dB_out), _ptr(dC_out),
+                                               _ptr(out["dB"]), _ptr(out["dC"]), _ptr(out["db_weight"]),
+                                               _ptr(out["dc_weight"]), _ptr(ws), nbytes, _current(dev)))
+    return out
 
 
 # ------------------------------------------------------------------ norms

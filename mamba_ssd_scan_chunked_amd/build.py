@@ -21,7 +21,7 @@ SOURCES = ["ssd_api.cpp", "ssd_bwd_api.cpp", "ssd_bf16.hip", "ssd_f32.hip"] + [
     "ssd_%s_s%d_e%d_l%d.hip" % (t, sq, eu, lo) for t in ("bf16", "f32") for sq in (0, 1) for eu in (0, 1)
     for lo in (0, 1)] + ["ssd_bwd_bf16.hip", "ssd_bwd_f32.hip",
                            "block_common.hip", "ssd_conv.hip", "ssd_norm.hip", "ssd_selective.hip",
-                           "ssd_selective_bwd.hip", "ssd_selective_api.cpp"]
+                           "ssd_selective_bwd.hip", "ssd_selective_api.cpp", "ssd_recurrence.hip", "ssd_rotary.hip"]
 
 
 def hipcc() -> str:
