@@ -3,6 +3,22 @@
 //
 //   s = sigmoid(r),  L = A s,  a = e^L,  m = 1 - a,  beta = sqrt(1 - a^2) = sqrt(m (2 - m)),
 //   h_t = h_{t-1} - m h_{t-1} + beta sigmoid(i) x,      y = h  or  h silu(z).
+// Gradients, q_{t+1} being what token t + 1 sends back (or dfinal after a sequence's last token):
+//   g = dy [silu(z)] + q_{t+1},   q_t = g - m g,   dx = g beta sigmoid(i),
+//   M = g L (a h_{t-1} - sigmoid(i) x a^2 / beta),   dr = M (1 - s),   dA_log = sum of M.
+//
+// Memory-bound if the work is spread over the card and the inputs are read once.  There is one
+// state per channel, so a row's channels alone fill a few waves: rows are cut into tiles of
+// tokens, a workgroup each.  A tile's tokens stay in registers, in runs of a few tokens per lane;
+// runs, waves and tiles are joined as maps h -> P h + H (P the product of the decays): runs by
+// lane shuffles, waves through LDS, tiles through memory.  A tile publishes its map as soon as it
+// has it and takes those of the tiles before it; every 16th tile publishes its final state
+// instead, so that a tile reads 15 maps and one state at most and the waiting grows with a
+// sixteenth of the tiles.  Maps are always composed in the same order, whoever comes first:
+// results are deterministic.  A map of a channel is one 64-bit word that is its own flag (the
+// words are zeroed by a launch before), so nothing has to be fenced.  Tiles are handed out by a
+// counter, all rows' first tiles before their second: a tile waits only for tiles that
+// workgroups already running have taken, so every wait ends (and it is bounded besides).
 #include "ssd.h"
 
 #include <algorithm>
@@ -13,6 +29,17 @@
 
 namespace ssd {
 
+constexpr int kBlock = 64;           // channels of a workgroup
+constexpr int kWaves = 4;            // waves of a workgroup, at most
+constexpr int kGroup = 16;           // tiles from one published state to the next
+constexpr int kRunBack = 16;         // tokens of a wave backward, and between states kept for it
+
+// What the tiles of one direction publish: words (chains, tiles, 64) and (chains, groups, 64).
+struct Chain {
+    uint64_t *maps, *states;
+    unsigned* counter;
+};
+
 struct RecurrenceParams {
     const void *x, *r, *i, *z;
     const float *A_log, *init;
@@ -21,12 +48,31 @@ struct RecurrenceParams {
     float* fin;
     const float *dy, *dfin;
     float *dx, *dr, *di, *dz, *dinit;
-    float *part, *states;
+    float *part;                     // tiles' sums of dA_log, rows of D
+    float *kept;                     // state before every kRunBack-th token, (batch, n, D)
+    Chain chain;
     int64_t batch, T, D, nseqs, ldx, ldr, ldi, ldz;
+    unsigned nblk, ntile;            // blocks of channels, tiles per row
+    int stream;
 };
 
 // -exp(A_log), kept finite so that A times a gate of 0 is 0.
 __device__ inline float rate_of(float a_log) { return -fminf(expf(a_log), 1e30f); }
+
+// sigmoid(v) and sigmoid(-v), both to a few roundings of their own size, from t = e^-|v|
+// (argument and remainder as in exp_small); beyond +-100 as at +-100, where t is 0.
+struct Gate {
+    float s, n;
+};
+__device__ inline Gate gate_of(float v) {
+    float a = fabsf(v);
+    a = a > 100.f ? 100.f : a;       // NaN stays
+    const float hi = a * -kLog2e, lo = fmaf(a, -1.925963033500012e-08f, fmaf(a, -kLog2e, -hi));
+    float t = __builtin_amdgcn_exp2f(hi);
+    t = fmaf(t * lo, kLn2, t);
+    const float big = __builtin_amdgcn_rcpf(1.f + t), small = t * big;
+    return v < 0.f ? Gate{small, big} : Gate{big, small};
+}
 
 // m = 1 - e^L for L <= 0.  Near 0 the difference would cancel (and a long memory is a matter of
 // m, not of a): there m = -L (1 + L/2 + L^2/6 + ...), a polynomial fitted to the definition on
@@ -39,80 +85,501 @@ __device__ inline float one_minus_exp(float L) {
     const float far = 1.f - __builtin_amdgcn_exp2f(L * kLog2e);
     return L > -0.25f ? -L * q : far;
 }
+__device__ inline float beta_of(float m) { return __builtin_amdgcn_sqrtf(m * (2.f - m)); }
 
-struct Decay {
-    float s, L, m, beta;
+// ------------------------------------------------------------------ maps h -> P h + H
+// P = -1 marks a map that begins a sequence anew: what comes before it does not matter, whatever
+// it is (a select, so that Inf and NaN stay in their sequence).
+struct Map {
+    float P, H;
 };
-__device__ inline Decay decay_of(float r, float A) {
-    Decay d;
-    d.s = sigmoid(r);
-    d.L = A * d.s;
-    d.m = one_minus_exp(d.L);
-    d.beta = __builtin_amdgcn_sqrtf(d.m * (2.f - d.m));
-    return d;
+template <bool SEQ> __device__ inline Map then(Map first, Map second) {
+    if (SEQ && second.P < 0.f) return second;
+    Map m;
+    m.H = fmaf(second.P, first.H, second.H);
+    m.P = SEQ && first.P < 0.f ? -1.f : first.P * second.P;
+    return m;
+}
+template <bool SEQ> __device__ inline float apply(Map m, float h) {
+    return SEQ && m.P < 0.f ? m.H : fmaf(m.P, h, m.H);
 }
 
-template <typename T> __device__ inline float at(const void* p, int64_t i) { return (float)((const T*)p)[i]; }
-
-// A thread per (row, channel) walks the row.
-template <typename T> __global__ __launch_bounds__(64) void recurrence_forward_kernel(RecurrenceParams p) {
-    const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x, b = blockIdx.y;
-    if (c >= p.D) return;
-    const float A = rate_of(p.A_log[c]);
-    int64_t seq = b;
-    float h = 0.f;
-    for (int64_t t = 0; t < p.T; ++t) {
-        const int64_t n = b * p.T + t;
-        bool fresh = t == 0;
-        if (p.seq_idx) {
-            const int64_t id = clamp_id(p.seq_idx[n], p.nseqs);
-            fresh = fresh || id != seq;
-            seq = id;
-        }
-        if (fresh) h = p.init ? p.init[seq * p.D + c] : 0.f;
-        const Decay d = decay_of(at<T>(p.r, n * p.ldr + c), A);
-        h += fmaf(-d.m, h, d.beta * sigmoid(at<T>(p.i, n * p.ldi + c)) * at<T>(p.x, n * p.ldx + c));
-        if (p.states) p.states[n * p.D + c] = h;
-        if (p.y) ((T*)p.y)[n * p.D + c] = (T)(p.z ? h * silu(at<T>(p.z, n * p.ldz + c)) : h);
-        if (p.fin && (t + 1 == p.T || (p.seq_idx && clamp_id(p.seq_idx[n + 1], p.nseqs) != seq))) p.fin[seq * p.D + c] = h;
+// A map as a word that is never 0 in its low half.
+__device__ inline uint64_t word_of(Map m) {
+    const uint32_t low = __float_as_uint(m.P) + 1u;
+    return (uint64_t)__float_as_uint(m.H) << 32 | (low ? low : 1u);
+}
+__device__ inline Map map_of(uint64_t w) {
+    return {__uint_as_float((uint32_t)w - 1u), __uint_as_float((uint32_t)(w >> 32))};
+}
+__device__ inline void publish(uint64_t* p, Map m) {
+    __hip_atomic_store(p, word_of(m), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Up to N words `step` apart, each as soon as it is there.  The bound (about a second) is never
+// reached in a call by itself; it ends the waits of calls that were given one workspace at the
+// same time.  A word that did not come is 0: its map is NaN.
+template <int N> __device__ inline void await(const uint64_t* p, int64_t step, int n, uint64_t (&w)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) w[k] = 0;
+    for (int tries = 0; tries < 1 << 20; ++tries) {
+        bool all = true;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (k < n && !(uint32_t)w[k])
+                w[k] = __hip_atomic_load(p + k * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int k = 0; k < N; ++k) all = all && (k >= n || (uint32_t)w[k]);
+        if (all) break;
+        __builtin_amdgcn_s_sleep(2);
     }
 }
 
-template <typename T> __global__ __launch_bounds__(64) void recurrence_backward_kernel(RecurrenceParams p) {
-    const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x, b = blockIdx.y;
-    if (c >= p.D) return;
-    const float A = rate_of(p.A_log[c]);
-    float q = 0.f, dA = 0.f;
-    for (int64_t t = p.T - 1; t >= 0; --t) {
-        const int64_t n = b * p.T + t;
-        int64_t seq = b;
-        bool fresh = t == 0, last = t + 1 == p.T;
-        if (p.seq_idx) {
-            seq = clamp_id(p.seq_idx[n], p.nseqs);
-            fresh = fresh || clamp_id(p.seq_idx[n - 1], p.nseqs) != seq;
-            last = last || clamp_id(p.seq_idx[n + 1], p.nseqs) != seq;
+// Shared memory of a workgroup.
+struct Joint {
+    Map total[kWaves][kBlock];       // waves' maps
+    Map before[kWaves][kBlock];      // of the tiles before, in as many parts
+    float start[kWaves][kBlock];     // state before each wave
+    float carry[kBlock];             // state before the tile
+    unsigned ticket;
+};
+
+// The maps of the waves are in j.total.  Returns, in j.start of the own wave, the state that
+// reaches it; `first` is what reaches the row's first tile.  `at` is the tile's place in the
+// order of the walk, of `ntile`; lanes are channels here.
+template <bool SEQ>
+__device__ inline void join(const Chain& c, Joint& j, int64_t chain, unsigned at, unsigned ntile, int wave, int waves,
+                            bool forward, float first) {
+    const int lane = threadIdx.x & 63;
+    const int w = forward ? wave : waves - 1 - wave;          // place of the wave in the order of the walk
+    auto total = [&](int k) { return j.total[forward ? k : waves - 1 - k][lane]; };
+    __syncthreads();
+    float h = first;
+    if (ntile > 1) {
+        const unsigned group = at / kGroup, from = group * kGroup;
+        Map own{1.f, 0.f};
+        if (w == 0) {
+            for (int k = 0; k < waves; ++k) own = then<SEQ>(own, total(k));
+            // the group's last tile publishes its state; nobody follows the row's last one
+            if (at != from + kGroup - 1 && at + 1 != ntile) publish(c.maps + (chain * ntile + at) * kBlock + lane, own);
         }
-        if (last) q = p.dfin ? p.dfin[seq * p.D + c] : 0.f;
-        const float before = fresh ? (p.init ? p.init[seq * p.D + c] : 0.f) : p.states[(n - 1) * p.D + c];
-        float g = p.dy[n * p.D + c];
-        if (p.z) {
-            const float z = at<T>(p.z, n * p.ldz + c), s = sigmoid(z);
-            p.dz[n * p.D + c] = g * p.states[n * p.D + c] * silu_slope(z, s);
-            g *= z * s;
+        // the tiles of the group before this one, in `waves` parts
+        constexpr int kPart = kGroup / kWaves;
+        const int n = (int)(at - from), per = (n + waves - 1) / waves, lo = w * per, hi = lo + per < n ? lo + per : n;
+        Map part{1.f, 0.f};
+        for (int k = lo; k < hi; k += kPart) {
+            uint64_t word[kPart];
+            await(c.maps + (chain * ntile + from + k) * kBlock + lane, (int64_t)kBlock, hi - k < kPart ? hi - k : kPart, word);
+#pragma unroll
+            for (int e = 0; e < kPart; ++e)
+                if (k + e < hi) part = then<SEQ>(part, map_of(word[e]));
         }
-        g += q;
-        const Decay d = decay_of(at<T>(p.r, n * p.ldr + c), A);
-        const float iv = at<T>(p.i, n * p.ldi + c), si = sigmoid(iv), x = at<T>(p.x, n * p.ldx + c), u = si * x;
-        const float a = 1.f - d.m, ratio = d.beta > 0.f ? d.L / d.beta : 0.f;
-        const float M = g * (d.L * a * before - u * a * a * ratio);
-        p.dx[n * p.D + c] = g * d.beta * si;
-        p.di[n * p.D + c] = g * d.beta * u * sigmoid(-iv);
-        p.dr[n * p.D + c] = M * sigmoid(-at<T>(p.r, n * p.ldr + c));
-        dA += M;
-        q = g - d.m * g;
-        if (fresh && p.dinit) p.dinit[seq * p.D + c] = q;
+        j.before[w][lane] = part;
+        const unsigned ngroup = (ntile + kGroup - 1) / kGroup;
+        if (w == 0 && group > 0) {
+            uint64_t word[1];
+            await(c.states + (chain * ngroup + group - 1) * kBlock + lane, (int64_t)0, 1, word);
+            h = map_of(word[0]).H;
+        }
+        __syncthreads();
+        if (w == 0) {
+            for (int k = 0; k < waves; ++k) h = apply<SEQ>(j.before[k][lane], h);
+            if (at == from + kGroup - 1 && at + 1 != ntile)
+                publish(c.states + (chain * ngroup + group) * kBlock + lane, Map{1.f, apply<SEQ>(own, h)});
+            j.carry[lane] = h;
+        }
+        __syncthreads();
+        h = j.carry[lane];
     }
-    p.part[b * p.D + c] = dA;
+    for (int k = 0; k < w; ++k) h = apply<SEQ>(total(k), h);
+    j.start[wave][lane] = h;
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Where a workgroup and a lane work.  LPT lanes with V channels each hold a token's 64 channels;
+// the wave's 64 / LPT lane groups hold a run of R tokens each.  The last vector of a row is moved
+// back to end with it: it repeats channels of its neighbour with equal results.
+struct Tile {
+    int64_t b, c0, chain;
+    unsigned at;
+    int group, slot;
+    bool active;                     // the lane's channels exist
+};
+template <int V> __device__ inline Tile tile_of(const RecurrenceParams& p, Joint& j) {
+    constexpr int LPT = kBlock / V;
+    unsigned t = blockIdx.x;
+    if (p.ntile > 1) {
+        if (threadIdx.x == 0) j.ticket = __hip_atomic_fetch_add(p.chain.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        t = __builtin_amdgcn_readfirstlane(j.ticket);
+    }
+    const unsigned chains = p.nblk * (unsigned)p.batch, lane = threadIdx.x & 63;
+    Tile q;
+    q.at = t / chains;
+    q.chain = t % chains;
+    q.b = (unsigned)q.chain / p.nblk;
+    const int64_t first = (int64_t)((unsigned)q.chain % p.nblk) * kBlock;
+    q.group = lane / LPT;
+    q.slot = (lane % LPT) * V;
+    q.active = first + q.slot < p.D;
+    const int64_t c = first + q.slot;
+    q.c0 = c + V <= p.D ? c : (p.D >= V ? p.D - V : 0);
+    return q;
+}
+
+// Sequence of each token of a run, and which tokens begin or end one.
+template <int R> struct Runs {
+    int64_t id[R];
+    unsigned fresh, last;            // bits
+};
+template <int R> __device__ inline Runs<R> runs_of(const RecurrenceParams& p, int64_t b, int64_t t0) {
+    Runs<R> q;
+    q.fresh = q.last = 0;
+    const int32_t* s = p.seq_idx + b * p.T;
+    int64_t prev = t0 > 0 && t0 <= p.T ? clamp_id(s[t0 - 1], p.nseqs) : -1;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const int64_t t = t0 + k;
+        q.id[k] = t < p.T ? clamp_id(s[t], p.nseqs) : -1;
+        if (t < p.T && q.id[k] != prev) {
+            q.fresh |= 1u << k;
+            if (k) q.last |= 1u << (k - 1);
+        }
+        if (k && t == p.T) q.last |= 1u << (k - 1);
+        prev = q.id[k];
+    }
+    const int64_t t = t0 + R - 1;
+    if (t < p.T && (t + 1 == p.T || clamp_id(s[t + 1], p.nseqs) != q.id[R - 1])) q.last |= 1u << (R - 1);
+    return q;
+}
+
+template <int V> __device__ inline void load_or(const float* p, int64_t at, float other, float (&v)[V]) {
+    if (p) {
+        load_f32<V>(p + at, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = other;
+    }
+}
+
+// Maps of the lane groups before (after) the own one in its wave, per channel, and the wave's
+// map into `total`.
+template <int V, bool SEQ, bool FORWARD> __device__ inline void scan_groups(Map (&m)[V], Map (&before)[V], Map* total, int slot, int group) {
+    constexpr int LPT = kBlock / V, N = V;
+    const int place = FORWARD ? group : N - 1 - group;
+#pragma unroll
+    for (int d = 1; d < N; d *= 2) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Map o = FORWARD ? Map{__shfl_up(m[v].P, d * LPT), __shfl_up(m[v].H, d * LPT)}
+                                  : Map{__shfl_down(m[v].P, d * LPT), __shfl_down(m[v].H, d * LPT)};
+            if (place >= d) m[v] = then<SEQ>(o, m[v]);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if constexpr (N > 1) {
+            const Map o = FORWARD ? Map{__shfl_up(m[v].P, LPT), __shfl_up(m[v].H, LPT)}
+                                  : Map{__shfl_down(m[v].P, LPT), __shfl_down(m[v].H, LPT)};
+            before[v] = place ? o : Map{1.f, 0.f};
+        } else {
+            before[v] = Map{1.f, 0.f};
+        }
+        if (place == N - 1) total[slot + v] = m[v];
+    }
+}
+
+// A step of the state.
+__device__ inline float advance(float h, float m, float u) { return h + fmaf(-m, h, u); }
+
+// Whole rows.  TOK tokens per wave; KEEP: no output, but the state before every kRunBack-th token.
+template <typename T, int V, int TOK, bool SEQ, bool GATE, bool STREAM, bool KEEP>
+__global__ __launch_bounds__(64 * kWaves) void recurrence_forward_kernel(RecurrenceParams p) {
+    constexpr int R = TOK / V;
+    __shared__ Joint j;
+    const Tile q = tile_of<V>(p, j);
+    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int64_t t0 = ((int64_t)q.at * waves + wave) * TOK + q.group * R;
+    float m[R][V], u[R][V];
+    Pack<T, V> z[GATE ? R : 1];
+    Map run[V], before[V];
+    Runs<SEQ ? R : 1> s{};
+#pragma unroll
+    for (int v = 0; v < V; ++v) run[v] = {1.f, 0.f};
+    if (SEQ) s = runs_of<SEQ ? R : 1>(p, q.b, t0);
+    if (q.active) {
+        float A[V];
+        Pack<T, V> x[R], r[R], g[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t n = q.b * p.T + (t0 + k < p.T ? t0 + k : p.T - 1);
+            r[k] = load_pack<V>((const T*)p.r + n * p.ldr + q.c0);
+            g[k] = load_pack<V>((const T*)p.i + n * p.ldi + q.c0);
+            x[k] = load_pack<V>((const T*)p.x + n * p.ldx + q.c0);
+            if constexpr (GATE) z[k] = load_pack<V>((const T*)p.z + n * p.ldz + q.c0);
+        }
+        load_f32<V>(p.A_log + q.c0, A);
+#pragma unroll
+        for (int v = 0; v < V; ++v) A[v] = rate_of(A[v]);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const bool real = t0 + k < p.T;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float mm = one_minus_exp(A[v] * gate_of((float)r[k].v[v]).s);
+                m[k][v] = real ? mm : 0.f;
+                u[k][v] = real ? beta_of(mm) * gate_of((float)g[k].v[v]).s * (float)x[k].v[v] : 0.f;
+            }
+            const bool fresh = SEQ && (s.fresh >> k & 1);
+            if (fresh && p.init) {
+                float h[V];
+                load_f32<V>(p.init + s.id[SEQ ? k : 0] * p.D + q.c0, h);
+#pragma unroll
+                for (int v = 0; v < V; ++v) u[k][v] = advance(h[v], m[k][v], u[k][v]);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                run[v].H = fresh ? u[k][v] : advance(run[v].H, m[k][v], u[k][v]);
+                run[v].P = fresh || (SEQ && run[v].P < 0.f) ? -1.f : fmaf(-m[k][v], run[v].P, run[v].P);
+            }
+        }
+    }
+    scan_groups<V, SEQ, true>(run, before, j.total[wave], q.slot, q.group);
+    // the row's initial state; a row of packed sequences begins with a fresh token
+    const int64_t c = q.chain % p.nblk * kBlock + (threadIdx.x & 63);
+    const int64_t own = c < p.D ? c : p.D - 1;
+    float first = 0.f;
+    if (!SEQ && p.init) {
+        // channel of the lane's slot: the last vector's slots are moved back with it
+        const int64_t slot = threadIdx.x & 63, vec = c - slot % V;
+        const int64_t at = vec + V <= p.D ? c : (p.D >= V ? p.D - V + slot % V : own);
+        first = p.init[q.b * p.D + (at < p.D ? at : p.D - 1)];
+    }
+    join<SEQ>(p.chain, j, q.chain, q.at, p.ntile, wave, waves, true, first);
+    if (!q.active) return;
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = apply<SEQ>(before[v], j.start[wave][q.slot + v]);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const int64_t t = t0 + k, n = q.b * p.T + t;
+        if (t >= p.T) break;
+        if constexpr (KEEP) {
+            if (t % kRunBack == 0) store_f32<V>(p.kept + (q.b * ((p.T + kRunBack - 1) / kRunBack) + t / kRunBack) * p.D + q.c0, h);
+        }
+        const bool fresh = SEQ && (s.fresh >> k & 1);
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = fresh ? u[k][v] : advance(h[v], m[k][v], u[k][v]);
+        if constexpr (!KEEP) {
+            float y[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) y[v] = GATE ? h[v] * silu_for<T>((float)z[GATE ? k : 0].v[v]) : h[v];
+            store_f32<V, STREAM>((T*)p.y + n * p.D + q.c0, y);
+            if (p.fin && (SEQ ? (s.last >> k & 1) : t + 1 == p.T))
+                store_f32<V>(p.fin + (SEQ ? s.id[SEQ ? k : 0] : q.b) * p.D + q.c0, h);
+        }
+    }
+}
+
+// Gradients of whole rows, tiles from the last to the first.
+template <typename T, int V, bool SEQ, bool GATE, bool STREAM>
+__global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(RecurrenceParams p) {
+    constexpr int TOK = kRunBack, R = TOK / V;
+    __shared__ Joint j;
+    __shared__ float sums[kWaves][kBlock];
+    const Tile q = tile_of<V>(p, j);
+    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const unsigned tile = p.ntile - 1 - q.at;
+    const int64_t w0 = ((int64_t)tile * waves + wave) * TOK, t0 = w0 + q.group * R;
+    Pack<T, V> x[R], r[R], g[R];
+    float m[R][V], hp[R][V], gy[R][V], A[V];
+    Map run[V], before[V];
+    Runs<SEQ ? R : 1> s{};
+    if (SEQ) s = runs_of<SEQ ? R : 1>(p, q.b, t0);
+    Map none[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) run[v] = none[v] = {1.f, 0.f};
+    float u[R][V];
+    if (q.active) {
+        load_f32<V>(p.A_log + q.c0, A);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t n = q.b * p.T + (t0 + k < p.T ? t0 + k : p.T - 1);
+            r[k] = load_pack<V>((const T*)p.r + n * p.ldr + q.c0);
+            g[k] = load_pack<V>((const T*)p.i + n * p.ldi + q.c0);
+            x[k] = load_pack<V>((const T*)p.x + n * p.ldx + q.c0);
+            load_f32<V>(p.dy + n * p.D + q.c0, gy[k]);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) A[v] = rate_of(A[v]);
+        // forwards through the run, from nothing
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const bool real = t0 + k < p.T, fresh = SEQ && (s.fresh >> k & 1);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float mm = one_minus_exp(A[v] * gate_of((float)r[k].v[v]).s);
+                m[k][v] = real ? mm : 0.f;
+                u[k][v] = real ? beta_of(mm) * gate_of((float)g[k].v[v]).s * (float)x[k].v[v] : 0.f;
+                hp[k][v] = 0.f;
+            }
+            if (fresh && p.init) load_f32<V>(p.init + s.id[SEQ ? k : 0] * p.D + q.c0, hp[k]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                run[v].H = advance(fresh ? hp[k][v] : run[v].H, m[k][v], u[k][v]);
+                run[v].P = fresh || (SEQ && run[v].P < 0.f) ? -1.f : fmaf(-m[k][v], run[v].P, run[v].P);
+            }
+        }
+    }
+    scan_groups<V, SEQ, true>(run, before, j.total[wave], q.slot, q.group);
+    Map back[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) back[v] = {1.f, 0.f};
+    if (q.active) {
+        float h[V];
+        const int64_t n = (p.T + kRunBack - 1) / kRunBack, piece = w0 / kRunBack < n ? w0 / kRunBack : n - 1;
+        if (p.kept) load_f32<V>(p.kept + (q.b * n + piece) * p.D + q.c0, h);
+        else load_or<V>(SEQ ? nullptr : p.init, q.b * p.D + q.c0, 0.f, h);
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = apply<SEQ>(before[v], h[v]);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const bool real = t0 + k < p.T, fresh = SEQ && (s.fresh >> k & 1);
+            const bool last = SEQ ? (s.last >> k & 1) : t0 + k + 1 == p.T;
+            const int64_t at = q.b * p.T + (real ? t0 + k : p.T - 1);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (!fresh) hp[k][v] = h[v];
+                h[v] = advance(hp[k][v], m[k][v], u[k][v]);
+                if (!real) gy[k][v] = 0.f;
+            }
+            if constexpr (GATE) {
+                float z[V], dz[V];
+                load_f32<V>((const T*)p.z + at * p.ldz + q.c0, z);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float sz = gate_of(z[v]).s;
+                    dz[v] = gy[k][v] * h[v] * silu_slope(z[v], sz);
+                    gy[k][v] *= z[v] * sz;
+                }
+                if (real) store_f32<V, STREAM>(p.dz + at * p.D + q.c0, dz);
+            }
+            if (last && p.dfin) {
+                float d[V];
+                load_f32<V>(p.dfin + (SEQ ? s.id[SEQ ? k : 0] : q.b) * p.D + q.c0, d);
+#pragma unroll
+                for (int v = 0; v < V; ++v) gy[k][v] += d[v];
+            }
+        }
+        // backwards through the run, from nothing
+#pragma unroll
+        for (int k = R - 1; k >= 0; --k) {
+            const bool fresh = SEQ && (s.fresh >> k & 1);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float e = gy[k][v] + back[v].H;
+                back[v].H = fresh ? 0.f : fmaf(-m[k][v], e, e);
+                back[v].P = fresh || (SEQ && back[v].P < 0.f) ? -1.f : fmaf(-m[k][v], back[v].P, back[v].P);
+            }
+        }
+    }
+    __syncthreads();
+    scan_groups<V, SEQ, false>(back, before, j.total[wave], q.slot, q.group);
+    join<SEQ>(p.chain, j, q.chain, q.at, p.ntile, wave, waves, false, 0.f);
+    float dA[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) dA[v] = 0.f;
+    if (q.active) {
+        float e[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) e[v] = apply<SEQ>(before[v], j.start[wave][q.slot + v]);
+#pragma unroll
+        for (int k = R - 1; k >= 0; --k) {
+            const int64_t t = t0 + k, n = q.b * p.T + t;
+            if (t >= p.T) continue;
+            float dx[V], dr[V], di[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float d = gy[k][v] + e[v], mm = m[k][v], a = 1.f - mm;
+                const Gate sr = gate_of((float)r[k].v[v]), si = gate_of((float)g[k].v[v]);
+                const float L = A[v] * sr.s, beta = beta_of(mm), in = si.s * (float)x[k].v[v];
+                const float ratio = beta > 0.f ? L * __builtin_amdgcn_rcpf(beta) : 0.f;
+                const float M = d * fmaf(L * a, hp[k][v], -in * a * a * ratio);
+                dx[v] = d * beta * si.s;
+                di[v] = d * beta * in * si.n;
+                dr[v] = M * sr.n;
+                dA[v] += M;
+                e[v] = fmaf(-mm, d, d);
+            }
+            store_f32<V, STREAM>(p.dx + n * p.D + q.c0, dx);
+            store_f32<V, STREAM>(p.dr + n * p.D + q.c0, dr);
+            store_f32<V, STREAM>(p.di + n * p.D + q.c0, di);
+            const bool fresh = SEQ ? (s.fresh >> k & 1) : t == 0;
+            if (fresh) {
+                if (p.dinit) store_f32<V>(p.dinit + (SEQ ? s.id[SEQ ? k : 0] : q.b) * p.D + q.c0, e);
+#pragma unroll
+                for (int v = 0; v < V; ++v) e[v] = 0.f;
+            }
+        }
+    }
+    // sums over the lane groups, then over the waves
+    constexpr int LPT = kBlock / V;
+#pragma unroll
+    for (int d = LPT; d < 64; d *= 2)
+#pragma unroll
+        for (int v = 0; v < V; ++v) dA[v] += __shfl_xor(dA[v], d);
+    if (q.group == 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) sums[wave][q.slot + v] = dA[v];
+    }
+    __syncthreads();
+    if (wave == 0 && q.group == 0 && q.active) {
+        for (int w = 1; w < waves; ++w)
+#pragma unroll
+            for (int v = 0; v < V; ++v) dA[v] += sums[w][q.slot + v];
+        store_f32<V>(p.part + (q.b * p.ntile + tile) * p.D + q.c0, dA);
+    }
+}
+
+// One token: a thread per (row, channel).
+template <typename T> __global__ __launch_bounds__(256) void recurrence_step_kernel(RecurrenceParams p) {
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (n >= p.batch * p.D) return;
+    const int64_t b = n / p.D, c = n % p.D;
+    const float m = one_minus_exp(rate_of(p.A_log[c]) * gate_of((float)((const T*)p.r)[b * p.ldr + c]).s);
+    const float u = beta_of(m) * gate_of((float)((const T*)p.i)[b * p.ldi + c]).s * (float)((const T*)p.x)[b * p.ldx + c];
+    const float h = advance(p.init[n], m, u);
+    p.fin[n] = h;
+    ((T*)p.y)[n] = (T)(p.z ? h * silu_for<T>((float)((const T*)p.z)[b * p.ldz + c]) : h);
+}
+
+// ------------------------------------------------------------------ launches
+enum Pass { kForward, kKeep, kBackward };
+template <typename T, int V, bool SEQ, bool GATE, bool STREAM>
+static void launch_one(Pass pass, const RecurrenceParams& p, int waves, hipStream_t s) {
+    const dim3 grid(p.nblk * (unsigned)p.batch * p.ntile), block(64 * waves);
+    constexpr int TOK = V == 1 ? 16 : 32;
+    if (pass == kForward) hipLaunchKernelGGL((recurrence_forward_kernel<T, V, TOK, SEQ, GATE, STREAM, false>), grid, block, 0, s, p);
+    if (pass == kBackward) hipLaunchKernelGGL((recurrence_backward_kernel<T, V, SEQ, GATE, STREAM>), grid, block, 0, s, p);
+    if constexpr (!GATE && !STREAM) {
+        if (pass == kKeep) hipLaunchKernelGGL((recurrence_forward_kernel<T, V, TOK, SEQ, false, false, true>), grid, block, 0, s, p);
+    }
+}
+template <typename T, int V, bool STREAM> static void launch_seq(Pass pass, const RecurrenceParams& p, int waves, hipStream_t s) {
+    const bool gate = p.z && pass != kKeep;
+    if (p.seq_idx) {
+        if (gate) launch_one<T, V, true, true, STREAM>(pass, p, waves, s);
+        else launch_one<T, V, true, false, STREAM>(pass, p, waves, s);
+    } else {
+        if (gate) launch_one<T, V, false, true, STREAM>(pass, p, waves, s);
+        else launch_one<T, V, false, false, STREAM>(pass, p, waves, s);
+    }
+}
+// Rows narrower than a vector take a channel per lane.
+template <typename T, int V> static hipError_t launch_pass(Pass pass, const RecurrenceParams& p, int waves, hipStream_t s) {
+    if (p.D < V) launch_seq<T, 1, false>(pass, p, waves, s);
+    else if (p.stream && pass != kKeep) launch_seq<T, V, true>(pass, p, waves, s);
+    else launch_seq<T, V, false>(pass, p, waves, s);
+    return hipGetLastError();
 }
 
 }  // namespace ssd
@@ -122,6 +589,23 @@ namespace {
 using namespace ssd_host;
 
 constexpr int64_t kMaxDim = int64_t(1) << 31;
+
+// Channels per lane, blocks of channels, waves of a workgroup and tiles per row.
+struct Shape {
+    int V;
+    int64_t nblk, waves, ntile;
+};
+Shape shape_of(const ssd_recurrence_problem_t* p, bool back) {
+    const int V = p->dtype == SSD_DTYPE_BF16 ? 8 : 4;
+    Shape s;
+    s.V = p->channels < V ? 1 : V;
+    s.nblk = (p->channels + ssd::kBlock - 1) / ssd::kBlock;
+    const int64_t tokens = back || s.V == 1 ? ssd::kRunBack : 32;        // of a wave
+    const int64_t runs = std::max<int64_t>(1, (p->seqlen + tokens - 1) / tokens);
+    s.waves = std::min<int64_t>(ssd::kWaves, runs);
+    s.ntile = (runs + s.waves - 1) / s.waves;
+    return s;
+}
 
 int validate(const ssd_recurrence_problem_t* p) {
     if (!p) return SSD_ERR_NULL_POINTER;
@@ -135,7 +619,12 @@ int validate(const ssd_recurrence_problem_t* p) {
     const double widest = double(std::max({p->ldx, p->ldr, p->ldi, p->ldz}));
     if (double(p->batch) * double(p->seqlen) * widest > 4e17 || double(p->nseqs) * p->channels > 4e17)
         return SSD_ERR_BAD_SHAPE;
-    if (p->batch >= 65536) return SSD_ERR_UNSUPPORTED;
+    // a launch holds fewer than 2^32 threads, a tile's chains fewer than 2^31
+    for (bool back : {false, true}) {
+        const Shape s = shape_of(p, back);
+        if (double(p->batch) * s.nblk >= 2e9 || double(p->batch) * s.nblk * s.ntile * 64 * s.waves >= 4e9)
+            return SSD_ERR_UNSUPPORTED;
+    }
     return SSD_OK;
 }
 
@@ -160,9 +649,48 @@ RecSizes rec_sizes(const ssd_recurrence_problem_t* p) {
 
 bool empty(const ssd_recurrence_problem_t* p) { return p->batch == 0 || p->seqlen == 0; }
 
-int64_t forward_bytes(const ssd_recurrence_problem_t*) { return 0; }
-int64_t backward_bytes(const ssd_recurrence_problem_t* p) {
-    return empty(p) ? 0 : align256(p->batch * p->seqlen * p->channels * 4) + align256(p->batch * p->channels * 4);
+// What the tiles publish, in bytes from the workspace's start: a counter, maps, states.
+struct ChainSpace {
+    int64_t maps, states, total;
+};
+ChainSpace chain_space(const ssd_recurrence_problem_t* p, const Shape& s) {
+    ChainSpace c{};
+    if (empty(p) || s.ntile == 1) return c;
+    const int64_t chains = p->batch * s.nblk, groups = (s.ntile + ssd::kGroup - 1) / ssd::kGroup;
+    c.maps = 256;
+    c.states = c.maps + chains * s.ntile * ssd::kBlock * 8;
+    c.total = align256(c.states + chains * groups * ssd::kBlock * 8);
+    return c;
+}
+// Backwards: both directions' chains, the kept states, the tiles' sums.
+struct BackwardSpace {
+    int64_t back, kept, part, total;
+};
+int64_t pieces_of(const ssd_recurrence_problem_t* p) { return (p->seqlen + ssd::kRunBack - 1) / ssd::kRunBack; }
+BackwardSpace backward_space(const ssd_recurrence_problem_t* p) {
+    BackwardSpace w{};
+    if (empty(p)) return w;
+    const Shape s = shape_of(p, true);
+    const int64_t pieces = pieces_of(p);
+    w.back = pieces > 1 ? chain_space(p, shape_of(p, false)).total : 0;
+    w.kept = w.back + chain_space(p, s).total;
+    w.part = w.kept + (pieces > 1 ? align256(p->batch * pieces * p->channels * 4) : 0);
+    w.total = w.part + (p->batch * s.ntile > 1 ? align256(p->batch * s.ntile * p->channels * 4) : 0);
+    return w;
+}
+int64_t forward_bytes(const ssd_recurrence_problem_t* p) { return chain_space(p, shape_of(p, false)).total; }
+int64_t backward_bytes(const ssd_recurrence_problem_t* p) { return backward_space(p).total; }
+
+ssd::Chain chain_at(const ssd_recurrence_problem_t* p, const Shape& s, void* at) {
+    const ChainSpace c = chain_space(p, s);
+    char* base = static_cast<char*>(at);
+    ssd::Chain r{};
+    if (c.total) {
+        r.counter = reinterpret_cast<unsigned*>(base);
+        r.maps = reinterpret_cast<uint64_t*>(base + c.maps);
+        r.states = reinterpret_cast<uint64_t*>(base + c.states);
+    }
+    return r;
 }
 
 ssd::RecurrenceParams params_of(const ssd_recurrence_problem_t* p, const void* x, const void* r, const void* i,
@@ -193,14 +721,14 @@ int done(const char* what, const ssd_recurrence_problem_t* p, hipError_t e) {
     return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
-dim3 grid_of(const ssd_recurrence_problem_t* p) { return dim3((unsigned)((p->channels + 63) / 64), (unsigned)p->batch); }
-
-hipError_t run_forward(const ssd_recurrence_problem_t* p, const ssd::RecurrenceParams& c, hipStream_t s) {
-    if (p->dtype == SSD_DTYPE_BF16)
-        hipLaunchKernelGGL((ssd::recurrence_forward_kernel<__bf16>), grid_of(p), dim3(64), 0, s, c);
-    else
-        hipLaunchKernelGGL((ssd::recurrence_forward_kernel<float>), grid_of(p), dim3(64), 0, s, c);
-    return hipGetLastError();
+// One pass over the rows; `space` holds its chain, zeroed.
+hipError_t run_pass(const ssd_recurrence_problem_t* p, ssd::Pass pass, ssd::RecurrenceParams c, void* space, hipStream_t st) {
+    const Shape s = shape_of(p, pass == ssd::kBackward);
+    c.nblk = (unsigned)s.nblk;
+    c.ntile = (unsigned)s.ntile;
+    c.chain = chain_at(p, s, space);
+    return p->dtype == SSD_DTYPE_BF16 ? ssd::launch_pass<__bf16, 8>(pass, c, (int)s.waves, st)
+                                      : ssd::launch_pass<float, 4>(pass, c, (int)s.waves, st);
 }
 
 }  // namespace
@@ -246,7 +774,10 @@ int ssd_recurrence_forward(const ssd_recurrence_problem_t* p, const void* x, con
     ssd::RecurrenceParams c = params_of(p, x, r, i, A_log, z, init_state, seq_idx);
     c.y = y;
     c.fin = final_state;
-    return done("forward", p, run_forward(p, c, st));
+    c.stream = n.y > ssd::kStreamBytes;
+    hipError_t h = ssd::launch_fill(static_cast<float*>(workspace), wsb / 4, st);
+    if (h == hipSuccess) h = run_pass(p, ssd::kForward, c, workspace, st);
+    return done("forward", p, h);
 }
 
 int ssd_recurrence_step(const ssd_recurrence_problem_t* p, const void* x, const void* r, const void* i,
@@ -272,7 +803,11 @@ int ssd_recurrence_step(const ssd_recurrence_problem_t* p, const void* x, const 
     ssd::RecurrenceParams c = params_of(p, x, r, i, A_log, z, state, nullptr);
     c.y = y;
     c.fin = state_out;
-    return done("step", p, run_forward(p, c, static_cast<hipStream_t>(stream)));
+    const dim3 grid((unsigned)((p->batch * p->channels + 255) / 256));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (p->dtype == SSD_DTYPE_BF16) hipLaunchKernelGGL((ssd::recurrence_step_kernel<__bf16>), grid, dim3(256), 0, st, c);
+    else hipLaunchKernelGGL((ssd::recurrence_step_kernel<float>), grid, dim3(256), 0, st, c);
+    return done("step", p, hipGetLastError());
 }
 
 int ssd_recurrence_backward(const ssd_recurrence_problem_t* p, const void* x, const void* r, const void* i,
@@ -311,31 +846,34 @@ int ssd_recurrence_backward(const ssd_recurrence_problem_t* p, const void* x, co
         return done("backward", p, e2);
     }
     ssd::RecurrenceParams c = params_of(p, x, r, i, A_log, z, init_state, seq_idx);
-    c.states = static_cast<float*>(workspace);
-    e2 = run_forward(p, c, st);
-    if (e2 != hipSuccess) return done("backward", p, e2);
-    c.dy = dy;
-    c.dfin = dfinal;
-    c.dx = dx;
-    c.dr = dr;
-    c.di = di;
-    c.dz = dz;
-    c.dinit = dinit;
-    c.part = c.states + align256(p->batch * p->seqlen * p->channels * 4) / 4;
-    // ids that do not occur keep a zero gradient
-    if (seq_idx && dinit) e2 = ssd::launch_fill(dinit, n.state / 4, st);
-    if (e2 == hipSuccess) {
-        if (p->dtype == SSD_DTYPE_BF16)
-            hipLaunchKernelGGL((ssd::recurrence_backward_kernel<__bf16>), grid_of(p), dim3(64), 0, st, c);
-        else
-            hipLaunchKernelGGL((ssd::recurrence_backward_kernel<float>), grid_of(p), dim3(64), 0, st, c);
-        e2 = hipGetLastError();
+    const BackwardSpace w = backward_space(p);
+    char* base = static_cast<char*>(workspace);
+    const Shape s = shape_of(p, true);
+    const bool direct = p->batch * s.ntile == 1;         // a single tile writes dA_log itself
+    e2 = ssd::launch_fill(reinterpret_cast<float*>(base), w.kept / 4, st);
+    if (e2 == hipSuccess && pieces_of(p) > 1) {
+        c.kept = reinterpret_cast<float*>(base + w.kept);
+        e2 = run_pass(p, ssd::kKeep, c, base, st);
     }
+    // ids that do not occur keep a zero gradient
+    if (e2 == hipSuccess && seq_idx && dinit) e2 = ssd::launch_fill(dinit, n.state / 4, st);
     if (e2 == hipSuccess) {
+        c.dy = dy;
+        c.dfin = dfinal;
+        c.dx = dx;
+        c.dr = dr;
+        c.di = di;
+        c.dz = dz;
+        c.dinit = dinit;
+        c.part = direct ? dA_log : reinterpret_cast<float*>(base + w.part);
+        c.stream = n.f > ssd::kStreamBytes;
+        e2 = run_pass(p, ssd::kBackward, c, base + w.back, st);
+    }
+    if (e2 == hipSuccess && !direct) {
         ssd::ColumnSums cs{};
         cs.part = c.part;
         cs.out = dA_log;
-        cs.rows = p->batch;
+        cs.rows = p->batch * s.ntile;
         cs.cols = cs.split = cs.split2 = p->channels;
         e2 = ssd::launch_column_sums(cs, st);
     }
