@@ -52,40 +52,49 @@ struct RecurrenceParams {
     float *kept;                     // state before every kRunBack-th token, (batch, n, D)
     Chain chain;
     int64_t batch, T, D, nseqs, ldx, ldr, ldi, ldz;
+    int64_t pieces;                  // kept states per row
     unsigned nblk, ntile;            // blocks of channels, tiles per row
     int stream;
 };
 
-// -exp(A_log), kept finite so that A times a gate of 0 is 0.
-__device__ inline float rate_of(float a_log) { return -fminf(expf(a_log), 1e30f); }
+// A log2(e), kept finite so that a gate of 0 times it is 0.
+__device__ inline float rate_of(float a_log) { return -kLog2e * fminf(expf(a_log), 1e30f); }
 
-// sigmoid(v) and sigmoid(-v), both to a few roundings of their own size, from t = e^-|v|
-// (argument and remainder as in exp_small); beyond +-100 as at +-100, where t is 0.
+// sigmoid(v), and sigmoid(-v) to its own relative precision, from t = e^-|v|.  EXACT: the
+// exponent's rounding is made good, as in exp_small (beyond +-100 as at +-100, where t is 0; NaN
+// stays).  Else t is off by |v| roundings, which for a bf16 v is 2^-16 of v's own step.
 struct Gate {
     float s, n;
 };
-__device__ inline Gate gate_of(float v) {
+template <bool EXACT> __device__ inline float exp_minus(float v) {
+    if constexpr (!EXACT) return __builtin_amdgcn_exp2f(v * -kLog2e);
+    const float hi = v * -kLog2e, lo = fmaf(v, -1.925963033500012e-08f, fmaf(v, -kLog2e, -hi));
+    const float t = __builtin_amdgcn_exp2f(hi);
+    return fmaf(t * lo, kLn2, t);
+}
+template <bool EXACT> __device__ inline Gate gates_of(float v) {
     float a = fabsf(v);
-    a = a > 100.f ? 100.f : a;       // NaN stays
-    const float hi = a * -kLog2e, lo = fmaf(a, -1.925963033500012e-08f, fmaf(a, -kLog2e, -hi));
-    float t = __builtin_amdgcn_exp2f(hi);
-    t = fmaf(t * lo, kLn2, t);
-    const float big = __builtin_amdgcn_rcpf(1.f + t), small = t * big;
+    if (EXACT) a = a > 100.f ? 100.f : a;
+    const float t = exp_minus<EXACT>(a), big = __builtin_amdgcn_rcpf(1.f + t), small = t * big;
     return v < 0.f ? Gate{small, big} : Gate{big, small};
 }
-
-// m = 1 - e^L for L <= 0.  Near 0 the difference would cancel (and a long memory is a matter of
-// m, not of a): there m = -L (1 + L/2 + L^2/6 + ...), a polynomial fitted to the definition on
-// [-1/4, 0] by interpolation at Chebyshev points (relative error 3e-9).
-__device__ inline float one_minus_exp(float L) {
-    float q = fmaf(0.007513605989515781f, L, 0.04149065539240837f);
-    q = fmaf(q, L, 0.16665108501911163f);
-    q = fmaf(q, L, 0.4999995231628418f);
-    q = fmaf(q, L, 1.f);
-    const float far = 1.f - __builtin_amdgcn_exp2f(L * kLog2e);
-    return L > -0.25f ? -L * q : far;
+template <bool EXACT> __device__ inline float gate_of(float v) {
+    if constexpr (EXACT) return gates_of<true>(v).s;
+    return __builtin_amdgcn_rcpf(1.f + exp_minus<false>(v));
 }
-__device__ inline float beta_of(float m) { return __builtin_amdgcn_sqrtf(m * (2.f - m)); }
+
+// m = 1 - e^L for L <= 0, from K = L log2(e).  Near 0 the difference would cancel (and a long
+// memory is a matter of m, not of a): there m = -L (1 + L/2 + L^2/6 + ...), a polynomial fitted
+// to the definition on [-1/8, 0] by interpolation at Chebyshev points (relative error 1.6e-8),
+// its coefficients times ln(2)^k for K.
+__device__ inline float one_minus_exp2(float K) {
+    float q = fmaf(0.009151561185717583f, K, 0.05545208230614662f);
+    q = fmaf(q, K, 0.24022464454174042f);
+    q = fmaf(q, K, 0.6931471824645996f);
+    const float far = 1.f - __builtin_amdgcn_exp2f(K);
+    return K > -0.18f ? -K * q : far;
+}
+__device__ inline float beta_of(float m) { return __builtin_amdgcn_sqrtf(fmaf(-m, m, m + m)); }
 
 // ------------------------------------------------------------------ maps h -> P h + H
 // P = -1 marks a map that begins a sequence anew: what comes before it does not matter, whatever
@@ -134,41 +143,87 @@ template <int N> __device__ inline void await(const uint64_t* p, int64_t step, i
     }
 }
 
-// Shared memory of a workgroup.
-struct Joint {
+// Shared memory of a workgroup: maps of the runs of each wave (H then their incoming states).
+template <int RUNS> struct Joint {
+    float P[kWaves][RUNS][kBlock], H[kWaves][RUNS][kBlock];
     Map total[kWaves][kBlock];       // waves' maps
     Map before[kWaves][kBlock];      // of the tiles before, in as many parts
-    float start[kWaves][kBlock];     // state before each wave
     float carry[kBlock];             // state before the tile
     unsigned ticket;
 };
 
-// The maps of the waves are in j.total.  Returns, in j.start of the own wave, the state that
-// reaches it; `first` is what reaches the row's first tile.  `at` is the tile's place in the
-// order of the walk, of `ntile`; lanes are channels here.
-template <bool SEQ>
-__device__ inline void join(const Chain& c, Joint& j, int64_t chain, unsigned at, unsigned ntile, int wave, int waves,
-                            bool forward, float first) {
+// Where a workgroup and a lane work.  LPT lanes with V channels each hold a token's 64 channels;
+// the wave's V lane groups hold a run of tokens each.  The last vector of a row is moved back to
+// end with it: it repeats channels of its neighbour with equal results.  Between the runs' maps a
+// lane stands for one of the 64 places (own).
+struct Tile {
+    int64_t b, c0, own;
+    unsigned at, chain;
+    int wave, group, slot;
+    bool active, here;               // the lane's channels, its place exist
+};
+template <int V> __device__ inline Tile tile_of(const RecurrenceParams& p, unsigned* ticket) {
+    constexpr int LPT = kBlock / V;
+    unsigned t = blockIdx.x;
+    if (p.ntile > 1) {
+        if (threadIdx.x == 0) *ticket = __hip_atomic_fetch_add(p.chain.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        t = __builtin_amdgcn_readfirstlane(*ticket);
+    }
+    const unsigned chains = p.nblk * (unsigned)p.batch, lane = threadIdx.x & 63;
+    Tile q;
+    q.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    q.at = t / chains;
+    q.chain = t % chains;
+    q.b = q.chain / p.nblk;
+    const int64_t first = (int64_t)(q.chain % p.nblk) * kBlock;
+    auto channel = [&](int64_t vec) { return vec + V <= p.D ? vec : p.D - V; };
+    q.group = lane / LPT;
+    q.slot = (lane % LPT) * V;
+    q.active = first + q.slot < p.D;
+    q.c0 = q.active ? channel(first + q.slot) : 0;
+    q.here = first + lane / V * V < p.D;
+    q.own = q.here ? channel(first + lane / V * V) + lane % V : 0;
+    return q;
+}
+
+// Joins the runs whose maps the lanes left in j.P and j.H: puts into j.H the state that reaches
+// each run, in the order of the walk.  `first` is what reaches the row's first tile, `keep` is
+// called with the number of each run of the wave and the state that reaches it (lanes are places).
+template <int RUNS, bool SEQ, bool FORWARD, typename Keep>
+__device__ inline void join(const Chain& c, Joint<RUNS>& j, const Tile& q, unsigned ntile, int waves, float first, Keep keep) {
     const int lane = threadIdx.x & 63;
-    const int w = forward ? wave : waves - 1 - wave;          // place of the wave in the order of the walk
-    auto total = [&](int k) { return j.total[forward ? k : waves - 1 - k][lane]; };
-    __syncthreads();
+    const int w = FORWARD ? q.wave : waves - 1 - q.wave;      // place of the wave in the order of the walk
+    auto run = [&](int k) { return FORWARD ? k : RUNS - 1 - k; };
+    auto total = [&](int k) { return j.total[FORWARD ? k : waves - 1 - k][lane]; };
+    Map m[RUNS], all{1.f, 0.f};
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k) {
+        m[k] = {j.P[q.wave][run(k)][lane], j.H[q.wave][run(k)][lane]};
+        all = then<SEQ>(all, m[k]);
+    }
     float h = first;
+    if (waves > 1) {
+        j.total[q.wave][lane] = all;
+        __syncthreads();
+    }
     if (ntile > 1) {
-        const unsigned group = at / kGroup, from = group * kGroup;
+        const unsigned group = q.at / kGroup, from = group * kGroup;
+        const bool closes = q.at == from + kGroup - 1;        // the group: publishes its state
+        const bool ends = q.at + 1 == ntile;                  // nobody follows
         Map own{1.f, 0.f};
         if (w == 0) {
             for (int k = 0; k < waves; ++k) own = then<SEQ>(own, total(k));
-            // the group's last tile publishes its state; nobody follows the row's last one
-            if (at != from + kGroup - 1 && at + 1 != ntile) publish(c.maps + (chain * ntile + at) * kBlock + lane, own);
+            if (!closes && !ends) publish(c.maps + ((int64_t)q.chain * ntile + q.at) * kBlock + lane, own);
         }
         // the tiles of the group before this one, in `waves` parts
         constexpr int kPart = kGroup / kWaves;
-        const int n = (int)(at - from), per = (n + waves - 1) / waves, lo = w * per, hi = lo + per < n ? lo + per : n;
+        const int n = (int)(q.at - from), per = (n + waves - 1) / waves, lo = w * per, hi = lo + per < n ? lo + per : n;
         Map part{1.f, 0.f};
         for (int k = lo; k < hi; k += kPart) {
             uint64_t word[kPart];
-            await(c.maps + (chain * ntile + from + k) * kBlock + lane, (int64_t)kBlock, hi - k < kPart ? hi - k : kPart, word);
+            await(c.maps + ((int64_t)q.chain * ntile + from + k) * kBlock + lane, (int64_t)kBlock, hi - k < kPart ? hi - k : kPart, word);
 #pragma unroll
             for (int e = 0; e < kPart; ++e)
                 if (k + e < hi) part = then<SEQ>(part, map_of(word[e]));
@@ -177,114 +232,64 @@ __device__ inline void join(const Chain& c, Joint& j, int64_t chain, unsigned at
         const unsigned ngroup = (ntile + kGroup - 1) / kGroup;
         if (w == 0 && group > 0) {
             uint64_t word[1];
-            await(c.states + (chain * ngroup + group - 1) * kBlock + lane, (int64_t)0, 1, word);
+            await(c.states + ((int64_t)q.chain * ngroup + group - 1) * kBlock + lane, (int64_t)0, 1, word);
             h = map_of(word[0]).H;
         }
         __syncthreads();
         if (w == 0) {
             for (int k = 0; k < waves; ++k) h = apply<SEQ>(j.before[k][lane], h);
-            if (at == from + kGroup - 1 && at + 1 != ntile)
-                publish(c.states + (chain * ngroup + group) * kBlock + lane, Map{1.f, apply<SEQ>(own, h)});
+            if (closes && !ends)
+                publish(c.states + ((int64_t)q.chain * ngroup + group) * kBlock + lane, Map{1.f, apply<SEQ>(own, h)});
             j.carry[lane] = h;
         }
         __syncthreads();
         h = j.carry[lane];
     }
     for (int k = 0; k < w; ++k) h = apply<SEQ>(total(k), h);
-    j.start[wave][lane] = h;
-    __builtin_amdgcn_wave_barrier();
-}
-
-// Where a workgroup and a lane work.  LPT lanes with V channels each hold a token's 64 channels;
-// the wave's 64 / LPT lane groups hold a run of R tokens each.  The last vector of a row is moved
-// back to end with it: it repeats channels of its neighbour with equal results.
-struct Tile {
-    int64_t b, c0, chain;
-    unsigned at;
-    int group, slot;
-    bool active;                     // the lane's channels exist
-};
-template <int V> __device__ inline Tile tile_of(const RecurrenceParams& p, Joint& j) {
-    constexpr int LPT = kBlock / V;
-    unsigned t = blockIdx.x;
-    if (p.ntile > 1) {
-        if (threadIdx.x == 0) j.ticket = __hip_atomic_fetch_add(p.chain.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        t = __builtin_amdgcn_readfirstlane(j.ticket);
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k) {
+        keep(run(k), h);
+        j.H[q.wave][run(k)][lane] = h;
+        h = apply<SEQ>(m[k], h);
     }
-    const unsigned chains = p.nblk * (unsigned)p.batch, lane = threadIdx.x & 63;
-    Tile q;
-    q.at = t / chains;
-    q.chain = t % chains;
-    q.b = (unsigned)q.chain / p.nblk;
-    const int64_t first = (int64_t)((unsigned)q.chain % p.nblk) * kBlock;
-    q.group = lane / LPT;
-    q.slot = (lane % LPT) * V;
-    q.active = first + q.slot < p.D;
-    const int64_t c = first + q.slot;
-    q.c0 = c + V <= p.D ? c : (p.D >= V ? p.D - V : 0);
-    return q;
+    __builtin_amdgcn_wave_barrier();
 }
 
 // Sequence of each token of a run, and which tokens begin or end one.
 template <int R> struct Runs {
-    int64_t id[R];
+    int id[R];
     unsigned fresh, last;            // bits
 };
 template <int R> __device__ inline Runs<R> runs_of(const RecurrenceParams& p, int64_t b, int64_t t0) {
     Runs<R> q;
     q.fresh = q.last = 0;
     const int32_t* s = p.seq_idx + b * p.T;
-    int64_t prev = t0 > 0 && t0 <= p.T ? clamp_id(s[t0 - 1], p.nseqs) : -1;
+    auto id = [&](int64_t t) { return t >= 0 && t < p.T ? (int)clamp_id(s[t], p.nseqs) : -1; };
+    int prev = id(t0 - 1);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-        const int64_t t = t0 + k;
-        q.id[k] = t < p.T ? clamp_id(s[t], p.nseqs) : -1;
-        if (t < p.T && q.id[k] != prev) {
-            q.fresh |= 1u << k;
+        q.id[k] = id(t0 + k);
+        if (q.id[k] != prev) {
+            if (q.id[k] >= 0) q.fresh |= 1u << k;
             if (k) q.last |= 1u << (k - 1);
         }
-        if (k && t == p.T) q.last |= 1u << (k - 1);
         prev = q.id[k];
     }
-    const int64_t t = t0 + R - 1;
-    if (t < p.T && (t + 1 == p.T || clamp_id(s[t + 1], p.nseqs) != q.id[R - 1])) q.last |= 1u << (R - 1);
+    if (prev >= 0 && id(t0 + R) != prev) q.last |= 1u << (R - 1);
     return q;
 }
 
-template <int V> __device__ inline void load_or(const float* p, int64_t at, float other, float (&v)[V]) {
-    if (p) {
-        load_f32<V>(p + at, v);
+// A run's R tokens from `row` (flat token) on, of which `rest` exist; the last one stands for
+// those that do not.
+template <int R, int V, typename T, typename Get>
+__device__ inline void load_run(const T* base, int64_t ld, int64_t row, int64_t rest, bool full, Get get) {
+    const T* q = base + row * ld;
+    if (full) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) get(k, q + k * ld);
     } else {
 #pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = other;
-    }
-}
-
-// Maps of the lane groups before (after) the own one in its wave, per channel, and the wave's
-// map into `total`.
-template <int V, bool SEQ, bool FORWARD> __device__ inline void scan_groups(Map (&m)[V], Map (&before)[V], Map* total, int slot, int group) {
-    constexpr int LPT = kBlock / V, N = V;
-    const int place = FORWARD ? group : N - 1 - group;
-#pragma unroll
-    for (int d = 1; d < N; d *= 2) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const Map o = FORWARD ? Map{__shfl_up(m[v].P, d * LPT), __shfl_up(m[v].H, d * LPT)}
-                                  : Map{__shfl_down(m[v].P, d * LPT), __shfl_down(m[v].H, d * LPT)};
-            if (place >= d) m[v] = then<SEQ>(o, m[v]);
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        if constexpr (N > 1) {
-            const Map o = FORWARD ? Map{__shfl_up(m[v].P, LPT), __shfl_up(m[v].H, LPT)}
-                                  : Map{__shfl_down(m[v].P, LPT), __shfl_down(m[v].H, LPT)};
-            before[v] = place ? o : Map{1.f, 0.f};
-        } else {
-            before[v] = Map{1.f, 0.f};
-        }
-        if (place == N - 1) total[slot + v] = m[v];
+        for (int k = 0; k < R; ++k) get(k, q + (k < rest ? k : rest - 1) * ld);
     }
 }
 
@@ -295,88 +300,93 @@ __device__ inline float advance(float h, float m, float u) { return h + fmaf(-m,
 template <typename T, int V, int TOK, bool SEQ, bool GATE, bool STREAM, bool KEEP>
 __global__ __launch_bounds__(64 * kWaves) void recurrence_forward_kernel(RecurrenceParams p) {
     constexpr int R = TOK / V;
-    __shared__ Joint j;
-    const Tile q = tile_of<V>(p, j);
-    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int64_t t0 = ((int64_t)q.at * waves + wave) * TOK + q.group * R;
-    float m[R][V], u[R][V];
+    constexpr bool EXACT = sizeof(T) == 4;
+    __shared__ Joint<V> j;
+    const Tile q = tile_of<V>(p, &j.ticket);
+    const int waves = blockDim.x >> 6;
+    const int64_t w0 = ((int64_t)q.at * waves + q.wave) * TOK, t0 = w0 + q.group * R, rest = p.T - t0;
+    const int64_t row = q.b * p.T + t0;
+    const bool full = w0 + TOK <= p.T;
+    float P[R][V], H[R][V];          // m and u, then the map from the run's start to after each token
     Pack<T, V> z[GATE ? R : 1];
-    Map run[V], before[V];
     Runs<SEQ ? R : 1> s{};
-#pragma unroll
-    for (int v = 0; v < V; ++v) run[v] = {1.f, 0.f};
     if (SEQ) s = runs_of<SEQ ? R : 1>(p, q.b, t0);
+    float end_p[V], end_h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) end_p[v] = 1.f, end_h[v] = 0.f;
     if (q.active) {
         float A[V];
         Pack<T, V> x[R], r[R], g[R];
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const int64_t n = q.b * p.T + (t0 + k < p.T ? t0 + k : p.T - 1);
-            r[k] = load_pack<V>((const T*)p.r + n * p.ldr + q.c0);
-            g[k] = load_pack<V>((const T*)p.i + n * p.ldi + q.c0);
-            x[k] = load_pack<V>((const T*)p.x + n * p.ldx + q.c0);
-            if constexpr (GATE) z[k] = load_pack<V>((const T*)p.z + n * p.ldz + q.c0);
-        }
+        load_run<R, V>((const T*)p.r + q.c0, p.ldr, row, rest, full, [&](int k, const T* a) { r[k] = load_pack<V>(a); });
+        load_run<R, V>((const T*)p.i + q.c0, p.ldi, row, rest, full, [&](int k, const T* a) { g[k] = load_pack<V>(a); });
+        load_run<R, V>((const T*)p.x + q.c0, p.ldx, row, rest, full, [&](int k, const T* a) { x[k] = load_pack<V>(a); });
+        if constexpr (GATE)
+            load_run<R, V>((const T*)p.z + q.c0, p.ldz, row, rest, full, [&](int k, const T* a) { z[k] = load_pack<V>(a); });
         load_f32<V>(p.A_log + q.c0, A);
 #pragma unroll
         for (int v = 0; v < V; ++v) A[v] = rate_of(A[v]);
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const bool real = t0 + k < p.T;
+        for (int k = 0; k < R; ++k)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float mm = one_minus_exp(A[v] * gate_of((float)r[k].v[v]).s);
-                m[k][v] = real ? mm : 0.f;
-                u[k][v] = real ? beta_of(mm) * gate_of((float)g[k].v[v]).s * (float)x[k].v[v] : 0.f;
+                P[k][v] = one_minus_exp2(A[v] * gate_of<EXACT>((float)r[k].v[v]));
+                H[k][v] = beta_of(P[k][v]) * (gate_of<EXACT>((float)g[k].v[v]) * (float)x[k].v[v]);
             }
+        if (!full) {
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (k >= rest) P[k][v] = H[k][v] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
             const bool fresh = SEQ && (s.fresh >> k & 1);
             if (fresh && p.init) {
                 float h[V];
-                load_f32<V>(p.init + s.id[SEQ ? k : 0] * p.D + q.c0, h);
+                load_f32<V>(p.init + (int64_t)s.id[SEQ ? k : 0] * p.D + q.c0, h);
 #pragma unroll
-                for (int v = 0; v < V; ++v) u[k][v] = advance(h[v], m[k][v], u[k][v]);
+                for (int v = 0; v < V; ++v) H[k][v] = advance(h[v], P[k][v], H[k][v]);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                run[v].H = fresh ? u[k][v] : advance(run[v].H, m[k][v], u[k][v]);
-                run[v].P = fresh || (SEQ && run[v].P < 0.f) ? -1.f : fmaf(-m[k][v], run[v].P, run[v].P);
+                const float m = P[k][v];
+                end_h[v] = H[k][v] = fresh ? H[k][v] : advance(end_h[v], m, H[k][v]);
+                end_p[v] = P[k][v] = fresh ? 0.f : fmaf(-m, end_p[v], end_p[v]);
             }
         }
-    }
-    scan_groups<V, SEQ, true>(run, before, j.total[wave], q.slot, q.group);
-    // the row's initial state; a row of packed sequences begins with a fresh token
-    const int64_t c = q.chain % p.nblk * kBlock + (threadIdx.x & 63);
-    const int64_t own = c < p.D ? c : p.D - 1;
-    float first = 0.f;
-    if (!SEQ && p.init) {
-        // channel of the lane's slot: the last vector's slots are moved back with it
-        const int64_t slot = threadIdx.x & 63, vec = c - slot % V;
-        const int64_t at = vec + V <= p.D ? c : (p.D >= V ? p.D - V + slot % V : own);
-        first = p.init[q.b * p.D + (at < p.D ? at : p.D - 1)];
-    }
-    join<SEQ>(p.chain, j, q.chain, q.at, p.ntile, wave, waves, true, first);
-    if (!q.active) return;
-    float h[V];
+        if (SEQ && s.fresh) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = apply<SEQ>(before[v], j.start[wave][q.slot + v]);
+            for (int v = 0; v < V; ++v) end_p[v] = -1.f;
+        }
+    }
+    store_f32<V>(&j.P[q.wave][q.group][q.slot], end_p);
+    store_f32<V>(&j.H[q.wave][q.group][q.slot], end_h);
+    // a row of packed sequences begins with a fresh token, others with their initial state
+    const float first = !SEQ && p.init ? p.init[q.b * p.D + q.own] : 0.f;
+    join<V, SEQ, true>(p.chain, j, q, p.ntile, waves, first, [&](int run, float h) {
+        if constexpr (KEEP) {
+            const int64_t t = w0 + run * R;
+            if (run * R % kRunBack == 0 && t < p.T && q.here) p.kept[(q.b * p.pieces + t / kRunBack) * p.D + q.own] = h;
+        }
+    });
+    if (KEEP || !q.active) return;
+    float h0[V];
+    load_f32<V>(&j.H[q.wave][q.group][q.slot], h0);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-        const int64_t t = t0 + k, n = q.b * p.T + t;
-        if (t >= p.T) break;
-        if constexpr (KEEP) {
-            if (t % kRunBack == 0) store_f32<V>(p.kept + (q.b * ((p.T + kRunBack - 1) / kRunBack) + t / kRunBack) * p.D + q.c0, h);
-        }
+        if (k >= rest) break;
         const bool fresh = SEQ && (s.fresh >> k & 1);
+        float h[V], y[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = fresh ? u[k][v] : advance(h[v], m[k][v], u[k][v]);
-        if constexpr (!KEEP) {
-            float y[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) y[v] = GATE ? h[v] * silu_for<T>((float)z[GATE ? k : 0].v[v]) : h[v];
-            store_f32<V, STREAM>((T*)p.y + n * p.D + q.c0, y);
-            if (p.fin && (SEQ ? (s.last >> k & 1) : t + 1 == p.T))
-                store_f32<V>(p.fin + (SEQ ? s.id[SEQ ? k : 0] : q.b) * p.D + q.c0, h);
+        for (int v = 0; v < V; ++v) {
+            if (fresh) h0[v] = 0.f;                          // P is 0 from here on in the run
+            h[v] = fmaf(P[k][v], h0[v], H[k][v]);
+            y[v] = GATE ? h[v] * silu_for<T>((float)z[GATE ? k : 0].v[v]) : h[v];
         }
+        store_f32<V, STREAM>((T*)p.y + (row + k) * p.D + q.c0, y);
+        if (p.fin && (SEQ ? (s.last >> k & 1) : k + 1 == rest))
+            store_f32<V>(p.fin + (SEQ ? (int64_t)s.id[SEQ ? k : 0] : q.b) * p.D + q.c0, h);
     }
 }
 
@@ -384,159 +394,187 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_forward_kernel(Recurre
 template <typename T, int V, bool SEQ, bool GATE, bool STREAM>
 __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(RecurrenceParams p) {
     constexpr int TOK = kRunBack, R = TOK / V;
-    __shared__ Joint j;
+    constexpr bool EXACT = sizeof(T) == 4;
+    __shared__ Joint<V> j;
     __shared__ float sums[kWaves][kBlock];
-    const Tile q = tile_of<V>(p, j);
-    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const Tile q = tile_of<V>(p, &j.ticket);
+    const int waves = blockDim.x >> 6;
     const unsigned tile = p.ntile - 1 - q.at;
-    const int64_t w0 = ((int64_t)tile * waves + wave) * TOK, t0 = w0 + q.group * R;
-    Pack<T, V> x[R], r[R], g[R];
+    const int64_t piece = (int64_t)tile * waves + q.wave, w0 = piece * TOK, t0 = w0 + q.group * R, rest = p.T - t0;
+    const int64_t row = q.b * p.T + t0;
+    const bool full = w0 + TOK <= p.T;
+    Pack<T, V> x[R], r[R], g[R], z[GATE ? R : 1];
     float m[R][V], hp[R][V], gy[R][V], A[V];
-    Map run[V], before[V];
     Runs<SEQ ? R : 1> s{};
     if (SEQ) s = runs_of<SEQ ? R : 1>(p, q.b, t0);
-    Map none[V];
+    float end_p[V], end_h[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) run[v] = none[v] = {1.f, 0.f};
-    float u[R][V];
+    for (int v = 0; v < V; ++v) end_p[v] = 1.f, end_h[v] = 0.f;
+    // the state before the wave's first token, of the lane's place
+    float h0 = 0.f;
+    if (p.kept) {
+        if (w0 < p.T) h0 = p.kept[(q.b * p.pieces + piece) * p.D + q.own];
+    } else if (!SEQ && p.init) {
+        h0 = p.init[q.b * p.D + q.own];
+    }
+    float P[R][V];                   // map from the run's start to before each token, with hp
     if (q.active) {
+        load_run<R, V>((const T*)p.r + q.c0, p.ldr, row, rest, full, [&](int k, const T* a) { r[k] = load_pack<V>(a); });
+        load_run<R, V>((const T*)p.i + q.c0, p.ldi, row, rest, full, [&](int k, const T* a) { g[k] = load_pack<V>(a); });
+        load_run<R, V>((const T*)p.x + q.c0, p.ldx, row, rest, full, [&](int k, const T* a) { x[k] = load_pack<V>(a); });
+        load_run<R, V>(p.dy + q.c0, p.D, row, rest, full, [&](int k, const float* a) { load_f32<V>(a, gy[k]); });
+        if constexpr (GATE)
+            load_run<R, V>((const T*)p.z + q.c0, p.ldz, row, rest, full, [&](int k, const T* a) { z[k] = load_pack<V>(a); });
         load_f32<V>(p.A_log + q.c0, A);
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const int64_t n = q.b * p.T + (t0 + k < p.T ? t0 + k : p.T - 1);
-            r[k] = load_pack<V>((const T*)p.r + n * p.ldr + q.c0);
-            g[k] = load_pack<V>((const T*)p.i + n * p.ldi + q.c0);
-            x[k] = load_pack<V>((const T*)p.x + n * p.ldx + q.c0);
-            load_f32<V>(p.dy + n * p.D + q.c0, gy[k]);
-        }
-#pragma unroll
         for (int v = 0; v < V; ++v) A[v] = rate_of(A[v]);
-        // forwards through the run, from nothing
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const bool real = t0 + k < p.T, fresh = SEQ && (s.fresh >> k & 1);
+            const bool fresh = SEQ && (s.fresh >> k & 1);
+            if (fresh) {
+                if (p.init) {
+                    load_f32<V>(p.init + (int64_t)s.id[SEQ ? k : 0] * p.D + q.c0, end_h);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) end_h[v] = 0.f;
+                }
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float mm = one_minus_exp(A[v] * gate_of((float)r[k].v[v]).s);
-                m[k][v] = real ? mm : 0.f;
-                u[k][v] = real ? beta_of(mm) * gate_of((float)g[k].v[v]).s * (float)x[k].v[v] : 0.f;
-                hp[k][v] = 0.f;
+                float mm = one_minus_exp2(A[v] * gate_of<EXACT>((float)r[k].v[v]));
+                float u = beta_of(mm) * (gate_of<EXACT>((float)g[k].v[v]) * (float)x[k].v[v]);
+                if (!full && k >= rest) mm = u = gy[k][v] = 0.f;
+                m[k][v] = mm;
+                if (fresh) end_p[v] = 0.f;
+                P[k][v] = end_p[v];
+                hp[k][v] = end_h[v];
+                end_h[v] = advance(end_h[v], mm, u);
+                end_p[v] = fmaf(-mm, end_p[v], end_p[v]);
             }
-            if (fresh && p.init) load_f32<V>(p.init + s.id[SEQ ? k : 0] * p.D + q.c0, hp[k]);
+        }
+        if (SEQ && s.fresh) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                run[v].H = advance(fresh ? hp[k][v] : run[v].H, m[k][v], u[k][v]);
-                run[v].P = fresh || (SEQ && run[v].P < 0.f) ? -1.f : fmaf(-m[k][v], run[v].P, run[v].P);
-            }
+            for (int v = 0; v < V; ++v) end_p[v] = -1.f;
         }
     }
-    scan_groups<V, SEQ, true>(run, before, j.total[wave], q.slot, q.group);
-    Map back[V];
+    store_f32<V>(&j.P[q.wave][q.group][q.slot], end_p);
+    store_f32<V>(&j.H[q.wave][q.group][q.slot], end_h);
+    __builtin_amdgcn_wave_barrier();
+    {
+        const int lane = threadIdx.x & 63;
+        Map run[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) back[v] = {1.f, 0.f};
+        for (int k = 0; k < V; ++k) run[k] = {j.P[q.wave][k][lane], j.H[q.wave][k][lane]};
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            j.H[q.wave][k][lane] = h0;
+            h0 = apply<SEQ>(run[k], h0);
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int v = 0; v < V; ++v) end_p[v] = 1.f;
     if (q.active) {
         float h[V];
-        const int64_t n = (p.T + kRunBack - 1) / kRunBack, piece = w0 / kRunBack < n ? w0 / kRunBack : n - 1;
-        if (p.kept) load_f32<V>(p.kept + (q.b * n + piece) * p.D + q.c0, h);
-        else load_or<V>(SEQ ? nullptr : p.init, q.b * p.D + q.c0, 0.f, h);
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = apply<SEQ>(before[v], h[v]);
+        load_f32<V>(&j.H[q.wave][q.group][q.slot], h);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const bool real = t0 + k < p.T, fresh = SEQ && (s.fresh >> k & 1);
-            const bool last = SEQ ? (s.last >> k & 1) : t0 + k + 1 == p.T;
-            const int64_t at = q.b * p.T + (real ? t0 + k : p.T - 1);
+            const bool fresh = SEQ && (s.fresh >> k & 1);
+            const bool last = SEQ ? (s.last >> k & 1) : k + 1 == rest;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (!fresh) hp[k][v] = h[v];
-                h[v] = advance(hp[k][v], m[k][v], u[k][v]);
-                if (!real) gy[k][v] = 0.f;
+                if (fresh) h[v] = 0.f;                       // P is 0 from here on in the run
+                hp[k][v] = fmaf(P[k][v], h[v], hp[k][v]);
             }
             if constexpr (GATE) {
-                float z[V], dz[V];
-                load_f32<V>((const T*)p.z + at * p.ldz + q.c0, z);
+                float dz[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float sz = gate_of(z[v]).s;
-                    dz[v] = gy[k][v] * h[v] * silu_slope(z[v], sz);
-                    gy[k][v] *= z[v] * sz;
+                    const float zv = (float)z[k].v[v], sz = gate_of<EXACT>(zv);
+                    const float u = beta_of(m[k][v]) * (gate_of<EXACT>((float)g[k].v[v]) * (float)x[k].v[v]);
+                    dz[v] = gy[k][v] * advance(hp[k][v], m[k][v], u) * silu_slope(zv, sz);
+                    gy[k][v] *= zv * sz;
                 }
-                if (real) store_f32<V, STREAM>(p.dz + at * p.D + q.c0, dz);
+                if (k < rest) store_f32<V, STREAM>(p.dz + (row + k) * p.D + q.c0, dz);
             }
             if (last && p.dfin) {
                 float d[V];
-                load_f32<V>(p.dfin + (SEQ ? s.id[SEQ ? k : 0] : q.b) * p.D + q.c0, d);
+                load_f32<V>(p.dfin + (SEQ ? (int64_t)s.id[SEQ ? k : 0] : q.b) * p.D + q.c0, d);
 #pragma unroll
                 for (int v = 0; v < V; ++v) gy[k][v] += d[v];
             }
         }
-        // backwards through the run, from nothing
+    }
+    // backwards through the run, from nothing
+#pragma unroll
+    for (int v = 0; v < V; ++v) end_h[v] = 0.f;
+    if (q.active) {
 #pragma unroll
         for (int k = R - 1; k >= 0; --k) {
             const bool fresh = SEQ && (s.fresh >> k & 1);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float e = gy[k][v] + back[v].H;
-                back[v].H = fresh ? 0.f : fmaf(-m[k][v], e, e);
-                back[v].P = fresh || (SEQ && back[v].P < 0.f) ? -1.f : fmaf(-m[k][v], back[v].P, back[v].P);
+                const float e = gy[k][v] + end_h[v];
+                end_h[v] = fresh ? 0.f : fmaf(-m[k][v], e, e);
+                end_p[v] = fmaf(-m[k][v], end_p[v], end_p[v]);
             }
         }
+        if (SEQ && s.fresh) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) end_p[v] = -1.f;
+        }
     }
-    __syncthreads();
-    scan_groups<V, SEQ, false>(back, before, j.total[wave], q.slot, q.group);
-    join<SEQ>(p.chain, j, q.chain, q.at, p.ntile, wave, waves, false, 0.f);
+    store_f32<V>(&j.P[q.wave][q.group][q.slot], end_p);
+    store_f32<V>(&j.H[q.wave][q.group][q.slot], end_h);
+    join<V, SEQ, false>(p.chain, j, q, p.ntile, waves, 0.f, [](int, float) {});
     float dA[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) dA[v] = 0.f;
     if (q.active) {
         float e[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) e[v] = apply<SEQ>(before[v], j.start[wave][q.slot + v]);
+        load_f32<V>(&j.H[q.wave][q.group][q.slot], e);
 #pragma unroll
         for (int k = R - 1; k >= 0; --k) {
-            const int64_t t = t0 + k, n = q.b * p.T + t;
-            if (t >= p.T) continue;
+            if (k >= rest) continue;
             float dx[V], dr[V], di[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float d = gy[k][v] + e[v], mm = m[k][v], a = 1.f - mm;
-                const Gate sr = gate_of((float)r[k].v[v]), si = gate_of((float)g[k].v[v]);
-                const float L = A[v] * sr.s, beta = beta_of(mm), in = si.s * (float)x[k].v[v];
+                const Gate sr = gates_of<EXACT>((float)r[k].v[v]), si = gates_of<EXACT>((float)g[k].v[v]);
+                const float L = A[v] * sr.s * kLn2, beta = beta_of(mm), in = si.s * (float)x[k].v[v];
                 const float ratio = beta > 0.f ? L * __builtin_amdgcn_rcpf(beta) : 0.f;
-                const float M = d * fmaf(L * a, hp[k][v], -in * a * a * ratio);
+                const float M = d * (a * fmaf(L, hp[k][v], -in * a * ratio));
                 dx[v] = d * beta * si.s;
                 di[v] = d * beta * in * si.n;
                 dr[v] = M * sr.n;
                 dA[v] += M;
                 e[v] = fmaf(-mm, d, d);
             }
-            store_f32<V, STREAM>(p.dx + n * p.D + q.c0, dx);
-            store_f32<V, STREAM>(p.dr + n * p.D + q.c0, dr);
-            store_f32<V, STREAM>(p.di + n * p.D + q.c0, di);
-            const bool fresh = SEQ ? (s.fresh >> k & 1) : t == 0;
+            store_f32<V, STREAM>(p.dx + (row + k) * p.D + q.c0, dx);
+            store_f32<V, STREAM>(p.dr + (row + k) * p.D + q.c0, dr);
+            store_f32<V, STREAM>(p.di + (row + k) * p.D + q.c0, di);
+            const bool fresh = SEQ ? (s.fresh >> k & 1) : t0 + k == 0;
             if (fresh) {
-                if (p.dinit) store_f32<V>(p.dinit + (SEQ ? s.id[SEQ ? k : 0] : q.b) * p.D + q.c0, e);
+                if (p.dinit) store_f32<V>(p.dinit + (SEQ ? (int64_t)s.id[SEQ ? k : 0] : q.b) * p.D + q.c0, e);
 #pragma unroll
                 for (int v = 0; v < V; ++v) e[v] = 0.f;
             }
         }
     }
-    // sums over the lane groups, then over the waves
-    constexpr int LPT = kBlock / V;
+    // sums over the runs of each wave, then over the waves
+    store_f32<V>(&j.P[q.wave][q.group][q.slot], dA);
+    __builtin_amdgcn_wave_barrier();
+    const int lane = threadIdx.x & 63;
+    float sum = 0.f;
 #pragma unroll
-    for (int d = LPT; d < 64; d *= 2)
-#pragma unroll
-        for (int v = 0; v < V; ++v) dA[v] += __shfl_xor(dA[v], d);
-    if (q.group == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) sums[wave][q.slot + v] = dA[v];
+    for (int k = 0; k < V; ++k) sum += j.P[q.wave][k][lane];
+    if (waves > 1) {
+        sums[q.wave][lane] = sum;
+        __syncthreads();
     }
-    __syncthreads();
-    if (wave == 0 && q.group == 0 && q.active) {
-        for (int w = 1; w < waves; ++w)
-#pragma unroll
-            for (int v = 0; v < V; ++v) dA[v] += sums[w][q.slot + v];
-        store_f32<V>(p.part + (q.b * p.ntile + tile) * p.D + q.c0, dA);
+    if (q.wave == 0 && q.here) {
+        for (int w = 1; w < waves; ++w) sum += sums[w][lane];
+        p.part[(q.b * p.ntile + tile) * p.D + q.own] = sum;
     }
 }
 
@@ -545,8 +583,9 @@ template <typename T> __global__ __launch_bounds__(256) void recurrence_step_ker
     const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (n >= p.batch * p.D) return;
     const int64_t b = n / p.D, c = n % p.D;
-    const float m = one_minus_exp(rate_of(p.A_log[c]) * gate_of((float)((const T*)p.r)[b * p.ldr + c]).s);
-    const float u = beta_of(m) * gate_of((float)((const T*)p.i)[b * p.ldi + c]).s * (float)((const T*)p.x)[b * p.ldx + c];
+    constexpr bool EXACT = sizeof(T) == 4;
+    const float m = one_minus_exp2(rate_of(p.A_log[c]) * gate_of<EXACT>((float)((const T*)p.r)[b * p.ldr + c]));
+    const float u = beta_of(m) * (gate_of<EXACT>((float)((const T*)p.i)[b * p.ldi + c]) * (float)((const T*)p.x)[b * p.ldx + c]);
     const float h = advance(p.init[n], m, u);
     p.fin[n] = h;
     ((T*)p.y)[n] = (T)(p.z ? h * silu_for<T>((float)((const T*)p.z)[b * p.ldz + c]) : h);
@@ -711,6 +750,7 @@ ssd::RecurrenceParams params_of(const ssd_recurrence_problem_t* p, const void* x
     c.ldr = p->ldr;
     c.ldi = p->ldi;
     c.ldz = p->ldz;
+    c.pieces = pieces_of(p);
     return c;
 }
 

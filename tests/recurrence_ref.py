@@ -10,6 +10,11 @@ across a cut, so with H the same recurrence over magnitudes
 and each level of a tree of cuts adds roundings of H_t itself, below 20 in all.  Backwards the
 same holds for the gradient that reaches a state, over dy.
 
+A gate of bf16 activations takes e^-v with the exponent v log2(e) rounded to fp32, which moves it
+by |v| roundings (half a step of a number near v is at most |v| 2^-24): N_M and the gates' own
+factors have |r| and |i| more there, beta half of |r| (|v| beyond 100 is as 100: the sigmoid is
+below FLUSH or 1 there).
+
 Underflow: a sigmoid below FLUSH = 2^-126, fp32's smallest normal number, may count as 0.  That
 moves silu(z) by FLUSH |z|, sigmoid(i) x by FLUSH |x|, and, beta being sqrt(2 |A| sigmoid(r))
 there, beta and |L| / beta by at most sqrt(2 |A| FLUSH), 1.5e-19 sqrt |A|: terms of that size times
@@ -43,47 +48,52 @@ def parts(x, r, i, A_log):
     return L, torch.exp(L), -torch.expm1(L), beta, beta * torch.sigmoid(i) * x
 
 
+def argument(v, bf16):
+    return v.abs().clamp(max=100) if bf16 else torch.zeros_like(v)
+
+
 def lost_beta(A_log):
     return torch.sqrt(2 * FLUSH * torch.exp(A_log))
 
 
-def forward(x, r, i, A_log, z, init, lens):
+def forward(x, r, i, A_log, z, init, lens, bf16=False):
     """(y, final, bound of y, bound of final, states, their magnitudes, their errors), 64 bits."""
     b, T, D = x.shape
     L, a, m, beta, u = parts(x, r, i, A_log)
+    n_m, n_u = N_M + argument(r, bf16), N_U + argument(r, bf16) / 2 + argument(i, bf16)
     lost = FLUSH * x.abs() + lost_beta(A_log) * (torch.sigmoid(i) * x).abs()
     hs, Hs, Es = (torch.zeros(b, T, D, dtype=torch.double) for _ in range(3))
     final, fin_e = [], []
     for k, (row, t0, n) in enumerate(ref.sequences(b, T, lens)):
         h, H, E = init[k], init[k].abs(), torch.zeros(D, dtype=torch.double)
         for t in range(t0, t0 + n):
-            E = a[row, t] * E + U32 * N_M * m[row, t] * H
+            E = a[row, t] * E + U32 * n_m[row, t] * m[row, t] * H
             h, H = a[row, t] * h + u[row, t], a[row, t] * H + u[row, t].abs()
-            E = E + U32 * (4 * H + N_U * u[row, t].abs()) + lost[row, t]
+            E = E + U32 * (4 * H + n_u[row, t] * u[row, t].abs()) + lost[row, t]
             hs[row, t], Hs[row, t], Es[row, t] = h, H, E
         final.append(h)
         fin_e.append(E + N_TREE * U32 * H)
     Es = Es + N_TREE * U32 * Hs
     gate = torch.ones_like(x) if z is None else ref.silu(z)
-    # silu's argument error does not grow with |z|: 12 roundings with the product
-    bound = Es * gate.abs() + (0 if z is None else 12 * U32 * (hs * gate).abs() + FLUSH * (hs * z).abs())
+    bound = Es * gate.abs() + (0 if z is None else U32 * (12 + argument(z, bf16)) * (hs * gate).abs() + FLUSH * (hs * z).abs())
     return hs * gate, torch.stack(final), bound, torch.stack(fin_e), hs, Hs, Es
 
 
-def backward(x, r, i, A_log, dy, z, init, dfinal, lens):
+def backward(x, r, i, A_log, dy, z, init, dfinal, lens, bf16=False):
     """{name: (gradient, bound)}, 64 bits, from the formulas."""
     b, T, D = x.shape
-    _, _, _, _, hs, Hs, Es = forward(x, r, i, A_log, z, init, lens)
+    _, _, _, _, hs, Hs, Es = forward(x, r, i, A_log, z, init, lens, bf16)
+    nr, ni = argument(r, bf16), argument(i, bf16)
     L, a, m, beta, _ = parts(x, r, i, A_log)
     si, s = torch.sigmoid(i), torch.sigmoid(r)
     v = si * x
     out = {}
-    gy, gn, gl = dy, 1, torch.zeros_like(dy)
+    gy, gn, gl = dy, torch.ones_like(dy), torch.zeros_like(dy)
     if z is not None:
         sz = torch.sigmoid(z)
         slope, wide = sz * (1 + z * (1 - sz)), sz * (1 + z.abs() * (1 - sz))
-        out["dz"] = (dy * hs * slope, dy.abs() * (Es * slope.abs() + hs.abs() * (20 * U32 * wide + FLUSH * (1 + z.abs()))))
-        gy, gn, gl = dy * z * sz, 12, FLUSH * (dy * z).abs()
+        out["dz"] = (dy * hs * slope, dy.abs() * (Es * slope.abs() + hs.abs() * (U32 * (20 + argument(z, bf16)) * wide + FLUSH * (1 + z.abs()))))
+        gy, gn, gl = dy * z * sz, 12 + argument(z, bf16), FLUSH * (dy * z).abs()
     g, G, EG = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(x)
     before, Hb, Eb = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(x)
     dinit, dinit_e = torch.zeros_like(init), torch.zeros_like(init)
@@ -95,9 +105,9 @@ def backward(x, r, i, A_log, dy, z, init, dfinal, lens):
         for t in range(t0 + n - 1, t0 - 1, -1):
             own = gy[row, t]
             g[row, t], G[row, t] = own + q, own.abs() + Q
-            EG[row, t] = E + U32 * ((gn + 4) * own.abs() + 4 * Q) + gl[row, t]
+            EG[row, t] = E + U32 * ((gn[row, t] + 4) * own.abs() + 4 * Q) + gl[row, t]
             q, Q = a[row, t] * g[row, t], a[row, t] * G[row, t]
-            E = a[row, t] * EG[row, t] + U32 * (N_M * m[row, t] + 2) * G[row, t]
+            E = a[row, t] * EG[row, t] + U32 * ((N_M + nr[row, t]) * m[row, t] + 2) * G[row, t]
             first = t == t0
             before[row, t] = init[k] if first else hs[row, t - 1]
             Hb[row, t] = init[k].abs() if first else Hs[row, t - 1]
@@ -106,15 +116,15 @@ def backward(x, r, i, A_log, dy, z, init, dfinal, lens):
     EG = EG + N_TREE * U32 * G
     ratio = torch.where(beta > 0, L / beta, torch.zeros_like(L))
     lost = lost_beta(A_log)
-    out["dx"] = (g * beta * si, (EG + 40 * U32 * G) * beta * si + G * (lost * si + FLUSH))
+    out["dx"] = (g * beta * si, (EG + U32 * (40 + nr / 2 + ni) * G) * beta * si + G * (lost * si + FLUSH))
     out["di"] = (g * beta * v * (1 - si),
-                 (EG + 50 * U32 * G) * (beta * v * (1 - si)).abs() + G * ((lost * v * (1 - si)).abs() + 2 * FLUSH * x.abs()))
+                 (EG + U32 * (50 + nr / 2 + 2 * ni) * G) * (beta * v * (1 - si)).abs() + G * ((lost * v * (1 - si)).abs() + 2 * FLUSH * x.abs()))
     M = g * (L * a * before - v * a * a * ratio)
-    ea = U32 * (N_M * m + 2)                                            # of a
+    ea = U32 * ((N_M + nr) * m + 2)                                            # of a
     size = L.abs() * a * Hb + v.abs() * a * a * ratio.abs()
-    M_e = EG * size + G * (40 * U32 * size + L.abs() * (a * Eb + ea * Hb) + v.abs() * ratio.abs() * 2 * a * ea)
+    M_e = EG * size + G * (U32 * (40 + 2 * nr + ni) * size + L.abs() * (a * Eb + ea * Hb) + v.abs() * ratio.abs() * 2 * a * ea)
     M_e = M_e + G * (lost * v.abs() + FLUSH * (torch.exp(A_log) * Hb + x.abs()))
-    out["dr"] = (M * (1 - s), (M_e + 12 * U32 * M.abs()) * (1 - s) + FLUSH * M.abs())
+    out["dr"] = (M * (1 - s), (M_e + U32 * (12 + nr) * M.abs()) * (1 - s) + FLUSH * M.abs())
     out["dA_log"] = (M.sum((0, 1)), M_e.sum((0, 1)) + (b * T + 20) * U32 * M.abs().sum((0, 1)))
     out["dinit"] = (dinit, dinit_e)
     return out

@@ -54,7 +54,7 @@ def check_forward(ssd, q, got=None):
     y, f = forward(ssd, q) if got is None else got
     assert y.dtype == q["x"].dtype and f.dtype == torch.float32
     w = wide(q)
-    want, final, ey, ef = rr.forward(w["x"], w["r"], w["i"], w["A_log"], w["z"], w["init"], q["lens"])[:4]
+    want, final, ey, ef = rr.forward(w["x"], w["r"], w["i"], w["A_log"], w["z"], w["init"], q["lens"], q["x"].dtype == torch.bfloat16)[:4]
     rr.check(y, want, ey, "y")
     rr.check(f, final, ef, "final")
 
@@ -62,7 +62,8 @@ def check_forward(ssd, q, got=None):
 def check_backward(ssd, q, got=None):
     got = backward(ssd, q) if got is None else got
     w = wide(q)
-    want = rr.backward(w["x"], w["r"], w["i"], w["A_log"], w["dy"], w["z"], w["init"], w["dfinal"], q["lens"])
+    want = rr.backward(w["x"], w["r"], w["i"], w["A_log"], w["dy"], w["z"], w["init"], w["dfinal"], q["lens"],
+                       q["x"].dtype == torch.bfloat16)
     assert set(got) == set(want)
     for k in want:
         assert got[k].dtype == torch.float32
