@@ -16,9 +16,10 @@
 // instead, so that a tile reads 15 maps and one state at most and the waiting grows with a
 // sixteenth of the tiles.  Maps are always composed in the same order, whoever comes first:
 // results are deterministic.  A map of a channel is one 64-bit word that is its own flag (the
-// words are zeroed by a launch before), so nothing has to be fenced.  Tiles are handed out by a
-// counter, all rows' first tiles before their second: a tile waits only for tiles that
-// workgroups already running have taken, so every wait ends (and it is bounded besides).
+// words are zeroed by a launch before), so nothing has to be fenced.  The tiles of a chain (a row's
+// 64 channels) are handed out by its counter: a tile waits only for tiles that workgroups already
+// running have taken, so every wait ends (and it is bounded besides).  One counter for all chains
+// held the card up: 5120 workgroups took 94 us, 10240 of half the size 141.
 #include "ssd.h"
 
 #include <algorithm>
@@ -34,10 +35,12 @@ constexpr int kWaves = 4;            // waves of a workgroup, at most
 constexpr int kGroup = 16;           // tiles from one published state to the next
 constexpr int kRunBack = 16;         // tokens of a wave backward, and between states kept for it
 
+constexpr int kCounter = 32;         // words between two chains' counters: a line each
+
 // What the tiles of one direction publish: words (chains, tiles, 64) and (chains, groups, 64).
 struct Chain {
     uint64_t *maps, *states;
-    unsigned* counter;
+    unsigned* counters;              // a chain's next tile, kCounter apart
 };
 
 struct RecurrenceParams {
@@ -158,23 +161,17 @@ template <int RUNS> struct Joint {
 // lane stands for one of the 64 places (own).
 struct Tile {
     int64_t b, c0, own;
-    unsigned at, chain;
+    unsigned at, chain;              // the tile's place in the order of the walk
     int wave, group, slot;
     bool active, here;               // the lane's channels, its place exist
 };
-template <int V> __device__ inline Tile tile_of(const RecurrenceParams& p, unsigned* ticket) {
+template <int V> __device__ inline Tile tile_of(const RecurrenceParams& p) {
     constexpr int LPT = kBlock / V;
-    unsigned t = blockIdx.x;
-    if (p.ntile > 1) {
-        if (threadIdx.x == 0) *ticket = __hip_atomic_fetch_add(p.chain.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        t = __builtin_amdgcn_readfirstlane(*ticket);
-    }
     const unsigned chains = p.nblk * (unsigned)p.batch, lane = threadIdx.x & 63;
     Tile q;
+    q.chain = blockIdx.x % chains;
+    q.at = 0;
     q.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    q.at = t / chains;
-    q.chain = t % chains;
     q.b = q.chain / p.nblk;
     const int64_t first = (int64_t)(q.chain % p.nblk) * kBlock;
     auto channel = [&](int64_t vec) { return vec + V <= p.D ? vec : p.D - V; };
@@ -185,6 +182,15 @@ template <int V> __device__ inline Tile tile_of(const RecurrenceParams& p, unsig
     q.here = first + lane / V * V < p.D;
     q.own = q.here ? channel(first + lane / V * V) + lane % V : 0;
     return q;
+}
+
+// The workgroup's tile of its chain, from the chain's counter.
+__device__ inline void take_tile(const RecurrenceParams& p, Tile& q, unsigned* ticket) {
+    if (p.ntile == 1) return;
+    if (threadIdx.x == 0)
+        *ticket = __hip_atomic_fetch_add(p.chain.counters + (int64_t)q.chain * kCounter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    q.at = __builtin_amdgcn_readfirstlane(*ticket);
 }
 
 // Joins the runs whose maps the lanes left in j.P and j.H: puts into j.H the state that reaches
@@ -255,42 +261,49 @@ __device__ inline void join(const Chain& c, Joint<RUNS>& j, const Tile& q, unsig
     __builtin_amdgcn_wave_barrier();
 }
 
-// Sequence of each token of a run, and which tokens begin or end one.
+// Sequence of each token of a run, and which tokens begin or end one; from the ids of the run and
+// its neighbours.
+template <int R> struct Ids {
+    int v[R + 2];
+};
+template <int R> __device__ inline Ids<R> load_ids(const RecurrenceParams& p, int64_t b, int64_t t0) {
+    Ids<R> q;
+#pragma unroll
+    for (int k = 0; k < R + 2; ++k) {
+        const int64_t t = t0 + k - 1;
+        q.v[k] = p.seq_idx[b * p.T + (t < 0 ? 0 : (t < p.T ? t : p.T - 1))];
+    }
+    return q;
+}
 template <int R> struct Runs {
     int id[R];
     unsigned fresh, last;            // bits
 };
-template <int R> __device__ inline Runs<R> runs_of(const RecurrenceParams& p, int64_t b, int64_t t0) {
+template <int R> __device__ inline Runs<R> runs_of(const RecurrenceParams& p, const Ids<R>& ids, int64_t t0) {
     Runs<R> q;
     q.fresh = q.last = 0;
-    const int32_t* s = p.seq_idx + b * p.T;
-    auto id = [&](int64_t t) { return t >= 0 && t < p.T ? (int)clamp_id(s[t], p.nseqs) : -1; };
-    int prev = id(t0 - 1);
+    auto id = [&](int k) {
+        const int64_t t = t0 + k - 1;
+        return t >= 0 && t < p.T ? (int)clamp_id(ids.v[k], p.nseqs) : -1;
+    };
+    int prev = id(0);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-        q.id[k] = id(t0 + k);
+        q.id[k] = id(k + 1);
         if (q.id[k] != prev) {
             if (q.id[k] >= 0) q.fresh |= 1u << k;
             if (k) q.last |= 1u << (k - 1);
         }
         prev = q.id[k];
     }
-    if (prev >= 0 && id(t0 + R) != prev) q.last |= 1u << (R - 1);
+    if (prev >= 0 && id(R + 1) != prev) q.last |= 1u << (R - 1);
     return q;
 }
 
-// A run's R tokens from `row` (flat token) on, of which `rest` exist; the last one stands for
-// those that do not.
-template <int R, int V, typename T, typename Get>
-__device__ inline void load_run(const T* base, int64_t ld, int64_t row, int64_t rest, bool full, Get get) {
-    const T* q = base + row * ld;
-    if (full) {
-#pragma unroll
-        for (int k = 0; k < R; ++k) get(k, q + k * ld);
-    } else {
-#pragma unroll
-        for (int k = 0; k < R; ++k) get(k, q + (k < rest ? k : rest - 1) * ld);
-    }
+// Where a run's R tokens from flat token `row` on lie, of which `rest` exist; the last one stands
+// for those that do not.
+template <typename T> __device__ inline const T* token_at(const void* base, int64_t ld, int64_t row, int64_t rest, bool full, int k) {
+    return (const T*)base + (row + (full || k < rest ? k : rest - 1)) * ld;
 }
 
 // A step of the state.
@@ -298,67 +311,70 @@ __device__ inline float advance(float h, float m, float u) { return h + fmaf(-m,
 
 // Whole rows.  TOK tokens per wave; KEEP: no output, but the state before every kRunBack-th token.
 template <typename T, int V, int TOK, bool SEQ, bool GATE, bool STREAM, bool KEEP>
-__global__ __launch_bounds__(64 * kWaves) void recurrence_forward_kernel(RecurrenceParams p) {
-    constexpr int R = TOK / V;
+__global__ __launch_bounds__(64 * kWaves, GATE || sizeof(T) == 4 ? 1 : 4) void recurrence_forward_kernel(RecurrenceParams p) {
+    constexpr int R = TOK / V, RS = SEQ ? R : 1;
     constexpr bool EXACT = sizeof(T) == 4;
     __shared__ Joint<V> j;
-    const Tile q = tile_of<V>(p, &j.ticket);
+    Tile q = tile_of<V>(p);
+    take_tile(p, q, &j.ticket);
     const int waves = blockDim.x >> 6;
-    const int64_t w0 = ((int64_t)q.at * waves + q.wave) * TOK, t0 = w0 + q.group * R, rest = p.T - t0;
-    const int64_t row = q.b * p.T + t0;
+    const int64_t w0 = ((int64_t)q.at * waves + q.wave) * TOK, t0 = w0 + q.group * R, rest = p.T - t0, row = q.b * p.T + t0;
     const bool full = w0 + TOK <= p.T;
-    float P[R][V], H[R][V];          // m and u, then the map from the run's start to after each token
-    Pack<T, V> z[GATE ? R : 1];
-    Runs<SEQ ? R : 1> s{};
-    if (SEQ) s = runs_of<SEQ ? R : 1>(p, q.b, t0);
-    float end_p[V], end_h[V];
+    float P[R][V], H[R][V];          // map from the run's start to after each token
+    Pack<T, V> x[R], r[R], g[R], z[GATE ? R : 1];
+    float A[V], end_p[V], end_h[V];
+    Runs<RS> s{};
+    load_f32<V>(p.A_log + q.c0, A);
 #pragma unroll
-    for (int v = 0; v < V; ++v) end_p[v] = 1.f, end_h[v] = 0.f;
-    if (q.active) {
-        float A[V];
-        Pack<T, V> x[R], r[R], g[R];
-        load_run<R, V>((const T*)p.r + q.c0, p.ldr, row, rest, full, [&](int k, const T* a) { r[k] = load_pack<V>(a); });
-        load_run<R, V>((const T*)p.i + q.c0, p.ldi, row, rest, full, [&](int k, const T* a) { g[k] = load_pack<V>(a); });
-        load_run<R, V>((const T*)p.x + q.c0, p.ldx, row, rest, full, [&](int k, const T* a) { x[k] = load_pack<V>(a); });
-        if constexpr (GATE)
-            load_run<R, V>((const T*)p.z + q.c0, p.ldz, row, rest, full, [&](int k, const T* a) { z[k] = load_pack<V>(a); });
-        load_f32<V>(p.A_log + q.c0, A);
+    for (int k = 0; k < R; ++k) {
+        r[k] = load_pack<V>(token_at<T>(p.r, p.ldr, row, rest, full, k) + q.c0);
+        g[k] = load_pack<V>(token_at<T>(p.i, p.ldi, row, rest, full, k) + q.c0);
+        x[k] = load_pack<V>(token_at<T>(p.x, p.ldx, row, rest, full, k) + q.c0);
+    }
+    if (SEQ) s = runs_of<RS>(p, load_ids<RS>(p, q.b, t0), t0);
 #pragma unroll
-        for (int v = 0; v < V; ++v) A[v] = rate_of(A[v]);
+    for (int v = 0; v < V; ++v) {
+        A[v] = rate_of(A[v]);
+        end_p[v] = 1.f;
+        end_h[v] = 0.f;
+    }
 #pragma unroll
-        for (int k = 0; k < R; ++k)
+    for (int k = 0; k < R; ++k) {
+        float m[V], u[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                P[k][v] = one_minus_exp2(A[v] * gate_of<EXACT>((float)r[k].v[v]));
-                H[k][v] = beta_of(P[k][v]) * (gate_of<EXACT>((float)g[k].v[v]) * (float)x[k].v[v]);
-            }
+        for (int v = 0; v < V; ++v) {
+            m[v] = one_minus_exp2(A[v] * gate_of<EXACT>((float)r[k].v[v]));
+            u[v] = beta_of(m[v]) * (gate_of<EXACT>((float)g[k].v[v]) * (float)x[k].v[v]);
+        }
         if (!full) {
 #pragma unroll
-            for (int k = 0; k < R; ++k)
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (k >= rest) P[k][v] = H[k][v] = 0.f;
+            for (int v = 0; v < V; ++v)
+                if (k >= rest) m[v] = u[v] = 0.f;
         }
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const bool fresh = SEQ && (s.fresh >> k & 1);
-            if (fresh && p.init) {
-                float h[V];
-                load_f32<V>(p.init + (int64_t)s.id[SEQ ? k : 0] * p.D + q.c0, h);
-#pragma unroll
-                for (int v = 0; v < V; ++v) H[k][v] = advance(h[v], P[k][v], H[k][v]);
-            }
+        const bool fresh = SEQ && (s.fresh >> k & 1);
+        if (SEQ && fresh) {
+            float h[V];
+            if (p.init) load_f32<V>(p.init + (int64_t)s.id[SEQ ? k : 0] * p.D + q.c0, h);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float m = P[k][v];
-                end_h[v] = H[k][v] = fresh ? H[k][v] : advance(end_h[v], m, H[k][v]);
-                end_p[v] = P[k][v] = fresh ? 0.f : fmaf(-m, end_p[v], end_p[v]);
+                end_h[v] = p.init ? h[v] : 0.f;
+                end_p[v] = 0.f;
             }
         }
-        if (SEQ && s.fresh) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) end_p[v] = -1.f;
+        for (int v = 0; v < V; ++v) {
+            end_h[v] = H[k][v] = advance(end_h[v], m[v], u[v]);
+            end_p[v] = P[k][v] = fmaf(-m[v], end_p[v], end_p[v]);
         }
+        __builtin_amdgcn_sched_barrier(0);       // token by token: the inputs' registers become free
+    }
+    if (SEQ && s.fresh) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) end_p[v] = -1.f;
+    }
+    if constexpr (GATE) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) z[k] = load_pack<V>(token_at<T>(p.z, p.ldz, row, rest, full, k) + q.c0);
     }
     store_f32<V>(&j.P[q.wave][q.group][q.slot], end_p);
     store_f32<V>(&j.H[q.wave][q.group][q.slot], end_h);
@@ -397,7 +413,8 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
     constexpr bool EXACT = sizeof(T) == 4;
     __shared__ Joint<V> j;
     __shared__ float sums[kWaves][kBlock];
-    const Tile q = tile_of<V>(p, &j.ticket);
+    Tile q = tile_of<V>(p);
+    take_tile(p, q, &j.ticket);
     const int waves = blockDim.x >> 6;
     const unsigned tile = p.ntile - 1 - q.at;
     const int64_t piece = (int64_t)tile * waves + q.wave, w0 = piece * TOK, t0 = w0 + q.group * R, rest = p.T - t0;
@@ -406,7 +423,7 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
     Pack<T, V> x[R], r[R], g[R], z[GATE ? R : 1];
     float m[R][V], hp[R][V], gy[R][V], A[V];
     Runs<SEQ ? R : 1> s{};
-    if (SEQ) s = runs_of<SEQ ? R : 1>(p, q.b, t0);
+    if (SEQ) s = runs_of<SEQ ? R : 1>(p, load_ids<SEQ ? R : 1>(p, q.b, t0), t0);
     float end_p[V], end_h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) end_p[v] = 1.f, end_h[v] = 0.f;
@@ -419,12 +436,17 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
     }
     float P[R][V];                   // map from the run's start to before each token, with hp
     if (q.active) {
-        load_run<R, V>((const T*)p.r + q.c0, p.ldr, row, rest, full, [&](int k, const T* a) { r[k] = load_pack<V>(a); });
-        load_run<R, V>((const T*)p.i + q.c0, p.ldi, row, rest, full, [&](int k, const T* a) { g[k] = load_pack<V>(a); });
-        load_run<R, V>((const T*)p.x + q.c0, p.ldx, row, rest, full, [&](int k, const T* a) { x[k] = load_pack<V>(a); });
-        load_run<R, V>(p.dy + q.c0, p.D, row, rest, full, [&](int k, const float* a) { load_f32<V>(a, gy[k]); });
-        if constexpr (GATE)
-            load_run<R, V>((const T*)p.z + q.c0, p.ldz, row, rest, full, [&](int k, const T* a) { z[k] = load_pack<V>(a); });
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            r[k] = load_pack<V>(token_at<T>(p.r, p.ldr, row, rest, full, k) + q.c0);
+            g[k] = load_pack<V>(token_at<T>(p.i, p.ldi, row, rest, full, k) + q.c0);
+            x[k] = load_pack<V>(token_at<T>(p.x, p.ldx, row, rest, full, k) + q.c0);
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            load_f32<V>(token_at<float>(p.dy, p.D, row, rest, full, k) + q.c0, gy[k]);
+            if constexpr (GATE) z[k] = load_pack<V>(token_at<T>(p.z, p.ldz, row, rest, full, k) + q.c0);
+        }
         load_f32<V>(p.A_log + q.c0, A);
 #pragma unroll
         for (int v = 0; v < V; ++v) A[v] = rate_of(A[v]);
@@ -451,6 +473,7 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
                 end_h[v] = advance(end_h[v], mm, u);
                 end_p[v] = fmaf(-mm, end_p[v], end_p[v]);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (SEQ && s.fresh) {
 #pragma unroll
@@ -559,6 +582,7 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
 #pragma unroll
                 for (int v = 0; v < V; ++v) e[v] = 0.f;
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     // sums over the runs of each wave, then over the waves
@@ -589,6 +613,17 @@ template <typename T> __global__ __launch_bounds__(256) void recurrence_step_ker
     const float h = advance(p.init[n], m, u);
     p.fin[n] = h;
     ((T*)p.y)[n] = (T)(p.z ? h * silu_for<T>((float)((const T*)p.z)[b * p.ldz + c]) : h);
+}
+
+// Zeros for the words that tiles publish, 16 bytes a store.
+__global__ __launch_bounds__(256) void recurrence_clear_kernel(uint4* p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = uint4{0, 0, 0, 0};
+}
+static hipError_t launch_clear(void* p, int64_t bytes, hipStream_t s) {
+    if (bytes <= 0) return hipSuccess;
+    const int64_t n = bytes / 16, g = (n + 255) / 256;
+    hipLaunchKernelGGL(recurrence_clear_kernel, dim3((unsigned)(g < 2048 ? g : 2048)), dim3(256), 0, s, (uint4*)p, n);
+    return hipGetLastError();
 }
 
 // ------------------------------------------------------------------ launches
@@ -688,7 +723,7 @@ RecSizes rec_sizes(const ssd_recurrence_problem_t* p) {
 
 bool empty(const ssd_recurrence_problem_t* p) { return p->batch == 0 || p->seqlen == 0; }
 
-// What the tiles publish, in bytes from the workspace's start: a counter, maps, states.
+// What the tiles publish, in bytes from the workspace's start: counters, maps, states.
 struct ChainSpace {
     int64_t maps, states, total;
 };
@@ -696,7 +731,7 @@ ChainSpace chain_space(const ssd_recurrence_problem_t* p, const Shape& s) {
     ChainSpace c{};
     if (empty(p) || s.ntile == 1) return c;
     const int64_t chains = p->batch * s.nblk, groups = (s.ntile + ssd::kGroup - 1) / ssd::kGroup;
-    c.maps = 256;
+    c.maps = align256(chains * ssd::kCounter * 4);
     c.states = c.maps + chains * s.ntile * ssd::kBlock * 8;
     c.total = align256(c.states + chains * groups * ssd::kBlock * 8);
     return c;
@@ -725,7 +760,7 @@ ssd::Chain chain_at(const ssd_recurrence_problem_t* p, const Shape& s, void* at)
     char* base = static_cast<char*>(at);
     ssd::Chain r{};
     if (c.total) {
-        r.counter = reinterpret_cast<unsigned*>(base);
+        r.counters = reinterpret_cast<unsigned*>(base);
         r.maps = reinterpret_cast<uint64_t*>(base + c.maps);
         r.states = reinterpret_cast<uint64_t*>(base + c.states);
     }
@@ -815,7 +850,7 @@ int ssd_recurrence_forward(const ssd_recurrence_problem_t* p, const void* x, con
     c.y = y;
     c.fin = final_state;
     c.stream = n.y > ssd::kStreamBytes;
-    hipError_t h = ssd::launch_fill(static_cast<float*>(workspace), wsb / 4, st);
+    hipError_t h = ssd::launch_clear(workspace, wsb, st);
     if (h == hipSuccess) h = run_pass(p, ssd::kForward, c, workspace, st);
     return done("forward", p, h);
 }
@@ -890,7 +925,7 @@ int ssd_recurrence_backward(const ssd_recurrence_problem_t* p, const void* x, co
     char* base = static_cast<char*>(workspace);
     const Shape s = shape_of(p, true);
     const bool direct = p->batch * s.ntile == 1;         // a single tile writes dA_log itself
-    e2 = ssd::launch_fill(reinterpret_cast<float*>(base), w.kept / 4, st);
+    e2 = ssd::launch_clear(base, w.kept, st);
     if (e2 == hipSuccess && pieces_of(p) > 1) {
         c.kept = reinterpret_cast<float*>(base + w.kept);
         e2 = run_pass(p, ssd::kKeep, c, base, st);
