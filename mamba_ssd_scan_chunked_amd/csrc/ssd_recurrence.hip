@@ -306,6 +306,18 @@ template <typename T> __device__ inline const T* token_at(const void* base, int6
     return (const T*)base + (row + (full || k < rest ? k : rest - 1)) * ld;
 }
 
+// Keeps a pack of bf16 as it was loaded: without this the compiler converts it once and holds the
+// fp32 values, twice the registers, until their last use.
+template <typename T, int V> __device__ inline void stay_packed(Pack<T, V>& p) {
+    if constexpr (sizeof(p) % 4 == 0 && sizeof(T) < 4) {
+        uint32_t w[sizeof(p) / 4];
+        __builtin_memcpy(w, &p, sizeof(p));
+#pragma unroll
+        for (unsigned k = 0; k < sizeof(p) / 4; ++k) asm volatile("" : "+v"(w[k]));
+        __builtin_memcpy(&p, w, sizeof(p));
+    }
+}
+
 // A step of the state.
 __device__ inline float advance(float h, float m, float u) { return h + fmaf(-m, h, u); }
 
@@ -420,9 +432,19 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
     const int64_t piece = (int64_t)tile * waves + q.wave, w0 = piece * TOK, t0 = w0 + q.group * R, rest = p.T - t0;
     const int64_t row = q.b * p.T + t0;
     const bool full = w0 + TOK <= p.T;
-    Pack<T, V> x[R], r[R], g[R], z[GATE ? R : 1];
-    float m[R][V], hp[R][V], gy[R][V], A[V];
     Runs<SEQ ? R : 1> s{};
+    Pack<T, V> x[R], r[R], g[R], z[GATE ? R : 1];
+    float m[R][V], gy[R][V], A[V];
+    float hp[R][V];                  // what each token adds, then the state before it
+    // the state before the first token of a sequence
+    auto begin = [&](int k, float (&h)[V]) {
+        if (p.init) {
+            load_f32<V>(p.init + (int64_t)s.id[SEQ ? k : 0] * p.D + q.c0, h);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = 0.f;
+        }
+    };
     if (SEQ) s = runs_of<SEQ ? R : 1>(p, load_ids<SEQ ? R : 1>(p, q.b, t0), t0);
     float end_p[V], end_h[V];
 #pragma unroll
@@ -434,7 +456,6 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
     } else if (!SEQ && p.init) {
         h0 = p.init[q.b * p.D + q.own];
     }
-    float P[R][V];                   // map from the run's start to before each token, with hp
     if (q.active) {
 #pragma unroll
         for (int k = 0; k < R; ++k) {
@@ -452,27 +473,18 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
         for (int v = 0; v < V; ++v) A[v] = rate_of(A[v]);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const bool fresh = SEQ && (s.fresh >> k & 1);
-            if (fresh) {
-                if (p.init) {
-                    load_f32<V>(p.init + (int64_t)s.id[SEQ ? k : 0] * p.D + q.c0, end_h);
-                } else {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) end_h[v] = 0.f;
-                }
-            }
+            if (SEQ && (s.fresh >> k & 1)) begin(k, end_h);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float mm = one_minus_exp2(A[v] * gate_of<EXACT>((float)r[k].v[v]));
-                float u = beta_of(mm) * (gate_of<EXACT>((float)g[k].v[v]) * (float)x[k].v[v]);
-                if (!full && k >= rest) mm = u = gy[k][v] = 0.f;
-                m[k][v] = mm;
-                if (fresh) end_p[v] = 0.f;
-                P[k][v] = end_p[v];
-                hp[k][v] = end_h[v];
-                end_h[v] = advance(end_h[v], mm, u);
-                end_p[v] = fmaf(-mm, end_p[v], end_p[v]);
+                m[k][v] = one_minus_exp2(A[v] * gate_of<EXACT>((float)r[k].v[v]));
+                hp[k][v] = beta_of(m[k][v]) * (gate_of<EXACT>((float)g[k].v[v]) * (float)x[k].v[v]);
+                if (!full && k >= rest) m[k][v] = hp[k][v] = gy[k][v] = 0.f;
+                end_h[v] = advance(end_h[v], m[k][v], hp[k][v]);
+                end_p[v] = fmaf(-m[k][v], end_p[v], end_p[v]);
             }
+            stay_packed(r[k]);
+            stay_packed(g[k]);
+            stay_packed(x[k]);
             __builtin_amdgcn_sched_barrier(0);
         }
         if (SEQ && s.fresh) {
@@ -502,20 +514,20 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
         load_f32<V>(&j.H[q.wave][q.group][q.slot], h);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const bool fresh = SEQ && (s.fresh >> k & 1);
             const bool last = SEQ ? (s.last >> k & 1) : k + 1 == rest;
+            if (SEQ && (s.fresh >> k & 1)) begin(k, h);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (fresh) h[v] = 0.f;                       // P is 0 from here on in the run
-                hp[k][v] = fmaf(P[k][v], h[v], hp[k][v]);
+                const float u = hp[k][v];
+                hp[k][v] = h[v];
+                h[v] = advance(h[v], m[k][v], u);
             }
             if constexpr (GATE) {
                 float dz[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const float zv = (float)z[k].v[v], sz = gate_of<EXACT>(zv);
-                    const float u = beta_of(m[k][v]) * (gate_of<EXACT>((float)g[k].v[v]) * (float)x[k].v[v]);
-                    dz[v] = gy[k][v] * advance(hp[k][v], m[k][v], u) * silu_slope(zv, sz);
+                    dz[v] = gy[k][v] * h[v] * silu_slope(zv, sz);
                     gy[k][v] *= zv * sz;
                 }
                 if (k < rest) store_f32<V, STREAM>(p.dz + (row + k) * p.D + q.c0, dz);
@@ -628,31 +640,41 @@ static hipError_t launch_clear(void* p, int64_t bytes, hipStream_t s) {
 
 // ------------------------------------------------------------------ launches
 enum Pass { kForward, kKeep, kBackward };
-template <typename T, int V, bool SEQ, bool GATE, bool STREAM>
-static void launch_one(Pass pass, const RecurrenceParams& p, int waves, hipStream_t s) {
+template <Pass PASS, typename T, int V, bool SEQ, bool GATE, bool STREAM>
+static void launch_one(const RecurrenceParams& p, int waves, hipStream_t s) {
     const dim3 grid(p.nblk * (unsigned)p.batch * p.ntile), block(64 * waves);
     constexpr int TOK = V == 1 ? 16 : 32;
-    if (pass == kForward) hipLaunchKernelGGL((recurrence_forward_kernel<T, V, TOK, SEQ, GATE, STREAM, false>), grid, block, 0, s, p);
-    if (pass == kBackward) hipLaunchKernelGGL((recurrence_backward_kernel<T, V, SEQ, GATE, STREAM>), grid, block, 0, s, p);
-    if constexpr (!GATE && !STREAM) {
-        if (pass == kKeep) hipLaunchKernelGGL((recurrence_forward_kernel<T, V, TOK, SEQ, false, false, true>), grid, block, 0, s, p);
-    }
+    if constexpr (PASS == kBackward)
+        hipLaunchKernelGGL((recurrence_backward_kernel<T, V, SEQ, GATE, STREAM>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((recurrence_forward_kernel<T, V, TOK, SEQ, GATE, STREAM, PASS == kKeep>), grid, block, 0, s, p);
 }
-template <typename T, int V, bool STREAM> static void launch_seq(Pass pass, const RecurrenceParams& p, int waves, hipStream_t s) {
-    const bool gate = p.z && pass != kKeep;
-    if (p.seq_idx) {
-        if (gate) launch_one<T, V, true, true, STREAM>(pass, p, waves, s);
-        else launch_one<T, V, true, false, STREAM>(pass, p, waves, s);
-    } else {
-        if (gate) launch_one<T, V, false, true, STREAM>(pass, p, waves, s);
-        else launch_one<T, V, false, false, STREAM>(pass, p, waves, s);
+template <Pass PASS, typename T, int V, bool STREAM> static void launch_seq(const RecurrenceParams& p, int waves, hipStream_t s) {
+    if constexpr (PASS != kKeep) {
+        if (p.z) {
+            if (p.seq_idx) launch_one<PASS, T, V, true, true, STREAM>(p, waves, s);
+            else launch_one<PASS, T, V, false, true, STREAM>(p, waves, s);
+            return;
+        }
     }
+    if (p.seq_idx) launch_one<PASS, T, V, true, false, STREAM>(p, waves, s);
+    else launch_one<PASS, T, V, false, false, STREAM>(p, waves, s);
 }
 // Rows narrower than a vector take a channel per lane.
-template <typename T, int V> static hipError_t launch_pass(Pass pass, const RecurrenceParams& p, int waves, hipStream_t s) {
-    if (p.D < V) launch_seq<T, 1, false>(pass, p, waves, s);
-    else if (p.stream && pass != kKeep) launch_seq<T, V, true>(pass, p, waves, s);
-    else launch_seq<T, V, false>(pass, p, waves, s);
+template <Pass PASS, typename T, int V> static void launch_width(const RecurrenceParams& p, int waves, hipStream_t s) {
+    if (p.D < V) return launch_seq<PASS, T, 1, false>(p, waves, s);
+    if constexpr (PASS != kKeep) {
+        if (p.stream) return launch_seq<PASS, T, V, true>(p, waves, s);
+    }
+    launch_seq<PASS, T, V, false>(p, waves, s);
+}
+// Vectors are 16 bytes of the activations, but backwards of the fp32 gradients: with eight
+// channels a lane, whose stores of 16 bytes lie 32 apart, three gradients of 4 x 4096 x 2560 went
+// out at 4.0 TB/s, with four at 5.4.
+constexpr int vector_of(Pass pass, bool bf16) { return bf16 && pass != kBackward ? 8 : 4; }
+template <Pass PASS> static hipError_t launch_pass(bool bf16, const RecurrenceParams& p, int waves, hipStream_t s) {
+    if (bf16) launch_width<PASS, __bf16, vector_of(PASS, true)>(p, waves, s);
+    else launch_width<PASS, float, vector_of(PASS, false)>(p, waves, s);
     return hipGetLastError();
 }
 
@@ -664,17 +686,15 @@ using namespace ssd_host;
 
 constexpr int64_t kMaxDim = int64_t(1) << 31;
 
-// Channels per lane, blocks of channels, waves of a workgroup and tiles per row.
+// Blocks of channels, waves of a workgroup and tiles per row.
 struct Shape {
-    int V;
     int64_t nblk, waves, ntile;
 };
 Shape shape_of(const ssd_recurrence_problem_t* p, bool back) {
-    const int V = p->dtype == SSD_DTYPE_BF16 ? 8 : 4;
     Shape s;
-    s.V = p->channels < V ? 1 : V;
     s.nblk = (p->channels + ssd::kBlock - 1) / ssd::kBlock;
-    const int64_t tokens = back || s.V == 1 ? ssd::kRunBack : 32;        // of a wave
+    const bool narrow = p->channels < ssd::vector_of(ssd::kForward, p->dtype == SSD_DTYPE_BF16);
+    const int64_t tokens = back || narrow ? ssd::kRunBack : 32;          // of a wave
     const int64_t runs = std::max<int64_t>(1, (p->seqlen + tokens - 1) / tokens);
     s.waves = std::min<int64_t>(ssd::kWaves, runs);
     s.ntile = (runs + s.waves - 1) / s.waves;
@@ -797,13 +817,13 @@ int done(const char* what, const ssd_recurrence_problem_t* p, hipError_t e) {
 }
 
 // One pass over the rows; `space` holds its chain, zeroed.
-hipError_t run_pass(const ssd_recurrence_problem_t* p, ssd::Pass pass, ssd::RecurrenceParams c, void* space, hipStream_t st) {
-    const Shape s = shape_of(p, pass == ssd::kBackward);
+template <ssd::Pass PASS>
+hipError_t run_pass(const ssd_recurrence_problem_t* p, ssd::RecurrenceParams c, void* space, hipStream_t st) {
+    const Shape s = shape_of(p, PASS == ssd::kBackward);
     c.nblk = (unsigned)s.nblk;
     c.ntile = (unsigned)s.ntile;
     c.chain = chain_at(p, s, space);
-    return p->dtype == SSD_DTYPE_BF16 ? ssd::launch_pass<__bf16, 8>(pass, c, (int)s.waves, st)
-                                      : ssd::launch_pass<float, 4>(pass, c, (int)s.waves, st);
+    return ssd::launch_pass<PASS>(p->dtype == SSD_DTYPE_BF16, c, (int)s.waves, st);
 }
 
 }  // namespace
@@ -851,7 +871,7 @@ int ssd_recurrence_forward(const ssd_recurrence_problem_t* p, const void* x, con
     c.fin = final_state;
     c.stream = n.y > ssd::kStreamBytes;
     hipError_t h = ssd::launch_clear(workspace, wsb, st);
-    if (h == hipSuccess) h = run_pass(p, ssd::kForward, c, workspace, st);
+    if (h == hipSuccess) h = run_pass<ssd::kForward>(p, c, workspace, st);
     return done("forward", p, h);
 }
 
@@ -928,7 +948,7 @@ int ssd_recurrence_backward(const ssd_recurrence_problem_t* p, const void* x, co
     e2 = ssd::launch_clear(base, w.kept, st);
     if (e2 == hipSuccess && pieces_of(p) > 1) {
         c.kept = reinterpret_cast<float*>(base + w.kept);
-        e2 = run_pass(p, ssd::kKeep, c, base, st);
+        e2 = run_pass<ssd::kKeep>(p, c, base, st);
     }
     // ids that do not occur keep a zero gradient
     if (e2 == hipSuccess && seq_idx && dinit) e2 = ssd::launch_fill(dinit, n.state / 4, st);
@@ -942,7 +962,7 @@ int ssd_recurrence_backward(const ssd_recurrence_problem_t* p, const void* x, co
         c.dinit = dinit;
         c.part = direct ? dA_log : reinterpret_cast<float*>(base + w.part);
         c.stream = n.f > ssd::kStreamBytes;
-        e2 = run_pass(p, ssd::kBackward, c, base + w.back, st);
+        e2 = run_pass<ssd::kBackward>(p, c, base + w.back, st);
     }
     if (e2 == hipSuccess && !direct) {
         ssd::ColumnSums cs{};
