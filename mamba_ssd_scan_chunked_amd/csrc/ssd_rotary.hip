@@ -48,7 +48,8 @@ __device__ inline void turn_of(int64_t position, float freq, float* c, float* s)
     *s = __builtin_amdgcn_sinf(part);
 }
 __device__ inline int64_t position_of(const RotaryParams& p, int64_t t) {
-    return p.positions ? p.positions[t] : (unsigned)t % (unsigned)p.seqlen;      // both at most 2^31
+    if (p.positions) return p.positions[t];
+    return (unsigned)t % (unsigned)p.seqlen;               // both at most 2^31
 }
 
 // A lane's channels: its M units are e = lane, lane + L, ..., each two packs of V channels.
