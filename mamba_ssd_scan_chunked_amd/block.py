@@ -179,6 +179,14 @@ def _output(name, t, shape, dtype, dev):
     return t
 
 
+def _output_like(name, t, like, dev):
+    """The same for an output of ``like``'s shape and type (torch.empty takes a microsecond more)."""
+    if t is None:
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    _pkg._check_buffer(name, t, like.shape, like.dtype, dev)
+    return t
+
+
 FAR = 1 << 31                         # the library takes distances below this,
 FAR_IN_TILE = 1 << 25                 # and below this where a tile has 32-bit offsets
 
@@ -203,6 +211,35 @@ def _rows(t, far=FAR):
             if D <= ld < far:
                 return t, ld
     return t.contiguous(), D
+
+
+def _head_rows(name, t, like):
+    """B or C (..., G, N) of ``like``'s type and device as tokens ld elements apart: (t, ld),
+    copied if it is not that."""
+    if t.device != like.device:
+        raise ValueError("%s is on %s, B on %s" % (name, t.device, like.device))
+    if t.dtype is not like.dtype:
+        raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
+    shape = t.shape
+    width = shape[-2] * shape[-1]
+    if t.is_contiguous():
+        return t, width
+    stride = t.stride()
+    if stride[-1] == 1 and (stride[-2] == shape[-1] or shape[-2] == 1):
+        ld = step = 0
+        for size, apart in zip(shape[-3::-1], stride[-3::-1]):
+            if size == 1:
+                continue
+            if ld and apart != step:
+                break
+            ld = ld or apart
+            step = apart * size
+            if not ld:                          # a broadcast dimension
+                break
+        else:
+            if width <= ld < FAR:
+                return t, ld
+    return t.contiguous(), width
 
 
 def _workspace(ws, nbytes, dev):
@@ -521,7 +558,7 @@ def gated_recurrence(x, r, i, A_log, z=None, init_state=None, seq_idx=None, nseq
     dev = _gpu(x)
     with _on(dev, stream):
         p, args = _recurrence_arguments(x, r, i, A_log, z, init_state, seq_idx, nseqs)
-        y = _output("y", y, x.shape, x.dtype, dev)
+        y = _output_like("y", y, x, dev)
         if final_state is not None or return_final:
             final_state = _output("final_state", final_state, (p.nseqs, p.channels), torch.float32, dev)
         ws, nbytes = _workspace(workspace, recurrence_workspace_size(p), dev)
@@ -542,10 +579,11 @@ def gated_recurrence_backward(x, r, i, A_log, dy, z=None, init_state=None, dfina
         state = (p.nseqs, p.channels)
         dy = _given("dy", dy, x.shape, f32, dev)
         dfinal = _given("dfinal", dfinal, state, f32, dev)
-        shapes = {"dx": x.shape, "dr": x.shape, "di": x.shape, "dA_log": A_log.shape, "dz": x.shape, "dinit": state}
-        if z is None:
-            del shapes["dz"]
-        out = {k: torch.empty(s, dtype=f32, device=dev) for k, s in shapes.items()}
+        like = torch.empty_like
+        out = {"dx": like(dy), "dr": like(dy), "di": like(dy), "dA_log": like(args[3]),
+               "dinit": torch.empty(state, dtype=f32, device=dev)}
+        if z is not None:
+            out["dz"] = like(dy)
         ws, nbytes = _workspace(workspace, recurrence_backward_workspace_size(p), dev)
         _check(_lib().ssd_recurrence_backward(ctypes.byref(p), *map(_ptr, args), _ptr(dy), _ptr(dfinal),
                                               _ptr(out["dx"]), _ptr(out["dr"]), _ptr(out["di"]), _ptr(out["dA_log"]),
@@ -564,7 +602,7 @@ def gated_recurrence_step(x, r, i, A_log, state, z=None, y=None, state_out=None,
         b, D = x.shape
         (xr, r, i, z), lds, A_log, code = _recurrence_activations(x, r, i, A_log, z)
         state, state_out = _states(state, state_out, (b, D), dev)
-        y = _output("y", y, (b, D), x.dtype, dev)
+        y = _output_like("y", y, x, dev)
         p = recurrence_problem(b, 1, D, b, code, *lds)
         _check(_lib().ssd_recurrence_step(ctypes.byref(p), _ptr(xr), _ptr(r), _ptr(i), _ptr(A_log), _ptr(z),
                                           _ptr(state), _ptr(state_out), _ptr(y), _current(dev)))
@@ -585,23 +623,26 @@ def rotary_norm_backward_workspace_size(p: RotaryProblem) -> int:
 
 def _rotary_arguments(B, C, b_weight, c_weight, freqs, positions, interleaved, eps):
     """(problem, pointers' tensors in the order of the C call up to positions)."""
-    if B.dim() < 3 or C.dim() != B.dim() or C.shape[:-2] != B.shape[:-2] or C.shape[-1] != B.shape[-1]:
+    shape, other = B.shape, C.shape
+    if len(shape) < 3 or other[:-2] != shape[:-2] or other[-1] != shape[-1]:
         raise ValueError("B and C must be (..., G, N) with the same tokens and N")
     if freqs.dim() != 1:
         raise ValueError("freqs must have one dimension (rotary_dim / 2)")
     dev, f32 = B.device, torch.float32
-    lead, (G, N), H = B.shape[:-2], B.shape[-2:], C.shape[-2]
+    G, N = shape[-2:]
     code = _dtype("B", B)
     b_weight = _given("b_weight", b_weight, (N,), f32, dev)
     c_weight = _given("c_weight", c_weight, (N,), f32, dev)
     freqs = _given("freqs", freqs, freqs.shape, f32, dev)
-    positions = _given("positions", positions, lead, torch.int32, dev)
-    B, ldb = _grouped("B", B, (*lead, G, N), B, FAR)
-    C, ldc = _grouped("C", C, (*lead, H, N), B, FAR)
+    if positions is not None:
+        positions = _given("positions", positions, shape[:-2], torch.int32, dev)
+    B, ldb = _head_rows("B", B, B)
+    C, ldc = _head_rows("C", C, B)
     tokens = 1
-    for n in lead:
+    for n in shape[:-2]:
         tokens *= n
-    p = rotary_problem(tokens, G, H, N, 2 * freqs.shape[0], max(1, lead[-1]), eps, code, interleaved, ldb, ldc)
+    p = RotaryProblem(tokens, shape[-3] or 1, G, other[-2], N, 2 * freqs.shape[0], ldb, ldc, eps, code,
+                      ROTARY_INTERLEAVED if interleaved else 0, 0)
     return p, (B, C, b_weight, c_weight, freqs, positions)
 
 
@@ -618,10 +659,9 @@ def rotary_norm(B, C, b_weight, c_weight, freqs, positions=None, interleaved: bo
     their type."""
     dev = _gpu(B)
     with _on(dev, stream):
-        shapes = B.shape, C.shape
         p, args = _rotary_arguments(B, C, b_weight, c_weight, freqs, positions, interleaved, eps)
-        B_out = _output("B_out", B_out, shapes[0], B.dtype, dev)
-        C_out = _output("C_out", C_out, shapes[1], B.dtype, dev)
+        B_out = _output_like("B_out", B_out, B, dev)
+        C_out = _output_like("C_out", C_out, C, dev)
         _check(_lib().ssd_rotary_norm_forward(ctypes.byref(p), *map(_ptr, args), _ptr(B_out), _ptr(C_out),
                                               _current(dev)))
     return B_out, C_out
@@ -637,9 +677,8 @@ def rotary_norm_backward(B, C, b_weight, c_weight, freqs, dB_out, dC_out, positi
         p, args = _rotary_arguments(B, C, b_weight, c_weight, freqs, positions, interleaved, eps)
         dB_out = _given("dB_out", dB_out, B.shape, f32, dev)
         dC_out = _given("dC_out", dC_out, C.shape, f32, dev)
-        out = {"dB": torch.empty(B.shape, dtype=f32, device=dev), "dC": torch.empty(C.shape, dtype=f32, device=dev),
-               "db_weight": torch.empty(p.headdim, dtype=f32, device=dev),
-               "dc_weight": torch.empty(p.headdim, dtype=f32, device=dev)}
+        like = torch.empty_like
+        out = {"dB": like(dB_out), "dC": like(dC_out), "db_weight": like(args[2]), "dc_weight": like(args[3])}
         ws, nbytes = _workspace(workspace, rotary_norm_backward_workspace_size(p), dev)
         _check(_lib().ssd_rotary_norm_backward(ctypes.byref(p), *map(_ptr, args), _ptr(dB_out), _ptr(dC_out),
                                                _ptr(out["dB"]), _ptr(out["dC"]), _ptr(out["db_weight"]),

@@ -627,14 +627,16 @@ template <typename T> __global__ __launch_bounds__(256) void recurrence_step_ker
     ((T*)p.y)[n] = (T)(p.z ? h * silu_for<T>((float)((const T*)p.z)[b * p.ldz + c]) : h);
 }
 
-// Zeros for the words that tiles publish, 16 bytes a store.
-__global__ __launch_bounds__(256) void recurrence_clear_kernel(uint4* p, int64_t n) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = uint4{0, 0, 0, 0};
+// Zeros for the words that tiles publish, 16 bytes a store, and for a second array.
+__global__ __launch_bounds__(256) void recurrence_clear_kernel(uint4* p, int64_t n, float* q, int64_t m) {
+    const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    for (int64_t i = first; i < n; i += step) p[i] = uint4{0, 0, 0, 0};
+    for (int64_t i = first; i < m; i += step) q[i] = 0.f;
 }
-static hipError_t launch_clear(void* p, int64_t bytes, hipStream_t s) {
-    if (bytes <= 0) return hipSuccess;
-    const int64_t n = bytes / 16, g = (n + 255) / 256;
-    hipLaunchKernelGGL(recurrence_clear_kernel, dim3((unsigned)(g < 2048 ? g : 2048)), dim3(256), 0, s, (uint4*)p, n);
+static hipError_t launch_clear(void* p, int64_t bytes, float* q, int64_t floats, hipStream_t s) {
+    const int64_t n = bytes / 16, g = (std::max(n, floats) + 255) / 256;
+    if (g <= 0) return hipSuccess;
+    hipLaunchKernelGGL(recurrence_clear_kernel, dim3((unsigned)(g < 2048 ? g : 2048)), dim3(256), 0, s, (uint4*)p, n, q, floats);
     return hipGetLastError();
 }
 
@@ -870,7 +872,7 @@ int ssd_recurrence_forward(const ssd_recurrence_problem_t* p, const void* x, con
     c.y = y;
     c.fin = final_state;
     c.stream = n.y > ssd::kStreamBytes;
-    hipError_t h = ssd::launch_clear(workspace, wsb, st);
+    hipError_t h = ssd::launch_clear(workspace, wsb, nullptr, 0, st);
     if (h == hipSuccess) h = run_pass<ssd::kForward>(p, c, workspace, st);
     return done("forward", p, h);
 }
@@ -945,13 +947,12 @@ int ssd_recurrence_backward(const ssd_recurrence_problem_t* p, const void* x, co
     char* base = static_cast<char*>(workspace);
     const Shape s = shape_of(p, true);
     const bool direct = p->batch * s.ntile == 1;         // a single tile writes dA_log itself
-    e2 = ssd::launch_clear(base, w.kept, st);
+    // ids that do not occur keep a zero gradient
+    e2 = ssd::launch_clear(base, w.kept, dinit, seq_idx && dinit ? n.state / 4 : 0, st);
     if (e2 == hipSuccess && pieces_of(p) > 1) {
         c.kept = reinterpret_cast<float*>(base + w.kept);
         e2 = run_pass<ssd::kKeep>(p, c, base, st);
     }
-    // ids that do not occur keep a zero gradient
-    if (e2 == hipSuccess && seq_idx && dinit) e2 = ssd::launch_fill(dinit, n.state / 4, st);
     if (e2 == hipSuccess) {
         c.dy = dy;
         c.dfin = dfinal;
