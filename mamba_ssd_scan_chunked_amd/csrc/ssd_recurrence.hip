@@ -329,6 +329,7 @@ __global__ __launch_bounds__(64 * kWaves, GATE || sizeof(T) == 4 ? 1 : 4) void r
     __shared__ Joint<V> j;
     Tile q = tile_of<V>(p);
     take_tile(p, q, &j.ticket);
+    if (q.at >= p.ntile) return;             // only in a workspace that another call writes too
     const int waves = blockDim.x >> 6;
     const int64_t w0 = ((int64_t)q.at * waves + q.wave) * TOK, t0 = w0 + q.group * R, rest = p.T - t0, row = q.b * p.T + t0;
     const bool full = w0 + TOK <= p.T;
@@ -427,6 +428,7 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
     __shared__ float sums[kWaves][kBlock];
     Tile q = tile_of<V>(p);
     take_tile(p, q, &j.ticket);
+    if (q.at >= p.ntile) return;             // only in a workspace that another call writes too
     const int waves = blockDim.x >> 6;
     const unsigned tile = p.ntile - 1 - q.at;
     const int64_t piece = (int64_t)tile * waves + q.wave, w0 = piece * TOK, t0 = w0 + q.group * R, rest = p.T - t0;
@@ -449,7 +451,7 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
     float end_p[V], end_h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) end_p[v] = 1.f, end_h[v] = 0.f;
-    // the state before the wave's first token, of the lane's place
+    // the state before the wave's first token (or the row's), of the lane's place
     float h0 = 0.f;
     if (p.kept) {
         if (w0 < p.T) h0 = p.kept[(q.b * p.pieces + piece) * p.D + q.own];
@@ -500,6 +502,14 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
         Map run[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) run[k] = {j.P[q.wave][k][lane], j.H[q.wave][k][lane]};
+        if (!p.kept && waves > 1) {          // a single tile: from the waves before
+            Map all{1.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < V; ++k) all = then<SEQ>(all, run[k]);
+            j.before[q.wave][lane] = all;
+            __syncthreads();
+            for (int k = 0; k < q.wave; ++k) h0 = apply<SEQ>(j.before[k][lane], h0);
+        }
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             j.H[q.wave][k][lane] = h0;
@@ -768,9 +778,10 @@ BackwardSpace backward_space(const ssd_recurrence_problem_t* p) {
     if (empty(p)) return w;
     const Shape s = shape_of(p, true);
     const int64_t pieces = pieces_of(p);
-    w.back = pieces > 1 ? chain_space(p, shape_of(p, false)).total : 0;
+    const bool keep = s.ntile > 1;                       // a single tile finds its states itself
+    w.back = keep ? chain_space(p, shape_of(p, false)).total : 0;
     w.kept = w.back + chain_space(p, s).total;
-    w.part = w.kept + (pieces > 1 ? align256(p->batch * pieces * p->channels * 4) : 0);
+    w.part = w.kept + (keep ? align256(p->batch * pieces * p->channels * 4) : 0);
     w.total = w.part + (p->batch * s.ntile > 1 ? align256(p->batch * s.ntile * p->channels * 4) : 0);
     return w;
 }
@@ -949,7 +960,7 @@ int ssd_recurrence_backward(const ssd_recurrence_problem_t* p, const void* x, co
     const bool direct = p->batch * s.ntile == 1;         // a single tile writes dA_log itself
     // ids that do not occur keep a zero gradient
     e2 = ssd::launch_clear(base, w.kept, dinit, seq_idx && dinit ? n.state / 4 : 0, st);
-    if (e2 == hipSuccess && pieces_of(p) > 1) {
+    if (e2 == hipSuccess && s.ntile > 1) {
         c.kept = reinterpret_cast<float*>(base + w.kept);
         e2 = run_pass<ssd::kKeep>(p, c, base, st);
     }

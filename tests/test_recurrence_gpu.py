@@ -384,6 +384,57 @@ def test_offsets_past_32_bits():
     assert torch.equal(f[-1], f1[0]) and torch.equal(y[-1], y1[0]) and torch.equal(y[0], y1[0])
 
 
+def test_many_rows():
+    """More rows than a launch has in a second dimension; chains of one tile and of several."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("recurrence many rows")
+    for b, T, D in ((70000, 2, 4), (3000, 70, 8), (600, 300, 5)):
+        one = make("f32", 3, T, D)
+        big = {k: (v.repeat(b // 3, *[1] * (v.dim() - 1)) if torch.is_tensor(v) and v.dim() > 1 and v.shape[0] == 3 else v)
+               for k, v in one.items()}
+        big["n"] = big["x"].shape[0]
+        y, f = forward(ssd, big)
+        y3, f3 = forward(ssd, one)
+        m = b // 3
+        assert torch.equal(y.view(m, 3, T, D), y3.expand(m, 3, T, D)) and torch.equal(f.view(m, 3, D), f3.expand(m, 3, D))
+        g, g3 = backward(ssd, big), backward(ssd, one)
+        for k in ("dx", "dr", "di", "dz"):
+            assert torch.equal(g[k].view(m, 3, T, D), g3[k].expand(m, 3, T, D)), k
+        assert torch.equal(g["dinit"].view(m, 3, D), g3["dinit"].expand(m, 3, D))
+
+
+def test_outputs_larger_than_the_caches():
+    """Outputs stored past the caches are the same values."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("recurrence large outputs")
+    for dt, b, T, D in (("bf16", 3, 3000, 2050), ("f32", 2, 3000, 1500)):
+        q = make(dt, 1, T, 50, gate=True)
+        wide_ = {k: gpu(v).repeat(*([b] + [1] * (v.dim() - 2) + [D // 50])) if torch.is_tensor(v) and v.dim() > 1 else v
+                 for k, v in q.items()}
+        wide_["A_log"] = q["A_log"].repeat(D // 50)
+        wide_["n"] = b
+        y, f = forward(ssd, wide_)
+        assert y.numel() * y.element_size() > 32 << 20
+        y1, f1 = forward(ssd, q)
+        assert torch.equal(y.unflatten(-1, (-1, 50)), y1.unsqueeze(2).expand(b, T, D // 50, 50))
+        assert torch.equal(f.view(b, -1, 50), f1[:, None].expand(b, D // 50, 50))
+        g, g1 = backward(ssd, wide_), backward(ssd, q)
+        for k in ("dx", "dr", "di", "dz"):
+            assert torch.equal(g[k].unflatten(-1, (-1, 50)), g1[k].unsqueeze(2).expand(b, T, D // 50, 50)), k
+
+
+def test_sequence_ids_out_of_range_stay_in_memory():
+    """Ids beyond the states are clamped: values undefined, memory safe."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("recurrence ids out of range")
+    q = make("f32", 1, 200, 20, [[100, 100]])
+    guard = torch.full((4, 20), 3.0, device="cuda")
+    q["ids"] = torch.where(torch.arange(200)[None] < 100, -5, 1000).int()
+    y, f = forward(ssd, q, final_state=guard[1:3])
+    assert (guard[0] == 3.0).all() and (guard[3] == 3.0).all() and torch.isfinite(y).all()
+    assert all(torch.isfinite(t).all() for t in backward(ssd, q).values())
+
+
 def test_arguments_are_checked():
     import mamba_ssd_scan_chunked_amd as ssd
     announce("recurrence arguments")
