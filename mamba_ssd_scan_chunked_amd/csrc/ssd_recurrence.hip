@@ -323,7 +323,7 @@ __device__ inline float advance(float h, float m, float u) { return h + fmaf(-m,
 
 // Whole rows.  TOK tokens per wave; KEEP: no output, but the state before every kRunBack-th token.
 template <typename T, int V, int TOK, bool SEQ, bool GATE, bool STREAM, bool KEEP>
-__global__ __launch_bounds__(64 * kWaves, GATE || sizeof(T) == 4 ? 1 : 4) void recurrence_forward_kernel(RecurrenceParams p) {
+__global__ __launch_bounds__(64 * kWaves, sizeof(T) == 4 ? 1 : 4) void recurrence_forward_kernel(RecurrenceParams p) {
     constexpr int R = TOK / V, RS = SEQ ? R : 1;
     constexpr bool EXACT = sizeof(T) == 4;
     __shared__ Joint<V> j;
@@ -385,10 +385,6 @@ __global__ __launch_bounds__(64 * kWaves, GATE || sizeof(T) == 4 ? 1 : 4) void r
 #pragma unroll
         for (int v = 0; v < V; ++v) end_p[v] = -1.f;
     }
-    if constexpr (GATE) {
-#pragma unroll
-        for (int k = 0; k < R; ++k) z[k] = load_pack<V>(token_at<T>(p.z, p.ldz, row, rest, full, k) + q.c0);
-    }
     store_f32<V>(&j.P[q.wave][q.group][q.slot], end_p);
     store_f32<V>(&j.H[q.wave][q.group][q.slot], end_h);
     // a row of packed sequences begins with a fresh token, others with their initial state
@@ -400,6 +396,10 @@ __global__ __launch_bounds__(64 * kWaves, GATE || sizeof(T) == 4 ? 1 : 4) void r
         }
     });
     if (KEEP || !q.active) return;
+    if constexpr (GATE) {            // not before: its registers would cost a wave per SIMD
+#pragma unroll
+        for (int k = 0; k < R; ++k) z[k] = load_pack<V>(token_at<T>(p.z, p.ldz, row, rest, full, k) + q.c0);
+    }
     float h0[V];
     load_f32<V>(&j.H[q.wave][q.group][q.slot], h0);
 #pragma unroll

@@ -357,7 +357,7 @@ __global__ __launch_bounds__(1024) void rotary_sums_kernel(const float* part, fl
 // divided, and that leave a head at least four lanes; 0 if there are none (or a head would need
 // more than 128 units).
 static int vector_of(int64_t N, int64_t R, bool inter, int most) {
-    for (int V = most; V >= 2; V /= 2) {
+    for (int V = most; V >= (inter ? 2 : 1); V /= 2) {
         const bool fits = inter ? N % (2 * V) == 0 : R % (2 * V) == 0 && (N - R) % (2 * V) == 0;
         if (fits && N >= 8 * V) return N / (2 * V) <= 128 ? V : 0;
     }
@@ -401,13 +401,15 @@ static RotaryShape shape_of(int64_t tokens, int64_t heads, int64_t N, int64_t R,
 }
 
 template <typename T, bool BACK, int V, int L, int M> static void launch_one(const RotaryParams& p, dim3 grid, hipStream_t s) {
-    if constexpr (BACK) {
-        if (p.interleaved) hipLaunchKernelGGL((rotary_backward_kernel<T, V, L, M, true>), grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL((rotary_backward_kernel<T, V, L, M, false>), grid, dim3(256), 0, s, p);
-    } else {
-        if (p.interleaved) hipLaunchKernelGGL((rotary_forward_kernel<T, V, L, M, true>), grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL((rotary_forward_kernel<T, V, L, M, false>), grid, dim3(256), 0, s, p);
+    if constexpr (V > 1) {                   // a pair of neighbours needs a pack of two
+        if (p.interleaved) {
+            if constexpr (BACK) hipLaunchKernelGGL((rotary_backward_kernel<T, V, L, M, true>), grid, dim3(256), 0, s, p);
+            else hipLaunchKernelGGL((rotary_forward_kernel<T, V, L, M, true>), grid, dim3(256), 0, s, p);
+            return;
+        }
     }
+    if constexpr (BACK) hipLaunchKernelGGL((rotary_backward_kernel<T, V, L, M, false>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((rotary_forward_kernel<T, V, L, M, false>), grid, dim3(256), 0, s, p);
 }
 template <typename T, bool BACK> static hipError_t launch_rotary(const RotaryParams& p, const RotaryShape& k, hipStream_t s) {
     const dim3 grid((unsigned)k.groups);
@@ -422,6 +424,8 @@ template <typename T, bool BACK> static hipError_t launch_rotary(const RotaryPar
     SSD_ROTARY_CASE(4, 64, 2)
     SSD_ROTARY_CASE(2, 4, 1) SSD_ROTARY_CASE(2, 8, 1) SSD_ROTARY_CASE(2, 16, 1) SSD_ROTARY_CASE(2, 32, 1) SSD_ROTARY_CASE(2, 64, 1)
     SSD_ROTARY_CASE(2, 64, 2)
+    SSD_ROTARY_CASE(1, 4, 1) SSD_ROTARY_CASE(1, 8, 1) SSD_ROTARY_CASE(1, 16, 1) SSD_ROTARY_CASE(1, 32, 1) SSD_ROTARY_CASE(1, 64, 1)
+    SSD_ROTARY_CASE(1, 64, 2)
 #undef SSD_ROTARY_CASE
     return hipGetLastError();
 }
