@@ -10,8 +10,8 @@
 // Memory-bound if the work is spread over the card and the inputs are read once.  There is one
 // state per channel, so a row's channels alone fill a few waves: rows are cut into tiles of
 // tokens, a workgroup each.  A tile's tokens stay in registers, in runs of a few tokens per lane;
-// runs, waves and tiles are joined as maps h -> P h + H (P the product of the decays): runs by
-// lane shuffles, waves through LDS, tiles through memory.  A tile publishes its map as soon as it
+// runs, waves and tiles are joined as maps h -> P h + H (P the product of the decays): runs and
+// waves through LDS, tiles through memory.  A tile publishes its map as soon as it
 // has it and takes those of the tiles before it; every 16th tile publishes its final state
 // instead, so that a tile reads 15 maps and one state at most and the waiting grows with a
 // sixteenth of the tiles.  Maps are always composed in the same order, whoever comes first:
@@ -20,6 +20,24 @@
 // 64 channels) are handed out by its counter: a tile waits only for tiles that workgroups already
 // running have taken, so every wait ends (and it is bounded besides).  One counter for all chains
 // held the card up: 5120 workgroups took 94 us, 10240 of half the size 141.
+//
+// Backward, a first pass over the tiles leaves the state before every 16th token (one tile: none,
+// its waves join their runs in LDS); then tiles walk from a row's end, maps being q -> P q + Q of
+// what a run sends back.
+//
+// Measured on an MI355X (a device copy moves 5.1 TB/s), bf16, a call: 4 x 4096 tokens of 2560
+// channels 69 us for 336 MB, vector units at work for 74 %; 16384 tokens of 1536 with a gate 59 us
+// for 252 MB (58 %); gradients of 4 x 4096 x 2560, packed, 273 us: the first pass 72 (252 MB read),
+// the second 195 for 925 MB (74 %), sums and zeros 9; of 8 x 2048 x 1536 with a gate 176 (40 and
+// 130 for 705 MB).  So both bounds are near: about 43 vector instructions an element forward (six
+// of them transcendental) and 120 backward, a third of them the joins'.  Fewer instructions for
+// addresses (a branch for whole tiles) were slower, 77 -> 82 us; tiles of half the tokens 78 -> 91,
+// of twice as many 107; a workgroup that takes several tiles with the next one's loads in flight
+// 105 (200 registers); loads for the tile that would be next while the counter is asked 89.
+// Fp32: 4 x 2048 x 2560 73 us for 336 MB, gradients 178 (252 + 587 MB).
+// A row of more than one tile (128 tokens forward, 64 backward) costs a launch for the zeros and
+// about 2 us for the counter and the maps' way between dies: 2 x 128 tokens of 650 channels 6 us
+// on the GPU, 2 x 256 9.4; their gradients for 64 tokens 9, for 128 18.
 #include "ssd.h"
 
 #include <algorithm>
@@ -34,7 +52,6 @@ constexpr int kBlock = 64;           // channels of a workgroup
 constexpr int kWaves = 4;            // waves of a workgroup, at most
 constexpr int kGroup = 16;           // tiles from one published state to the next
 constexpr int kRunBack = 16;         // tokens of a wave backward, and between states kept for it
-
 constexpr int kCounter = 32;         // words between two chains' counters: a line each
 
 // What the tiles of one direction publish: words (chains, tiles, 64) and (chains, groups, 64).
