@@ -374,7 +374,7 @@ static int lanes_of(int64_t N, int V) {
         if (units <= L) return L;
     return 64;
 }
-constexpr int64_t kWalkers = 3072;   // three waves on each SIMD
+constexpr int64_t kWalkers = 3 * 1024;       // three waves on each SIMD
 // How a call is spread: V (0: a wave per head), lanes per head, heads per item, items, workgroups.
 struct RotaryShape {
     int V, L, M;
