@@ -21,8 +21,8 @@
 // running have taken, so every wait ends (and it is bounded besides).  One counter for all chains
 // held the card up: 5120 workgroups took 94 us, 10240 of half the size 141.
 //
-// Backward, a first pass over the tiles leaves the state before every 16th token (one tile: none,
-// its waves join their runs in LDS); then tiles walk from a row's end, maps being q -> P q + Q of
+// Backward, a first pass over the tiles leaves the state before every 16th token (not for a row of
+// one tile, whose waves join their runs in LDS); then tiles walk from a row's end, maps being q -> P q + Q of
 // what a run sends back.
 //
 // Measured on an MI355X (a device copy moves 5.1 TB/s), bf16, a call: 4 x 4096 tokens of 2560
@@ -35,9 +35,12 @@
 // of twice as many 107; a workgroup that takes several tiles with the next one's loads in flight
 // 105 (200 registers); loads for the tile that would be next while the counter is asked 89.
 // Fp32: 4 x 2048 x 2560 73 us for 336 MB, gradients 178 (252 + 587 MB).
-// A row of more than one tile (128 tokens forward, 64 backward) costs a launch for the zeros and
-// about 2 us for the counter and the maps' way between dies: 2 x 128 tokens of 650 channels 6 us
-// on the GPU, 2 x 256 9.4; their gradients for 64 tokens 9, for 128 18.
+// A row of up to 256 tokens forward, 128 backward, is one tile of up to eight waves: one launch,
+// no first pass (against two tiles that join through memory: 64 rows of 2560 channels,
+// gradients of 128 tokens 124 -> 100 us, 256 tokens forward 79 -> 75).  A longer one costs a
+// launch for the zeros and some us for the counter and the maps' way between dies: 2 rows of 650
+// channels on the GPU 5.7 us for 128 tokens, 8.0 for 256, 11 for 777; gradients 12 for 128, 25 for
+// 256, 27 for 777.
 #include "ssd.h"
 
 #include <algorithm>
@@ -49,7 +52,8 @@
 namespace ssd {
 
 constexpr int kBlock = 64;           // channels of a workgroup
-constexpr int kWaves = 4;            // waves of a workgroup, at most
+constexpr int kWaves = 8;            // waves of a workgroup, at most: rows of one tile
+constexpr int kTileWaves = 4;        // of one of several tiles
 constexpr int kGroup = 16;           // tiles from one published state to the next
 constexpr int kRunBack = 16;         // tokens of a wave backward, and between states kept for it
 constexpr int kCounter = 32;         // words between two chains' counters: a line each
@@ -163,13 +167,18 @@ template <int N> __device__ inline void await(const uint64_t* p, int64_t step, i
     }
 }
 
-// Shared memory of a workgroup: maps of the runs of each wave (H then their incoming states).
-template <int RUNS> struct Joint {
-    float P[kWaves][RUNS][kBlock], H[kWaves][RUNS][kBlock];
-    Map total[kWaves][kBlock];       // waves' maps
-    Map before[kWaves][kBlock];      // of the tiles before, in as many parts
+// Shared memory of a workgroup of up to W waves.
+template <int RUNS, int W> struct Joint {
+    struct Wave {
+        float P[RUNS][kBlock], H[RUNS][kBlock];        // maps of its runs, H then their incoming states
+        Map total[kBlock];           // its map
+        Map before[kBlock];          // of a part of the tiles before
+        float sums[kBlock];
+    };
     float carry[kBlock];             // state before the tile
-    unsigned ticket;
+    unsigned ticket, pad[3];
+    Wave wave[W];
+    static constexpr int bytes(int waves) { return (int)sizeof(Joint) - (W - waves) * (int)sizeof(Wave); }
 };
 
 // Where a workgroup and a lane work.  LPT lanes with V channels each hold a token's 64 channels;
@@ -210,25 +219,25 @@ __device__ inline void take_tile(const RecurrenceParams& p, Tile& q, unsigned* t
     q.at = __builtin_amdgcn_readfirstlane(*ticket);
 }
 
-// Joins the runs whose maps the lanes left in j.P and j.H: puts into j.H the state that reaches
+// Joins the runs whose maps the lanes left in their wave's P and H: puts into H the state that reaches
 // each run, in the order of the walk.  `first` is what reaches the row's first tile, `keep` is
 // called with the number of each run of the wave and the state that reaches it (lanes are places).
-template <int RUNS, bool SEQ, bool FORWARD, typename Keep>
-__device__ inline void join(const Chain& c, Joint<RUNS>& j, const Tile& q, unsigned ntile, int waves, float first, Keep keep) {
+template <int RUNS, bool SEQ, bool FORWARD, int W, typename Keep>
+__device__ inline void join(const Chain& c, Joint<RUNS, W>& j, const Tile& q, unsigned ntile, int waves, float first, Keep keep) {
     const int lane = threadIdx.x & 63;
     const int w = FORWARD ? q.wave : waves - 1 - q.wave;      // place of the wave in the order of the walk
     auto run = [&](int k) { return FORWARD ? k : RUNS - 1 - k; };
-    auto total = [&](int k) { return j.total[FORWARD ? k : waves - 1 - k][lane]; };
+    auto total = [&](int k) { return j.wave[FORWARD ? k : waves - 1 - k].total[lane]; };
     Map m[RUNS], all{1.f, 0.f};
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int k = 0; k < RUNS; ++k) {
-        m[k] = {j.P[q.wave][run(k)][lane], j.H[q.wave][run(k)][lane]};
+        m[k] = {j.wave[q.wave].P[run(k)][lane], j.wave[q.wave].H[run(k)][lane]};
         all = then<SEQ>(all, m[k]);
     }
     float h = first;
     if (waves > 1) {
-        j.total[q.wave][lane] = all;
+        j.wave[q.wave].total[lane] = all;
         __syncthreads();
     }
     if (ntile > 1) {
@@ -241,7 +250,7 @@ __device__ inline void join(const Chain& c, Joint<RUNS>& j, const Tile& q, unsig
             if (!closes && !ends) publish(c.maps + ((int64_t)q.chain * ntile + q.at) * kBlock + lane, own);
         }
         // the tiles of the group before this one, in `waves` parts
-        constexpr int kPart = kGroup / kWaves;
+        constexpr int kPart = kGroup / kTileWaves;
         const int n = (int)(q.at - from), per = (n + waves - 1) / waves, lo = w * per, hi = lo + per < n ? lo + per : n;
         Map part{1.f, 0.f};
         for (int k = lo; k < hi; k += kPart) {
@@ -251,7 +260,7 @@ __device__ inline void join(const Chain& c, Joint<RUNS>& j, const Tile& q, unsig
             for (int e = 0; e < kPart; ++e)
                 if (k + e < hi) part = then<SEQ>(part, map_of(word[e]));
         }
-        j.before[w][lane] = part;
+        j.wave[w].before[lane] = part;
         const unsigned ngroup = (ntile + kGroup - 1) / kGroup;
         if (w == 0 && group > 0) {
             uint64_t word[1];
@@ -260,7 +269,7 @@ __device__ inline void join(const Chain& c, Joint<RUNS>& j, const Tile& q, unsig
         }
         __syncthreads();
         if (w == 0) {
-            for (int k = 0; k < waves; ++k) h = apply<SEQ>(j.before[k][lane], h);
+            for (int k = 0; k < waves; ++k) h = apply<SEQ>(j.wave[k].before[lane], h);
             if (closes && !ends)
                 publish(c.states + ((int64_t)q.chain * ngroup + group) * kBlock + lane, Map{1.f, apply<SEQ>(own, h)});
             j.carry[lane] = h;
@@ -272,7 +281,7 @@ __device__ inline void join(const Chain& c, Joint<RUNS>& j, const Tile& q, unsig
 #pragma unroll
     for (int k = 0; k < RUNS; ++k) {
         keep(run(k), h);
-        j.H[q.wave][run(k)][lane] = h;
+        j.wave[q.wave].H[run(k)][lane] = h;
         h = apply<SEQ>(m[k], h);
     }
     __builtin_amdgcn_wave_barrier();
@@ -339,15 +348,16 @@ template <typename T, int V> __device__ inline void stay_packed(Pack<T, V>& p) {
 __device__ inline float advance(float h, float m, float u) { return h + fmaf(-m, h, u); }
 
 // Whole rows.  TOK tokens per wave; KEEP: no output, but the state before every kRunBack-th token.
-template <typename T, int V, int TOK, bool SEQ, bool GATE, bool STREAM, bool KEEP>
-__global__ __launch_bounds__(64 * kWaves, sizeof(T) == 4 ? 1 : 4) void recurrence_forward_kernel(RecurrenceParams p) {
+// W: waves of a workgroup, at most (one kernel for both numbers was 3 % slower with tiles of four).
+template <typename T, int V, int TOK, int W, bool SEQ, bool GATE, bool STREAM, bool KEEP>
+__global__ __launch_bounds__(64 * W, sizeof(T) == 4 ? 1 : 4) void recurrence_forward_kernel(RecurrenceParams p) {
     constexpr int R = TOK / V, RS = SEQ ? R : 1;
     constexpr bool EXACT = sizeof(T) == 4;
-    __shared__ Joint<V> j;
+    __shared__ Joint<V, W> j;
+    const int waves = blockDim.x >> 6;
     Tile q = tile_of<V>(p);
     take_tile(p, q, &j.ticket);
     if (q.at >= p.ntile) return;             // only in a workspace that another call writes too
-    const int waves = blockDim.x >> 6;
     const int64_t w0 = ((int64_t)q.at * waves + q.wave) * TOK, t0 = w0 + q.group * R, rest = p.T - t0, row = q.b * p.T + t0;
     const bool full = w0 + TOK <= p.T;
     float P[R][V], H[R][V];          // map from the run's start to after each token
@@ -402,8 +412,8 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 4 ? 1 : 4) void recurrenc
 #pragma unroll
         for (int v = 0; v < V; ++v) end_p[v] = -1.f;
     }
-    store_f32<V>(&j.P[q.wave][q.group][q.slot], end_p);
-    store_f32<V>(&j.H[q.wave][q.group][q.slot], end_h);
+    store_f32<V>(&j.wave[q.wave].P[q.group][q.slot], end_p);
+    store_f32<V>(&j.wave[q.wave].H[q.group][q.slot], end_h);
     // a row of packed sequences begins with a fresh token, others with their initial state
     const float first = !SEQ && p.init ? p.init[q.b * p.D + q.own] : 0.f;
     join<V, SEQ, true>(p.chain, j, q, p.ntile, waves, first, [&](int run, float h) {
@@ -418,7 +428,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 4 ? 1 : 4) void recurrenc
         for (int k = 0; k < R; ++k) z[k] = load_pack<V>(token_at<T>(p.z, p.ldz, row, rest, full, k) + q.c0);
     }
     float h0[V];
-    load_f32<V>(&j.H[q.wave][q.group][q.slot], h0);
+    load_f32<V>(&j.wave[q.wave].H[q.group][q.slot], h0);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
         if (k >= rest) break;
@@ -441,12 +451,12 @@ template <typename T, int V, bool SEQ, bool GATE, bool STREAM>
 __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(RecurrenceParams p) {
     constexpr int TOK = kRunBack, R = TOK / V;
     constexpr bool EXACT = sizeof(T) == 4;
-    __shared__ Joint<V> j;
-    __shared__ float sums[kWaves][kBlock];
+    extern __shared__ __align__(16) float shared[];
+    Joint<V, kWaves>& j = *(Joint<V, kWaves>*)shared;          // as much of it as the waves need
+    const int waves = blockDim.x >> 6;
     Tile q = tile_of<V>(p);
     take_tile(p, q, &j.ticket);
     if (q.at >= p.ntile) return;             // only in a workspace that another call writes too
-    const int waves = blockDim.x >> 6;
     const unsigned tile = p.ntile - 1 - q.at;
     const int64_t piece = (int64_t)tile * waves + q.wave, w0 = piece * TOK, t0 = w0 + q.group * R, rest = p.T - t0;
     const int64_t row = q.b * p.T + t0;
@@ -511,25 +521,25 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
             for (int v = 0; v < V; ++v) end_p[v] = -1.f;
         }
     }
-    store_f32<V>(&j.P[q.wave][q.group][q.slot], end_p);
-    store_f32<V>(&j.H[q.wave][q.group][q.slot], end_h);
+    store_f32<V>(&j.wave[q.wave].P[q.group][q.slot], end_p);
+    store_f32<V>(&j.wave[q.wave].H[q.group][q.slot], end_h);
     __builtin_amdgcn_wave_barrier();
     {
         const int lane = threadIdx.x & 63;
         Map run[V];
 #pragma unroll
-        for (int k = 0; k < V; ++k) run[k] = {j.P[q.wave][k][lane], j.H[q.wave][k][lane]};
+        for (int k = 0; k < V; ++k) run[k] = {j.wave[q.wave].P[k][lane], j.wave[q.wave].H[k][lane]};
         if (!p.kept && waves > 1) {          // a single tile: from the waves before
             Map all{1.f, 0.f};
 #pragma unroll
             for (int k = 0; k < V; ++k) all = then<SEQ>(all, run[k]);
-            j.before[q.wave][lane] = all;
+            j.wave[q.wave].before[lane] = all;
             __syncthreads();
-            for (int k = 0; k < q.wave; ++k) h0 = apply<SEQ>(j.before[k][lane], h0);
+            for (int k = 0; k < q.wave; ++k) h0 = apply<SEQ>(j.wave[k].before[lane], h0);
         }
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            j.H[q.wave][k][lane] = h0;
+            j.wave[q.wave].H[k][lane] = h0;
             h0 = apply<SEQ>(run[k], h0);
         }
     }
@@ -538,7 +548,7 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
     for (int v = 0; v < V; ++v) end_p[v] = 1.f;
     if (q.active) {
         float h[V];
-        load_f32<V>(&j.H[q.wave][q.group][q.slot], h);
+        load_f32<V>(&j.wave[q.wave].H[q.group][q.slot], h);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             const bool last = SEQ ? (s.last >> k & 1) : k + 1 == rest;
@@ -586,15 +596,15 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
             for (int v = 0; v < V; ++v) end_p[v] = -1.f;
         }
     }
-    store_f32<V>(&j.P[q.wave][q.group][q.slot], end_p);
-    store_f32<V>(&j.H[q.wave][q.group][q.slot], end_h);
+    store_f32<V>(&j.wave[q.wave].P[q.group][q.slot], end_p);
+    store_f32<V>(&j.wave[q.wave].H[q.group][q.slot], end_h);
     join<V, SEQ, false>(p.chain, j, q, p.ntile, waves, 0.f, [](int, float) {});
     float dA[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) dA[v] = 0.f;
     if (q.active) {
         float e[V];
-        load_f32<V>(&j.H[q.wave][q.group][q.slot], e);
+        load_f32<V>(&j.wave[q.wave].H[q.group][q.slot], e);
 #pragma unroll
         for (int k = R - 1; k >= 0; --k) {
             if (k >= rest) continue;
@@ -625,18 +635,18 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
         }
     }
     // sums over the runs of each wave, then over the waves
-    store_f32<V>(&j.P[q.wave][q.group][q.slot], dA);
+    store_f32<V>(&j.wave[q.wave].P[q.group][q.slot], dA);
     __builtin_amdgcn_wave_barrier();
     const int lane = threadIdx.x & 63;
     float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < V; ++k) sum += j.P[q.wave][k][lane];
+    for (int k = 0; k < V; ++k) sum += j.wave[q.wave].P[k][lane];
     if (waves > 1) {
-        sums[q.wave][lane] = sum;
+        j.wave[q.wave].sums[lane] = sum;
         __syncthreads();
     }
     if (q.wave == 0 && q.here) {
-        for (int w = 1; w < waves; ++w) sum += sums[w][lane];
+        for (int w = 1; w < waves; ++w) sum += j.wave[w].sums[lane];
         p.part[(q.b * p.ntile + tile) * p.D + q.own] = sum;
     }
 }
@@ -674,9 +684,12 @@ static void launch_one(const RecurrenceParams& p, int waves, hipStream_t s) {
     const dim3 grid(p.nblk * (unsigned)p.batch * p.ntile), block(64 * waves);
     constexpr int TOK = V == 1 ? 16 : 32;
     if constexpr (PASS == kBackward)
-        hipLaunchKernelGGL((recurrence_backward_kernel<T, V, SEQ, GATE, STREAM>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((recurrence_backward_kernel<T, V, SEQ, GATE, STREAM>), grid, block,
+                           (Joint<V, kWaves>::bytes(waves)), s, p);
+    else if (waves <= kTileWaves)
+        hipLaunchKernelGGL((recurrence_forward_kernel<T, V, TOK, kTileWaves, SEQ, GATE, STREAM, PASS == kKeep>), grid, block, 0, s, p);
     else
-        hipLaunchKernelGGL((recurrence_forward_kernel<T, V, TOK, SEQ, GATE, STREAM, PASS == kKeep>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((recurrence_forward_kernel<T, V, TOK, kWaves, SEQ, GATE, STREAM, PASS == kKeep>), grid, block, 0, s, p);
 }
 template <Pass PASS, typename T, int V, bool STREAM> static void launch_seq(const RecurrenceParams& p, int waves, hipStream_t s) {
     if constexpr (PASS != kKeep) {
@@ -725,7 +738,7 @@ Shape shape_of(const ssd_recurrence_problem_t* p, bool back) {
     const bool narrow = p->channels < ssd::vector_of(ssd::kForward, p->dtype == SSD_DTYPE_BF16);
     const int64_t tokens = back || narrow ? ssd::kRunBack : 32;          // of a wave
     const int64_t runs = std::max<int64_t>(1, (p->seqlen + tokens - 1) / tokens);
-    s.waves = std::min<int64_t>(ssd::kWaves, runs);
+    s.waves = runs <= ssd::kWaves ? runs : ssd::kTileWaves;
     s.ntile = (runs + s.waves - 1) / s.waves;
     return s;
 }
