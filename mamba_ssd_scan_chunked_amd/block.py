@@ -243,10 +243,10 @@ def _head_rows(name, t, like):
 
 
 def _workspace(ws, nbytes, dev):
-    if ws is None and nbytes:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if ws is None:
+        return (torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes) if nbytes else (None, 0)
     _pkg._check_workspace(ws, nbytes, dev)
-    return ws, 0 if ws is None else ws.numel()
+    return ws, ws.numel()
 
 
 def _sequences(x, seq_idx, nseqs):

@@ -81,8 +81,11 @@ struct RecurrenceParams {
     int stream;
 };
 
-// A log2(e), kept finite so that a gate of 0 times it is 0.
-__device__ inline float rate_of(float a_log) { return -kLog2e * fminf(expf(a_log), 1e30f); }
+// A log2(e), kept finite so that a gate of 0 times it is 0 (NaN stays).
+__device__ inline float rate_of(float a_log) {
+    const float rate = expf(a_log);
+    return -kLog2e * (rate > 1e30f ? 1e30f : rate);
+}
 
 // sigmoid(v), and sigmoid(-v) to its own relative precision, from t = e^-|v|.  EXACT: the
 // exponent's rounding is made good, as in exp_small (beyond +-100 as at +-100, where t is 0; NaN

@@ -232,6 +232,32 @@ def test_bad_values_stay_in_their_sequence():
             assert torch.isfinite(got["dinit"].cpu()[[0, 2, 3, 4, 5]]).all()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_nan_is_not_lost(dt):
+    """A NaN in any input shows from its token on, and only in its channel."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("recurrence NaN %s" % dt)
+    for T in (1, 40, 700):
+        q = make(dt, 1, T, 24)
+        clean_y, clean_f = forward(ssd, q)
+        clean = backward(ssd, q)
+        t = T // 2
+        for name in ("x", "r", "i", "z", "A_log", "init"):
+            bad = dict(q, **{name: q[name].clone()})
+            bad[name][(0, t, 5) if name in "xriz" else (5 if name == "A_log" else (0, 5))] = float("nan")
+            y, f = forward(ssd, bad)
+            g = backward(ssd, bad)
+            others = torch.arange(24) != 5
+            assert torch.equal(y.cpu()[..., others], clean_y.cpu()[..., others]), name
+            assert torch.equal(f.cpu()[:, others], clean_f.cpu()[:, others]), name
+            for k in clean:
+                assert torch.equal(g[k].cpu()[..., others], clean[k].cpu()[..., others]), (name, k)
+            first = t if name in "xriz" else 0
+            assert torch.isnan(y.cpu()[0, first, 5]) and torch.equal(y.cpu()[0, :first], clean_y.cpu()[0, :first]), name
+            if name != "z":
+                assert torch.isnan(f.cpu()[0, 5]), name
+
+
 def test_absent_sequences_and_empty_rows():
     import mamba_ssd_scan_chunked_amd as ssd
     announce("recurrence absent sequences")
