@@ -491,7 +491,7 @@ typedef struct {
  *   workspace   >= ssd_recurrence_workspace_size(p) bytes, 256-byte aligned (NULL / 0 when 0)
  * The recurrence runs in fp32; 1 - a and 1 - a^2 are formed without cancellation.  An infinite
  * input or state makes its channel Inf or NaN from its token to the end of its sequence; nothing
- * crosses into another sequence.  Rows of more than 256 tokens take two launches, the first of
+ * crosses into another sequence.  Rows of many tokens (over 128) take two launches, the first of
  * which zeroes the workspace: it holds what workgroups of this call tell each other, so two calls
  * that run at the same time need one each.  Outputs must not overlap inputs, the workspace or each
  * other (SSD_ERR_ALIAS); the state is not carried in place. */

@@ -34,8 +34,8 @@
 // addresses (a branch for whole tiles) were slower, 77 -> 82 us; tiles of half the tokens 78 -> 91,
 // of twice as many 107; a workgroup that takes several tiles with the next one's loads in flight
 // 105 (200 registers); loads for the tile that would be next while the counter is asked 89.
-// Fp32: 4 x 2048 x 2560 73 us for 336 MB, gradients 178 (252 + 587 MB).
-// A row of up to 256 tokens forward, 128 backward, is one tile of up to eight waves: one launch,
+// Fp32: 4 x 2048 x 2560 72 us for 336 MB, gradients 178 (252 + 587 MB).
+// A row of up to 256 tokens (fp32 and backward 128) is one tile of up to eight waves: one launch,
 // no first pass (against two tiles that join through memory: 64 rows of 2560 channels,
 // gradients of 128 tokens 124 -> 100 us, 256 tokens forward 79 -> 75).  A longer one costs a
 // launch for the zeros and some us for the counter and the maps' way between dies: 2 rows of 650
@@ -685,7 +685,9 @@ enum Pass { kForward, kKeep, kBackward };
 template <Pass PASS, typename T, int V, bool SEQ, bool GATE, bool STREAM>
 static void launch_one(const RecurrenceParams& p, int waves, hipStream_t s) {
     const dim3 grid(p.nblk * (unsigned)p.batch * p.ntile), block(64 * waves);
-    constexpr int TOK = V == 1 ? 16 : 32;
+    // fp32 has half the vector instructions a byte to spare: shorter runs start sooner (2 x 16 tokens
+    // of 650 channels 6.6 -> 4.6 us, 2 x 777 13.3 -> 11.9, 4 x 2048 x 2560 73.9 -> 71.7)
+    constexpr int TOK = V == 1 || sizeof(T) == 4 ? 16 : 32;
     if constexpr (PASS == kBackward)
         hipLaunchKernelGGL((recurrence_backward_kernel<T, V, SEQ, GATE, STREAM>), grid, block,
                            (Joint<V, kWaves>::bytes(waves)), s, p);
@@ -739,7 +741,7 @@ Shape shape_of(const ssd_recurrence_problem_t* p, bool back) {
     Shape s;
     s.nblk = (p->channels + ssd::kBlock - 1) / ssd::kBlock;
     const bool narrow = p->channels < ssd::vector_of(ssd::kForward, p->dtype == SSD_DTYPE_BF16);
-    const int64_t tokens = back || narrow ? ssd::kRunBack : 32;          // of a wave
+    const int64_t tokens = back || narrow || p->dtype == SSD_DTYPE_F32 ? ssd::kRunBack : 32;          // of a wave
     const int64_t runs = std::max<int64_t>(1, (p->seqlen + tokens - 1) / tokens);
     s.waves = runs <= ssd::kWaves ? runs : ssd::kTileWaves;
     s.ntile = (runs + s.waves - 1) / s.waves;
