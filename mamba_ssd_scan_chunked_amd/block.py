@@ -560,7 +560,10 @@ def gated_recurrence(x, r, i, A_log, z=None, init_state=None, seq_idx=None, nseq
         p, args = _recurrence_arguments(x, r, i, A_log, z, init_state, seq_idx, nseqs)
         y = _output_like("y", y, x, dev)
         if final_state is not None or return_final:
-            final_state = _output("final_state", final_state, (p.nseqs, p.channels), torch.float32, dev)
+            if final_state is None and init_state is not None:
+                final_state = torch.empty_like(args[5])
+            else:
+                final_state = _output("final_state", final_state, (p.nseqs, p.channels), torch.float32, dev)
         ws, nbytes = _workspace(workspace, recurrence_workspace_size(p), dev)
         _check(_lib().ssd_recurrence_forward(ctypes.byref(p), *map(_ptr, args), _ptr(y), _ptr(final_state), _ptr(ws),
                                              nbytes, _current(dev)))
@@ -581,7 +584,7 @@ def gated_recurrence_backward(x, r, i, A_log, dy, z=None, init_state=None, dfina
         dfinal = _given("dfinal", dfinal, state, f32, dev)
         like = torch.empty_like
         out = {"dx": like(dy), "dr": like(dy), "di": like(dy), "dA_log": like(args[3]),
-               "dinit": torch.empty(state, dtype=f32, device=dev)}
+               "dinit": torch.empty(state, dtype=f32, device=dev) if init_state is None else like(args[5])}
         if z is not None:
             out["dz"] = like(dy)
         ws, nbytes = _workspace(workspace, recurrence_backward_workspace_size(p), dev)
