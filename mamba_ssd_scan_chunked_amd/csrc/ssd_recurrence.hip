@@ -2,9 +2,9 @@
 // C entries of include/ssd.h.
 //
 //   s = sigmoid(r),  L = A s,  a = e^L,  m = 1 - a,  beta = sqrt(1 - a^2) = sqrt(m (2 - m)),
-//   h_t = h_{t-1} - m h_{t-1} + beta sigmoid(i) x,      y = h  or  h silu(z).
+//   h_t = a h_{t-1} + beta sigmoid(i) x,      y = h  or  h silu(z).
 // Gradients, q_{t+1} being what token t + 1 sends back (or dfinal after a sequence's last token):
-//   g = dy [silu(z)] + q_{t+1},   q_t = g - m g,   dx = g beta sigmoid(i),
+//   g = dy [silu(z)] + q_{t+1},   q_t = a g,   dx = g beta sigmoid(i),
 //   M = g L (a h_{t-1} - sigmoid(i) x a^2 / beta),   dr = M (1 - s),   dA_log = sum of M.
 //
 // Memory-bound if the work is spread over the card and the inputs are read once.  There is one
@@ -110,18 +110,31 @@ template <bool EXACT> __device__ inline float gate_of(float v) {
     return __builtin_amdgcn_rcpf(1.f + exp_minus<false>(v));
 }
 
-// m = 1 - e^L for L <= 0, from K = L log2(e).  Near 0 the difference would cancel (and a long
-// memory is a matter of m, not of a): there m = -L (1 + L/2 + L^2/6 + ...), a polynomial fitted
-// to the definition on [-1/8, 0] by interpolation at Chebyshev points (relative error 1.6e-8),
-// its coefficients times ln(2)^k for K.
-__device__ inline float one_minus_exp2(float K) {
+// A decay a = e^L, L <= 0, from K = L log2(e), as one number k.  Near 1 a long memory is a matter
+// of m = 1 - a, and k is -m, its sign bit set also where m is 0: m = -L (1 + L/2 + L^2/6 + ...), a
+// polynomial fitted to the definition on [-1/8, 0] by interpolation at Chebyshev points (relative
+// error 1.6e-8), its coefficients times ln(2)^k for K.  Below, k is a itself: what it multiplies
+// (a state, a gradient on its way back, dr and dA_log) is then right relative to itself, where 1 - m
+// is a multiple of 2^-24, and 0 from L = -17.3 on.  near stays a mask of the wave: as a factor of
+// 1 or 0 it took registers (spills; 16384 x 1536 with a gate 66 us against 61.5).
+struct Decay {
+    float k;
+    bool near;
+};
+__device__ inline Decay decay_of(float K) {
     float q = fmaf(0.009151561185717583f, K, 0.05545208230614662f);
     q = fmaf(q, K, 0.24022464454174042f);
     q = fmaf(q, K, 0.6931471824645996f);
-    const float far = 1.f - __builtin_amdgcn_exp2f(K);
-    return K > -0.18f ? -K * q : far;
+    const bool near = K > -0.18f;
+    return {near ? K * q : __builtin_amdgcn_exp2f(K), near};
 }
-__device__ inline float beta_of(float m) { return __builtin_amdgcn_sqrtf(fmaf(-m, m, m + m)); }
+__device__ inline Decay decay_from(float k) { return {k, __float_as_int(k) < 0}; }
+constexpr Decay kKeepAll{-0.f, true};
+__device__ inline float beta_of(Decay a) { return __builtin_amdgcn_sqrtf(fmaf(-a.k, a.k, a.near ? -2.f * a.k : 1.f)); }
+// a v + u and a v.  Near 1 as v - m v, so that an error of 1's last place does not add up over a
+// long memory.
+__device__ inline float advance(float v, Decay a, float u) { return (a.near ? v : 0.f) + fmaf(a.k, v, u); }
+__device__ inline float decayed(float v, Decay a) { return fmaf(a.k, v, a.near ? v : 0.f); }
 
 // ------------------------------------------------------------------ maps h -> P h + H
 // P = -1 marks a map that begins a sequence anew: what comes before it does not matter, whatever
@@ -347,9 +360,6 @@ template <typename T, int V> __device__ inline void stay_packed(Pack<T, V>& p) {
     }
 }
 
-// A step of the state.
-__device__ inline float advance(float h, float m, float u) { return h + fmaf(-m, h, u); }
-
 // Whole rows.  TOK tokens per wave; KEEP: no output, but the state before every kRunBack-th token.
 // W: waves of a workgroup, at most (one kernel for both numbers was 3 % slower with tiles of four).
 template <typename T, int V, int TOK, int W, bool SEQ, bool GATE, bool STREAM, bool KEEP>
@@ -383,16 +393,17 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 4 ? 1 : 4) void recurrence_for
     }
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-        float m[V], u[V];
+        Decay a[V];
+        float u[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            m[v] = one_minus_exp2(A[v] * gate_of<EXACT>((float)r[k].v[v]));
-            u[v] = beta_of(m[v]) * (gate_of<EXACT>((float)g[k].v[v]) * (float)x[k].v[v]);
+            a[v] = decay_of(A[v] * gate_of<EXACT>((float)r[k].v[v]));
+            u[v] = beta_of(a[v]) * (gate_of<EXACT>((float)g[k].v[v]) * (float)x[k].v[v]);
         }
         if (!full) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (k >= rest) m[v] = u[v] = 0.f;
+                if (k >= rest) a[v] = kKeepAll, u[v] = 0.f;
         }
         const bool fresh = SEQ && (s.fresh >> k & 1);
         if (SEQ && fresh) {
@@ -406,8 +417,8 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 4 ? 1 : 4) void recurrence_for
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            end_h[v] = H[k][v] = advance(end_h[v], m[v], u[v]);
-            end_p[v] = P[k][v] = fmaf(-m[v], end_p[v], end_p[v]);
+            end_h[v] = H[k][v] = advance(end_h[v], a[v], u[v]);
+            end_p[v] = P[k][v] = decayed(end_p[v], a[v]);
         }
         __builtin_amdgcn_sched_barrier(0);       // token by token: the inputs' registers become free
     }
@@ -466,7 +477,7 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
     const bool full = w0 + TOK <= p.T;
     Runs<SEQ ? R : 1> s{};
     Pack<T, V> x[R], r[R], g[R], z[GATE ? R : 1];
-    float m[R][V], gy[R][V], A[V];
+    float a[R][V], gy[R][V], A[V];
     float hp[R][V];                  // what each token adds, then the state before it
     // the state before the first token of a sequence
     auto begin = [&](int k, float (&h)[V]) {
@@ -508,11 +519,12 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
             if (SEQ && (s.fresh >> k & 1)) begin(k, end_h);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                m[k][v] = one_minus_exp2(A[v] * gate_of<EXACT>((float)r[k].v[v]));
-                hp[k][v] = beta_of(m[k][v]) * (gate_of<EXACT>((float)g[k].v[v]) * (float)x[k].v[v]);
-                if (!full && k >= rest) m[k][v] = hp[k][v] = gy[k][v] = 0.f;
-                end_h[v] = advance(end_h[v], m[k][v], hp[k][v]);
-                end_p[v] = fmaf(-m[k][v], end_p[v], end_p[v]);
+                Decay d = decay_of(A[v] * gate_of<EXACT>((float)r[k].v[v]));
+                hp[k][v] = beta_of(d) * (gate_of<EXACT>((float)g[k].v[v]) * (float)x[k].v[v]);
+                if (!full && k >= rest) d = kKeepAll, hp[k][v] = gy[k][v] = 0.f;
+                a[k][v] = d.k;
+                end_h[v] = advance(end_h[v], d, hp[k][v]);
+                end_p[v] = decayed(end_p[v], d);
             }
             stay_packed(r[k]);
             stay_packed(g[k]);
@@ -547,8 +559,6 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
         }
     }
     __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int v = 0; v < V; ++v) end_p[v] = 1.f;
     if (q.active) {
         float h[V];
         load_f32<V>(&j.wave[q.wave].H[q.group][q.slot], h);
@@ -560,7 +570,7 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
             for (int v = 0; v < V; ++v) {
                 const float u = hp[k][v];
                 hp[k][v] = h[v];
-                h[v] = advance(h[v], m[k][v], u);
+                h[v] = advance(h[v], decay_from(a[k][v]), u);
             }
             if constexpr (GATE) {
                 float dz[V];
@@ -580,7 +590,7 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
             }
         }
     }
-    // backwards through the run, from nothing
+    // backwards through the run, from nothing; the product of its decays is in place
 #pragma unroll
     for (int v = 0; v < V; ++v) end_h[v] = 0.f;
     if (q.active) {
@@ -590,16 +600,10 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float e = gy[k][v] + end_h[v];
-                end_h[v] = fresh ? 0.f : fmaf(-m[k][v], e, e);
-                end_p[v] = fmaf(-m[k][v], end_p[v], end_p[v]);
+                end_h[v] = fresh ? 0.f : decayed(e, decay_from(a[k][v]));
             }
         }
-        if (SEQ && s.fresh) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) end_p[v] = -1.f;
-        }
     }
-    store_f32<V>(&j.wave[q.wave].P[q.group][q.slot], end_p);
     store_f32<V>(&j.wave[q.wave].H[q.group][q.slot], end_h);
     join<V, SEQ, false>(p.chain, j, q, p.ntile, waves, 0.f, [](int, float) {});
     float dA[V];
@@ -614,16 +618,17 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
             float dx[V], dr[V], di[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float d = gy[k][v] + e[v], mm = m[k][v], a = 1.f - mm;
+                const Decay ak = decay_from(a[k][v]);
+                const float d = gy[k][v] + e[v], decay = (ak.near ? 1.f : 0.f) + ak.k;
                 const Gate sr = gates_of<EXACT>((float)r[k].v[v]), si = gates_of<EXACT>((float)g[k].v[v]);
-                const float L = A[v] * sr.s * kLn2, beta = beta_of(mm), in = si.s * (float)x[k].v[v];
+                const float L = A[v] * sr.s * kLn2, beta = beta_of(ak), in = si.s * (float)x[k].v[v];
                 const float ratio = beta > 0.f ? L * __builtin_amdgcn_rcpf(beta) : 0.f;
-                const float M = d * (a * fmaf(L, hp[k][v], -in * a * ratio));
+                const float M = d * (decay * fmaf(L, hp[k][v], -in * decay * ratio));
                 dx[v] = d * beta * si.s;
                 di[v] = d * beta * in * si.n;
                 dr[v] = M * sr.n;
                 dA[v] += M;
-                e[v] = fmaf(-mm, d, d);
+                e[v] = decayed(d, ak);
             }
             store_f32<V, STREAM>(p.dx + (row + k) * p.D + q.c0, dx);
             store_f32<V, STREAM>(p.dr + (row + k) * p.D + q.c0, dr);
@@ -660,9 +665,9 @@ template <typename T> __global__ __launch_bounds__(256) void recurrence_step_ker
     if (n >= p.batch * p.D) return;
     const int64_t b = n / p.D, c = n % p.D;
     constexpr bool EXACT = sizeof(T) == 4;
-    const float m = one_minus_exp2(rate_of(p.A_log[c]) * gate_of<EXACT>((float)((const T*)p.r)[b * p.ldr + c]));
-    const float u = beta_of(m) * (gate_of<EXACT>((float)((const T*)p.i)[b * p.ldi + c]) * (float)((const T*)p.x)[b * p.ldx + c]);
-    const float h = advance(p.init[n], m, u);
+    const Decay a = decay_of(rate_of(p.A_log[c]) * gate_of<EXACT>((float)((const T*)p.r)[b * p.ldr + c]));
+    const float u = beta_of(a) * (gate_of<EXACT>((float)((const T*)p.i)[b * p.ldi + c]) * (float)((const T*)p.x)[b * p.ldx + c]);
+    const float h = advance(p.init[n], a, u);
     p.fin[n] = h;
     ((T*)p.y)[n] = (T)(p.z ? h * silu_for<T>((float)((const T*)p.z)[b * p.ldz + c]) : h);
 }
