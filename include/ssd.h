@@ -493,7 +493,8 @@ typedef struct {
  * input or state makes its channel Inf or NaN from its token to the end of its sequence; nothing
  * crosses into another sequence.  Rows of many tokens (over 128) take two launches, the first of
  * which zeroes the workspace: it holds what workgroups of this call tell each other, so two calls
- * that run at the same time need one each.  Outputs must not overlap inputs, the workspace or each
+ * that run at the same time need one each (in one workspace both still end, but their outputs are
+ * undefined: NaN, values of neither, or not written).  Outputs must not overlap inputs, the workspace or each
  * other (SSD_ERR_ALIAS); the state is not carried in place. */
 size_t ssd_recurrence_workspace_size(const ssd_recurrence_problem_t* p);
 int ssd_recurrence_forward(const ssd_recurrence_problem_t* p, const void* x, const void* r, const void* i,

@@ -48,6 +48,7 @@
 
 #include "block_common.hpp"
 #include "block_host.hpp"
+#include "ssd_recurrence_map.hpp"
 
 namespace ssd {
 
@@ -136,37 +137,13 @@ __device__ inline float beta_of(Decay a) { return __builtin_amdgcn_sqrtf(fmaf(-a
 __device__ inline float advance(float v, Decay a, float u) { return (a.near ? v : 0.f) + fmaf(a.k, v, u); }
 __device__ inline float decayed(float v, Decay a) { return fmaf(a.k, v, a.near ? v : 0.f); }
 
-// ------------------------------------------------------------------ maps h -> P h + H
-// P = -1 marks a map that begins a sequence anew: what comes before it does not matter, whatever
-// it is (a select, so that Inf and NaN stay in their sequence).
-struct Map {
-    float P, H;
-};
-template <bool SEQ> __device__ inline Map then(Map first, Map second) {
-    if (SEQ && second.P < 0.f) return second;
-    Map m;
-    m.H = fmaf(second.P, first.H, second.H);
-    m.P = SEQ && first.P < 0.f ? -1.f : first.P * second.P;
-    return m;
-}
-template <bool SEQ> __device__ inline float apply(Map m, float h) {
-    return SEQ && m.P < 0.f ? m.H : fmaf(m.P, h, m.H);
-}
-
-// A map as a word that is never 0 in its low half.
-__device__ inline uint64_t word_of(Map m) {
-    const uint32_t low = __float_as_uint(m.P) + 1u;
-    return (uint64_t)__float_as_uint(m.H) << 32 | (low ? low : 1u);
-}
-__device__ inline Map map_of(uint64_t w) {
-    return {__uint_as_float((uint32_t)w - 1u), __uint_as_float((uint32_t)(w >> 32))};
-}
+// ------------------------------------------------------------------ what tiles publish
 __device__ inline void publish(uint64_t* p, Map m) {
     __hip_atomic_store(p, word_of(m), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 // Up to N words `step` apart, each as soon as it is there.  The bound (about a second) is never
 // reached in a call by itself; it ends the waits of calls that were given one workspace at the
-// same time.  A word that did not come is 0: its map is NaN.
+// same time.  A word that did not come is 0.
 template <int N> __device__ inline void await(const uint64_t* p, int64_t step, int n, uint64_t (&w)[N]) {
 #pragma unroll
     for (int k = 0; k < N; ++k) w[k] = 0;
@@ -281,7 +258,7 @@ __device__ inline void join(const Chain& c, Joint<RUNS, W>& j, const Tile& q, un
         if (w == 0 && group > 0) {
             uint64_t word[1];
             await(c.states + ((int64_t)q.chain * ngroup + group - 1) * kBlock + lane, (int64_t)0, 1, word);
-            h = map_of(word[0]).H;
+            h = state_of(word[0]);
         }
         __syncthreads();
         if (w == 0) {
