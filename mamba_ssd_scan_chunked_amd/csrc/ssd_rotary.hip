@@ -75,27 +75,33 @@ template <int V, int L, int M, bool INTER> struct Unit {
             if (!real[m]) c[m][0] = c[m][1] = 0;
         }
     }
+    __device__ inline int pair(int m, int i) const {
+        return INTER ? (i < V / 2 ? c[m][0] / 2 + i : c[m][1] / 2 + i - V / 2) : c[m][0] + i;
+    }
+    __device__ inline bool turns(const RotaryParams& p, int m, int i) const {
+        return INTER ? 2 * pair(m, i) < p.R : turned[m];
+    }
     __device__ inline void turn(const RotaryParams& p, int64_t position) {
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int j = INTER ? (i < V / 2 ? c[m][0] / 2 + i : c[m][1] / 2 + i - V / 2) : c[m][0] + i;
-                cs[m][i] = 1.f;
-                sn[m][i] = 0.f;
-                if (turned[m] && 2 * j < p.R) turn_of(position, p.freqs[j], &cs[m][i], &sn[m][i]);
+                cs[m][i] = sn[m][i] = 0.f;
+                if (turns(p, m, i)) turn_of(position, p.freqs[pair(m, i)], &cs[m][i], &sn[m][i]);
             }
     }
-    // Pairs of unit m turned, by the angles or (BACK) against them.
-    template <bool BACK> __device__ inline void rotate(int m, float (&v)[2][V]) const {
+    // Pairs of unit m turned, by the angles or (BACK) against them.  The channels behind the rotated
+    // ones pass by a select: by a turn of angle 0, an infinite or NaN one would spoil its neighbour.
+    template <bool BACK> __device__ inline void rotate(const RotaryParams& p, int m, float (&v)[2][V]) const {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int h = V / 2 > 0 ? V / 2 : 1;
             float& a = INTER ? v[i / h][2 * (i % h)] : v[0][i];
             float& b = INTER ? v[i / h][2 * (i % h) + 1] : v[1][i];
-            const float s = BACK ? -sn[m][i] : sn[m][i], p = a, q = b;
-            a = fmaf(p, cs[m][i], -q * s);
-            b = fmaf(p, s, q * cs[m][i]);
+            const float s = BACK ? -sn[m][i] : sn[m][i], x = a, y = b;
+            const bool on = turns(p, m, i);
+            a = on ? fmaf(x, cs[m][i], -y * s) : x;
+            b = on ? fmaf(x, s, y * cs[m][i]) : y;
         }
     }
 };
@@ -155,7 +161,7 @@ template <typename T, int V, int L, int M, bool INTER, bool STREAM> __device__ i
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int i = 0; i < V; ++i) v[m][e][i] *= r * w[m][e][i];
-                    q.template rotate<false>(m, v[m]);
+                    q.template rotate<false>(p, m, v[m]);
                     if (q.real[m]) {
                         store_f32<V, STREAM>(out + q.c[m][0], v[m][0]);
                         store_f32<V, STREAM>(out + q.c[m][1], v[m][1]);
@@ -237,7 +243,7 @@ __device__ inline void rotary_backward(const RotaryParams& p, float (&sums)[4][2
                 if (head + 1 < hi[k]) fetch(k, head + 1, raw[k], grad[k]);
 #pragma unroll
                 for (int m = 0; m < M; ++m) {
-                    q.template rotate<true>(m, e[m]);
+                    q.template rotate<true>(p, m, e[m]);
 #pragma unroll
                     for (int f = 0; f < 2; ++f)
 #pragma unroll
