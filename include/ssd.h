@@ -489,7 +489,8 @@ typedef struct {
  *   final_state (nseqs, channels)           fp32 output, or NULL; rows of ids that do not occur
  *                                           are not written
  *   workspace   >= ssd_recurrence_workspace_size(p) bytes, 256-byte aligned (NULL / 0 when 0)
- * The recurrence runs in fp32; 1 - a and 1 - a^2 are formed without cancellation.  An infinite
+ * The recurrence runs in fp32; 1 - a and 1 - a^2 are formed without cancellation, a small a keeps
+ * its own relative precision.  A_log counts as at most 88, and a sigma below 2^-126 as 0.  An infinite
  * input or state makes its channel Inf or NaN from its token to the end of its sequence; nothing
  * crosses into another sequence.  Rows of many tokens (over 128) take two launches, the first of
  * which zeroes the workspace: it holds what workgroups of this call tell each other, so two calls

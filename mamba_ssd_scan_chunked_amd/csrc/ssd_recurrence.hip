@@ -82,11 +82,9 @@ struct RecurrenceParams {
     int stream;
 };
 
-// A log2(e), kept finite so that a gate of 0 times it is 0 (NaN stays).
-__device__ inline float rate_of(float a_log) {
-    const float rate = expf(a_log);
-    return -kLog2e * (rate > 1e30f ? 1e30f : rate);
-}
+// A log2(e), kept finite so that a gate of 0 times it is 0 (NaN stays): e^88 log2(e) is 0.7 of fp32's
+// largest, so every product with a gate that is not 0 is right, however nearly closed.
+__device__ inline float rate_of(float a_log) { return -kLog2e * expf(a_log > 88.f ? 88.f : a_log); }
 
 // sigmoid(v), and sigmoid(-v) to its own relative precision, from t = e^-|v|.  EXACT: the
 // exponent's rounding is made good, as in exp_small (beyond +-100 as at +-100, where t is 0; NaN
@@ -598,9 +596,10 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
                 const Decay ak = decay_from(a[k][v]);
                 const float d = gy[k][v] + e[v], decay = (ak.near ? 1.f : 0.f) + ak.k;
                 const Gate sr = gates_of<EXACT>((float)r[k].v[v]), si = gates_of<EXACT>((float)g[k].v[v]);
-                const float L = A[v] * sr.s * kLn2, beta = beta_of(ak), in = si.s * (float)x[k].v[v];
-                const float ratio = beta > 0.f ? L * __builtin_amdgcn_rcpf(beta) : 0.f;
-                const float M = d * (decay * fmaf(L, hp[k][v], -in * decay * ratio));
+                // a L first: L alone times a state can leave fp32, and a be 0
+                const float aL = decay * (A[v] * sr.s * kLn2), beta = beta_of(ak), in = si.s * (float)x[k].v[v];
+                const float ratio = beta > 0.f ? aL * __builtin_amdgcn_rcpf(beta) : 0.f;
+                const float M = d * fmaf(aL, hp[k][v], -in * decay * ratio);
                 dx[v] = d * beta * si.s;
                 di[v] = d * beta * in * si.n;
                 dr[v] = M * sr.n;

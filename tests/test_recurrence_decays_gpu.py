@@ -51,7 +51,8 @@ def reference(q):
     ea = U32 * torch.where(L > -1, n_m * m + 4, a * (n_m * L.abs() + 4)) + FLUSH
     s, si = torch.sigmoid(r), torch.sigmoid(i)
     v = si * x
-    tiny = torch.where(r < -80, rr.lost_beta(A_log), 0.0)              # a gate that may count as 0
+    may_shut = (r < -80) & (s > 0)                                    # a gate that may count as 0
+    tiny = torch.where(may_shut, rr.lost_beta(A_log), 0.0)
     lost = FLUSH * x.abs() + tiny * v.abs()
     n_u = rr.N_U + nr / 2 + ni
     zero = torch.zeros_like(x)
@@ -84,7 +85,7 @@ def reference(q):
     M = g * (L * a * before - v * a * a * ratio)
     size = L.abs() * a * Hb + v.abs() * a * a * ratio.abs()
     M_e = EG * size + G * (U32 * (40 + 2 * nr + ni) * size + L.abs() * (a * Eb + ea * Hb) + v.abs() * ratio.abs() * 2 * a * ea)
-    M_e = M_e + G * (tiny * v.abs() + FLUSH * (torch.where(r < -80, torch.exp(A_log), 1.0) * Hb + x.abs()))
+    M_e = M_e + G * (tiny * v.abs() + FLUSH * (torch.where(may_shut, torch.exp(A_log), 1.0) * Hb + x.abs()))
     out["dr"] = (M * (1 - s), (M_e + U32 * (12 + nr) * M.abs()) * (1 - s) + FLUSH * M.abs())
     out["dA_log"] = (M.sum((0, 1)), M_e.sum((0, 1)) + (b * T + 20) * U32 * M.abs().sum((0, 1)))
     return out
@@ -119,3 +120,33 @@ def test_fast_decays(dt, size, shift):
     announce("recurrence fast decays %s %s %s" % (dt, size, shift))
     rates = [math.log(v) for v in (1, 2, 4, 6, 8, 10, 12, 14, 16, 20, 24, 28, 32, 40, 60, 80, 100, 0.1, 0.01)]
     check(ssd, make(dt, size[0], size[1], rates, shift, 1.0, size[2]))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("size", SIZES, ids=SIZE_IDS)
+def test_large_rates_with_nearly_closed_gates(dt, size):
+    """A_log from 60 to 76 where A sigmoid(r) is around 1: neither factor is near it."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("recurrence large rates %s %s" % (dt, size))
+    rates = [60.0 + k for k in range(17)]
+    q = make(dt, size[0], size[1], rates, 0.0, 1.0, size[2])
+    q["r"] = (q["r"].float() - q["A_log"]).to(q["r"].dtype)
+    check(ssd, q)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_largest_rates(dt):
+    """A_log counts as at most 88: beyond it an open gate forgets everything, a closed one nothing."""
+    import mamba_ssd_scan_chunked_amd as ssd
+    announce("recurrence largest rates %s" % dt)
+    q = make(dt, 1, 40, [70.0, 88.0, 88.5, 100.0, 1e30, math.inf], 2.0, 1.0)
+    q["r"][:, 20:] = -math.inf
+    q["init"], q["x"] = q["init"] * 1000, q["x"] * 256               # times the rate alone past fp32's range
+    capped = dict(q, A_log=q["A_log"].clamp(max=88))
+    check(ssd, capped)
+    d = {k: v.cuda() if torch.is_tensor(v) else v for k, v in q.items()}
+    both = [ssd.gated_recurrence(d["x"], d["r"], d["i"], A, None, d["init"]) for A in (d["A_log"], capped["A_log"].cuda())]
+    assert torch.equal(both[0][0], both[1][0]) and torch.equal(both[0][1], both[1][1])
+    both = [ssd.gated_recurrence_backward(d["x"], d["r"], d["i"], A, d["dy"], init_state=d["init"], dfinal=d["dfinal"])
+            for A in (d["A_log"], capped["A_log"].cuda())]
+    assert all(torch.equal(both[0][k], both[1][k]) and torch.isfinite(both[0][k]).all() for k in both[0])
