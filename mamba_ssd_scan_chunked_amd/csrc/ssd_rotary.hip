@@ -300,8 +300,10 @@ template <typename T, int V, int L, int M, bool INTER> __global__ __launch_bound
 // l + 64, ... and the channels behind them, read again where they are needed again.
 template <typename T, bool BACK> __global__ __launch_bounds__(64) void rotary_any_kernel(RotaryParams p) {
     const int lane = threadIdx.x, all = p.heads[0] + p.heads[1];
-    if constexpr (BACK)
+    if constexpr (BACK) {
         for (int c = lane; c < p.N; c += 64) p.part[0][blockIdx.x * p.part_stride + c] = p.part[1][blockIdx.x * p.part_stride + c] = 0.f;
+        __syncthreads();             // a channel's sum is another lane's from here on
+    }
     for (int64_t unit = blockIdx.x; unit < p.tokens * all; unit += gridDim.x) {
         const int64_t t = unit / all;
         int head = (int)(unit % all);
