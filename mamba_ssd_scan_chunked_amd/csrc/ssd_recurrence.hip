@@ -26,20 +26,20 @@
 // what a run sends back.
 //
 // Measured on an MI355X (a device copy moves 5.1 TB/s), bf16, a call: 4 x 4096 tokens of 2560
-// channels 69 us for 336 MB, vector units at work for 74 %; 16384 tokens of 1536 with a gate 59 us
-// for 252 MB (58 %); gradients of 4 x 4096 x 2560, packed, 273 us: the first pass 72 (252 MB read),
-// the second 195 for 925 MB (74 %), sums and zeros 9; of 8 x 2048 x 1536 with a gate 176 (40 and
-// 130 for 705 MB).  So both bounds are near: about 43 vector instructions an element forward (six
-// of them transcendental) and 120 backward, a third of them the joins'.  Fewer instructions for
+// channels 71 us for 336 MB, vector units at work for 76 %; 16384 tokens of 1536 with a gate 60 us
+// for 252 MB (60 %); gradients of 4 x 4096 x 2560, packed, 273 us: the first pass 73 (252 MB read),
+// the second 195 for 925 MB (79 %), sums and zeros 9; of 8 x 2048 x 1536 with a gate 177 (41 and
+// 128 for 705 MB).  So both bounds are near: about 45 vector instructions an element forward (six
+// of them transcendental) and 130 backward, a third of them the joins'.  Fewer instructions for
 // addresses (a branch for whole tiles) were slower, 77 -> 82 us; tiles of half the tokens 78 -> 91,
 // of twice as many 107; a workgroup that takes several tiles with the next one's loads in flight
 // 105 (200 registers); loads for the tile that would be next while the counter is asked 89.
-// Fp32: 4 x 2048 x 2560 72 us for 336 MB, gradients 178 (252 + 587 MB).
+// Fp32: 4 x 2048 x 2560 70 us for 336 MB, gradients 175 (252 + 587 MB).
 // A row of up to 256 tokens (fp32 and backward 128) is one tile of up to eight waves: one launch,
 // no first pass (against two tiles that join through memory: 64 rows of 2560 channels,
 // gradients of 128 tokens 124 -> 100 us, 256 tokens forward 79 -> 75).  A longer one costs a
 // launch for the zeros and some us for the counter and the maps' way between dies: 2 rows of 650
-// channels on the GPU 5.7 us for 128 tokens, 8.0 for 256, 11 for 777; gradients 12 for 128, 25 for
+// channels on the GPU 6.3 us for 128 tokens, 8.8 for 256, 11 for 777; gradients 12 for 128, 23 for
 // 256, 27 for 777.
 #include "ssd.h"
 
@@ -112,7 +112,7 @@ template <bool EXACT> __device__ inline float gate_of(float v) {
 // A decay a = e^L, L <= 0, from K = L log2(e), as one number k.  Near 1 a long memory is a matter
 // of m = 1 - a, and k is -m, its sign bit set also where m is 0: m = -L (1 + L/2 + L^2/6 + ...), a
 // polynomial fitted to the definition on [-1/8, 0] by interpolation at Chebyshev points (relative
-// error 1.6e-8), its coefficients times ln(2)^k for K.  Below, k is a itself: what it multiplies
+// error 3.4e-8 with its rounded coefficients), these times ln(2)^k for K.  Below, k is a itself: what it multiplies
 // (a state, a gradient on its way back, dr and dA_log) is then right relative to itself, where 1 - m
 // is a multiple of 2^-24, and 0 from L = -17.3 on.  near stays a mask of the wave: as a factor of
 // 1 or 0 it took registers (spills; 16384 x 1536 with a gate 66 us against 61.5).
@@ -635,7 +635,8 @@ __global__ __launch_bounds__(64 * kWaves) void recurrence_backward_kernel(Recurr
     }
 }
 
-// One token: a thread per (row, channel).
+// One token: a thread per (row, channel).  On the GPU 64 x 2560 with a gate 3.2 us (bf16) and 3.5
+// (fp32): a launch; 256 x 5120 7.7 and 8.5 for 24 and 37 MB.
 template <typename T> __global__ __launch_bounds__(256) void recurrence_step_kernel(RecurrenceParams p) {
     const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (n >= p.batch * p.D) return;

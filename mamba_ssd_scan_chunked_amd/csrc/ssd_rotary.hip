@@ -10,10 +10,11 @@
 // that a pair is in one lane and all lanes' packs together are whole lines.  A team walks the
 // heads of its token, B's and then C's, with the next head's loads in flight: the token's cosines
 // and sines (fp64 angles) are formed once for all of them.  Measured on an MI355X (a device copy
-// moves 5.1 TB/s), bf16: 8192 tokens of 8 + 32 heads of 128 27.7 us for 168 MB; 16384 tokens of one
-// head each 7.5 us on the GPU for 17 MB (one round of waves: latency), 12.4 with the binding;
-// gradients of 16384 tokens of 8 + 8 heads 69 us for 336 MB; one decoded token for four rows 3.1 us
-// on the GPU, 12 a call.  Gradients take packs of four channels, so that a store instruction's
+// moves 5.1 TB/s), bf16: 8192 tokens of 8 + 32 heads of 128 27.9 us for 168 MB; 16384 tokens of one
+// head each 7.0 us on the GPU for 17 MB (one round of waves: latency), 12.5 with the binding;
+// gradients of 16384 tokens of 8 + 8 heads 66 us for 336 MB; one decoded token for four rows 3.0 us
+// on the GPU, 12 a call.  Fp32: 16384 tokens of one head each 9.6 us on the GPU for 34 MB, 4096 of 8 +
+// 32 heads 32 us for 168 MB, gradients of 8192 tokens of 8 + 8 heads 42 us for 201 MB.  Gradients take packs of four channels, so that a store instruction's
 // 16-byte pieces of fp32 lie side by side.
 #include "ssd.h"
 
@@ -297,7 +298,9 @@ template <typename T, int V, int L, int M, bool INTER> __global__ __launch_bound
 }
 
 // Heads that no vectors fit (see vector_of): a wave per (token, head), lane l with pairs l,
-// l + 64, ... and the channels behind them, read again where they are needed again.
+// l + 64, ... and the channels behind them, read again where they are needed again.  16384 tokens
+// of two heads of 99: 16 us on the GPU, gradients 113 (13 and 32 MB, bf16): latency, one head at a time,
+// and sums in memory.
 template <typename T, bool BACK> __global__ __launch_bounds__(64) void rotary_any_kernel(RotaryParams p) {
     const int lane = threadIdx.x, all = p.heads[0] + p.heads[1];
     if constexpr (BACK) {
@@ -403,7 +406,11 @@ static RotaryShape shape_of(int64_t tokens, int64_t heads, int64_t N, int64_t R,
     // the chip and walk: few tokens' heads are spread over them once, many tokens' into 16384 items
     // or more, so that no wave walks much longer than another (16384 tokens of 16 heads of 128, bf16:
     // 4096 items 84 us, 8192 77, 16384 71, 32768 73; 2331 tokens of 9 heads of 80, fp32: 2915 items
-    // 12.8, 5247 14.2).
+    // 12.8, 5247 14.2).  On the GPU around the border, spread over the waves once against 16384 items:
+    // 16 heads of 128, bf16, 4000 tokens 22.8 and 24.5 us, 4200 23.1 and 23.7, 8192 43.3 and 41.2, 16384
+    // 78.5 and 67.1; 9 heads of 80, fp32, 4200 tokens 14.7 and 16.7, 8192 19.3 and 21.3; two heads of
+    // 128, 8000 tokens 13.1 and 13.3, 8400 12.3 and 13.6, 16384 16.2 and 16.8.  So for few heads the
+    // border lies low, by 2 us at most.
     const int64_t wanted = !back ? 8192 : (teams > kWalkers / 3 ? 16384 : kWalkers);
     const int64_t n = std::max<int64_t>(1, std::min(heads, wanted / std::max<int64_t>(1, teams)));
     s.chunk = (heads + n - 1) / n;
