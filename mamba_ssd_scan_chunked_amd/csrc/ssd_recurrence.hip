@@ -112,10 +112,10 @@ template <bool EXACT> __device__ inline float gate_of(float v) {
 // A decay a = e^L, L <= 0, from K = L log2(e), as one number k.  Near 1 a long memory is a matter
 // of m = 1 - a, and k is -m, its sign bit set also where m is 0: m = -L (1 + L/2 + L^2/6 + ...), a
 // polynomial fitted to the definition on [-1/8, 0] by interpolation at Chebyshev points (relative
-// error 3.4e-8 with its rounded coefficients), these times ln(2)^k for K.  Below, k is a itself: what it multiplies
-// (a state, a gradient on its way back, dr and dA_log) is then right relative to itself, where 1 - m
-// is a multiple of 2^-24, and 0 from L = -17.3 on.  near stays a mask of the wave: as a factor of
-// 1 or 0 it took registers (spills; 16384 x 1536 with a gate 66 us against 61.5).
+// error 3.4e-8 with its rounded coefficients), these times ln(2)^k for K.  Below, k is a itself:
+// what it multiplies (a state, a gradient on its way back, dr and dA_log) is then right relative to
+// itself, where 1 - m is a multiple of 2^-24, and 0 from L = -17.3 on.  near stays a mask of the
+// wave: as a factor of 1 or 0 it took registers (spills; 16384 x 1536 with a gate 66 us against 61.5).
 struct Decay {
     float k;
     bool near;

@@ -14,8 +14,8 @@
 // head each 7.0 us on the GPU for 17 MB (one round of waves: latency), 12.5 with the binding;
 // gradients of 16384 tokens of 8 + 8 heads 66 us for 336 MB; one decoded token for four rows 3.0 us
 // on the GPU, 12 a call.  Fp32: 16384 tokens of one head each 9.6 us on the GPU for 34 MB, 4096 of 8 +
-// 32 heads 32 us for 168 MB, gradients of 8192 tokens of 8 + 8 heads 42 us for 201 MB.  Gradients take packs of four channels, so that a store instruction's
-// 16-byte pieces of fp32 lie side by side.
+// 32 heads 32 us for 168 MB, gradients of 8192 tokens of 8 + 8 heads 42 us for 201 MB.  Gradients take
+// packs of four channels, so that a store instruction's 16-byte pieces of fp32 lie side by side.
 #include "ssd.h"
 
 #include <algorithm>
