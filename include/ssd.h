@@ -491,13 +491,14 @@ typedef struct {
  *   workspace   >= ssd_recurrence_workspace_size(p) bytes, 256-byte aligned (NULL / 0 when 0)
  * The recurrence runs in fp32; 1 - a and 1 - a^2 are formed without cancellation, a small a keeps
  * its own relative precision.  A_log counts as at most 88, sigma or A sigma(r) below 2^-126 as 0.
- * An infinite input or state makes its channel Inf or NaN from its token to the end of its sequence; nothing
- * crosses into another sequence.  Rows of more tokens than a workgroup holds (where the workspace
- * size is not 0: over 256 tokens in bf16, over 128 in fp32 and in rows of fewer than eight channels)
- * take two launches, the first of which zeroes the workspace: it holds what workgroups of this call
- * tell each other, so two calls that run at the same time need one each (in one workspace both still
- * end, but their outputs are undefined: NaN, values of neither, or not written).  Outputs must not overlap inputs, the workspace or each
- * other (SSD_ERR_ALIAS); the state is not carried in place. */
+ * An infinite input or state makes its channel Inf or NaN from its token to the end of its
+ * sequence; nothing crosses into another sequence.  Rows of more tokens than a workgroup holds
+ * (where the workspace size is not 0: over 256 tokens in bf16, over 128 in fp32 and in rows of fewer
+ * than eight channels) take two launches, the first of which zeroes the workspace: it holds what
+ * workgroups of this call tell each other, so two calls that run at the same time need one each (in
+ * one workspace both still end, but their outputs are undefined: NaN, values of neither, or not
+ * written).  Outputs must not overlap inputs, the workspace or each other (SSD_ERR_ALIAS); the state
+ * is not carried in place. */
 size_t ssd_recurrence_workspace_size(const ssd_recurrence_problem_t* p);
 int ssd_recurrence_forward(const ssd_recurrence_problem_t* p, const void* x, const void* r, const void* i,
                            const float* A_log, const void* z, const float* init_state, const int32_t* seq_idx, void* y,
